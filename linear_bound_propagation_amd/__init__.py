@@ -19,6 +19,10 @@ from typing import List, Optional, Sequence
 import numpy as np
 import torch
 
+from . import train as _train
+from .train import (clip_grad_norm, clip_grad_norm_workspace, cross_entropy, cross_entropy_workspace,  # noqa: F401
+                    linear, linear_backward, linear_workspace)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvbprop.so")
 
@@ -35,7 +39,8 @@ _OPS = {"input": VB_INPUT, "linear": VB_LINEAR, "conv": VB_CONV2D, "relu": VB_RE
 EXPORTS = ["vb_last_error", "vb_workspace_size", "vb_ibp", "vb_crown_backward", "vb_concretize",
            "vb_alpha_layout", "vb_alpha_init", "vb_alpha_step", "vb_alpha_step_rows", "vb_apply_splits",
            "vb_bab_workspace_size", "vb_bab", "vb_crown", "vb_crown_noalloc", "vb_verify",
-           "vb_profile_start", "vb_profile_stop", "vb_profile_record", "vb_pack_linear_bytes", "vb_pack_linear"]
+           "vb_profile_start", "vb_profile_stop", "vb_profile_record", "vb_pack_linear_bytes", "vb_pack_linear"] \
+    + _train.EXPORTS
 # host-only helpers declared in include/vb_testing.h (used by the CPU tests)
 TESTING_EXPORTS = ["vb_testing_fastdiv", "vb_testing_conv_tile_n", "vb_testing_identity_path"]
 
@@ -122,6 +127,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.vb_profile_record.restype = i32
     lib.vb_profile_record.argtypes = [ctypes.c_int64, ctypes.POINTER(ctypes.c_double),
                                       ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i32)]
+    _train.declare(lib)
     return lib
 
 

@@ -22,6 +22,7 @@
 
 #include "vb.h"
 #include "vb_internal.h"
+#include "vb_train_internal.h"
 
 using namespace vb;
 
@@ -2224,6 +2225,16 @@ vb_status check_domain(const float* xc) {
 // C ABI
 
 extern "C" const char* vb_last_error(void) { return g_err.c_str(); }
+
+// For the calls of vb_train.cpp, whose errors vb_last_error describes too.
+vb_status vb::set_error(vb_status s, const char* msg) noexcept {
+  try {
+    g_err = msg;
+  } catch (...) {
+    g_err.clear();
+  }
+  return s;
+}
 
 // Ints kept after the weight copies by unstable-only rows: per input a neuron
 // ranking and a neuron list over the widest node, and a count.

@@ -1,0 +1,261 @@
+// C ABI of the training operators (include/vb_train.h): argument checks and the
+// sequence of launches.  Nothing here throws.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "vb_train.h"
+#include "vb_train_internal.h"
+
+using namespace vb;
+
+namespace {
+
+vb_status fail(vb_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return set_error(s, buf);
+}
+
+#define HIPCHK(expr)                                                                        \
+  do {                                                                                      \
+    hipError_t e_ = (expr);                                                                 \
+    if (e_ != hipSuccess) return fail(VB_EDEVICE, "%s: %s", #expr, hipGetErrorString(e_)); \
+  } while (0)
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Rows and leading dimensions are bounded so that byte offsets within a matrix
+// fit 62 bits and row counts fit a grid dimension.
+constexpr int64_t MAX_ROWS = 0x7fffffff, MAX_LD = INT64_C(1) << 30;
+
+vb_status check_sizes(const char* fn, int64_t rows, int32_t n_in, int32_t n_out, int32_t dtype) {
+  if (rows < 0 || rows > MAX_ROWS) return fail(VB_EINVAL, "%s: rows must be in [0, 2^31) (got %lld)", fn, (long long)rows);
+  if (n_in <= 0 || n_out <= 0) return fail(VB_EINVAL, "%s: sizes must be positive (got %d, %d)", fn, n_in, n_out);
+  if (dtype < VB_F32 || dtype > VB_F16) return fail(VB_EINVAL, "%s: unknown dtype %d", fn, dtype);
+  return VB_OK;
+}
+
+vb_status check_matrix(const char* fn, const char* name, const void* p, int64_t ld, int64_t n, int dtype, bool required) {
+  if (!p) return required ? fail(VB_EINVAL, "%s: %s is NULL", fn, name) : VB_OK;
+  if ((uintptr_t)p % elem_size(dtype)) return fail(VB_EINVAL, "%s: %s is not aligned to its elements", fn, name);
+  if (ld < n || ld > MAX_LD)
+    return fail(VB_ESHAPE, "%s: leading dimension of %s must be in [%lld, 2^30] (got %lld)", fn, name, (long long)n, (long long)ld);
+  return VB_OK;
+}
+
+vb_status check_ws(const char* fn, const void* ws, size_t ws_bytes, size_t need) {
+  if (!need) return VB_OK;
+  if (!ws || ws_bytes < need)
+    return fail(VB_ENOMEM, "%s: workspace too small (%zu bytes, needs %zu)", fn, ws ? ws_bytes : (size_t)0, need);
+  if ((uintptr_t)ws & 15) return fail(VB_EINVAL, "%s: workspace is not 16-byte aligned", fn);
+  return VB_OK;
+}
+
+#define TRY(expr)                   \
+  do {                              \
+    if (vb_status s_ = (expr)) return s_; \
+  } while (0)
+
+}  // namespace
+
+extern "C" vb_status vb_linear_workspace(int64_t rows, int32_t n_in, int32_t n_out, int32_t dtype, int32_t backward,
+                                         size_t* bytes) {
+  if (!bytes) return fail(VB_EINVAL, "vb_linear_workspace: bytes is NULL");
+  TRY(check_sizes("vb_linear_workspace", rows, n_in, n_out, dtype));
+  *bytes = backward ? align_up((size_t)rows * n_out * elem_size(dtype)) : 0;
+  return VB_OK;
+}
+
+extern "C" vb_status vb_linear_forward(const vb_linear_fwd* p, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "vb_linear_forward";
+  if (!p) return fail(VB_EINVAL, "%s: NULL argument", fn);
+  TRY(check_sizes(fn, p->rows, p->n_in, p->n_out, p->dtype));
+  if (p->act < VB_ACT_NONE || p->act > VB_ACT_SILU) return fail(VB_EINVAL, "%s: unknown activation %d", fn, p->act);
+  if (p->rows == 0) return VB_OK;
+  TRY(check_matrix(fn, "x", p->x, p->ld_x, p->n_in, p->dtype, true));
+  TRY(check_matrix(fn, "weight", p->weight, p->ld_w, p->n_in, p->dtype, true));
+  TRY(check_matrix(fn, "bias", p->bias, p->n_out, p->n_out, p->dtype, false));
+  TRY(check_matrix(fn, "residual", p->residual, p->ld_res, p->n_out, p->dtype, false));
+  TRY(check_matrix(fn, "y", p->y, p->ld_y, p->n_out, p->dtype, true));
+  TRY(check_matrix(fn, "pre", p->pre, p->ld_pre, p->n_out, p->dtype, false));
+  if (p->residual == p->y && p->ld_res != p->ld_y) return fail(VB_ESHAPE, "%s: y over residual needs the same leading dimension", fn);
+  size_t need = 0;
+  TRY(vb_linear_workspace(p->rows, p->n_in, p->n_out, p->dtype, 0, &need));
+  TRY(check_ws(fn, ws, ws_bytes, need));
+  Product d{};
+  d.a = p->x, d.sam = p->ld_x, d.sak = 1;
+  d.b = p->weight, d.sbn = p->ld_w, d.sbk = 1;
+  d.M = p->rows, d.N = p->n_out, d.K = p->n_in;
+  d.bias = p->bias, d.res = p->residual, d.ld_res = p->ld_res;
+  d.out = p->y, d.ld_out = p->ld_y, d.pre = p->pre, d.ld_pre = p->ld_pre, d.act = p->act;
+  HIPCHK(launch_product(d, p->dtype, (hipStream_t)stream));
+  return VB_OK;
+}
+
+extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "vb_linear_backward";
+  if (!p) return fail(VB_EINVAL, "%s: NULL argument", fn);
+  TRY(check_sizes(fn, p->rows, p->n_in, p->n_out, p->dtype));
+  if (p->act < VB_ACT_NONE || p->act > VB_ACT_SILU) return fail(VB_EINVAL, "%s: unknown activation %d", fn, p->act);
+  const bool some = p->rows > 0;
+  TRY(check_matrix(fn, "dy", p->dy, p->ld_dy, p->n_out, p->dtype, some));
+  TRY(check_matrix(fn, "x", p->x, p->ld_x, p->n_in, p->dtype, some && p->dweight));
+  TRY(check_matrix(fn, "weight", p->weight, p->ld_w, p->n_in, p->dtype, some && p->dx));
+  TRY(check_matrix(fn, "saved", p->saved, p->ld_saved, p->n_out, p->dtype, some && p->act != VB_ACT_NONE));
+  TRY(check_matrix(fn, "dx", p->dx, p->ld_dx, p->n_in, p->dtype, false));
+  TRY(check_matrix(fn, "dweight", p->dweight, p->ld_dw, p->n_in, p->dtype, false));
+  TRY(check_matrix(fn, "dbias", p->dbias, p->n_out, p->n_out, p->dtype, false));
+  TRY(check_matrix(fn, "dresidual", p->dresidual, p->ld_dres, p->n_out, p->dtype, false));
+  if (!p->dx && !p->dweight && !p->dbias && !p->dresidual) return fail(VB_EINVAL, "%s: nothing to compute", fn);
+  if (p->dresidual == p->dy && p->dy && p->ld_dres != p->ld_dy)
+    return fail(VB_ESHAPE, "%s: dresidual over dy needs the same leading dimension", fn);
+  const hipStream_t st = (hipStream_t)stream;
+  const size_t es = elem_size(p->dtype);
+  if (!some) {
+    if (p->dweight) HIPCHK(launch_fill_zero(p->dweight, p->n_out, p->n_in * (long long)es, p->ld_dw * es, st));
+    if (p->dbias) HIPCHK(launch_fill_zero(p->dbias, 1, p->n_out * (long long)es, p->n_out * (long long)es, st));
+    return VB_OK;
+  }
+  size_t need = 0;
+  TRY(vb_linear_workspace(p->rows, p->n_in, p->n_out, p->dtype, 1, &need));
+  TRY(check_ws(fn, ws, ws_bytes, need));
+  const bool products = p->dx || p->dweight;
+  const bool own_g = products && p->act != VB_ACT_NONE;
+  if (own_g || p->dbias || p->dresidual) {
+    ActGrad g{};
+    g.dy = p->dy, g.ld_dy = p->ld_dy;
+    g.saved = p->act == VB_ACT_NONE ? nullptr : p->saved, g.ld_saved = p->ld_saved;
+    g.g = own_g ? ws : nullptr, g.ld_g = p->n_out;
+    g.dres = p->dresidual, g.ld_dres = p->ld_dres;
+    g.dbias = p->dbias;
+    g.rows = p->rows, g.n = p->n_out, g.act = p->act;
+    HIPCHK(launch_act_grad(g, p->dtype, st));
+  }
+  const void* g = own_g ? ws : p->dy;
+  const int64_t ld_g = own_g ? p->n_out : p->ld_dy;
+  if (p->dx) {
+    Product d{};
+    d.a = g, d.sam = ld_g, d.sak = 1;
+    d.b = p->weight, d.sbn = 1, d.sbk = p->ld_w;
+    d.M = p->rows, d.N = p->n_in, d.K = p->n_out;
+    d.out = p->dx, d.ld_out = p->ld_dx;
+    HIPCHK(launch_product(d, p->dtype, st));
+  }
+  if (p->dweight) {
+    Product d{};
+    d.a = g, d.sam = 1, d.sak = ld_g;
+    d.b = p->x, d.sbn = 1, d.sbk = p->ld_x;
+    d.M = p->n_out, d.N = p->n_in, d.K = p->rows;
+    d.out = p->dweight, d.ld_out = p->ld_dw;
+    HIPCHK(launch_product(d, p->dtype, st));
+  }
+  return VB_OK;
+}
+
+extern "C" vb_status vb_cross_entropy_workspace(int64_t rows, int32_t classes, int32_t dtype, size_t* bytes) {
+  if (!bytes) return fail(VB_EINVAL, "vb_cross_entropy_workspace: bytes is NULL");
+  TRY(check_sizes("vb_cross_entropy_workspace", rows, classes, classes, dtype));
+  *bytes = align_up(16 + (size_t)rows * 4);
+  return VB_OK;
+}
+
+extern "C" vb_status vb_cross_entropy(const vb_cross_entropy_args* p, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "vb_cross_entropy";
+  if (!p) return fail(VB_EINVAL, "%s: NULL argument", fn);
+  TRY(check_sizes(fn, p->rows, p->classes, p->classes, p->dtype));
+  const bool some = p->rows > 0;
+  TRY(check_matrix(fn, "logits", p->logits, p->ld, p->classes, p->dtype, some));
+  TRY(check_matrix(fn, "dlogits", p->dlogits, p->ld_d, p->classes, p->dtype, false));
+  if (some && !p->labels) return fail(VB_EINVAL, "%s: labels is NULL", fn);
+  if ((uintptr_t)p->labels & 7) return fail(VB_EINVAL, "%s: labels is not aligned to its elements", fn);
+  if (((uintptr_t)p->loss & 3) || ((uintptr_t)p->row_loss & 3)) return fail(VB_EINVAL, "%s: loss or row_loss is not aligned to its elements", fn);
+  if (!(p->label_smoothing >= 0.f && p->label_smoothing <= 1.f))
+    return fail(VB_EINVAL, "%s: label_smoothing must be in [0, 1] (got %g)", fn, p->label_smoothing);
+  if (!p->loss && !p->row_loss && !p->dlogits) return fail(VB_EINVAL, "%s: nothing to compute", fn);
+  if (p->dlogits && p->dlogits == p->logits && p->ld_d != p->ld)
+    return fail(VB_ESHAPE, "%s: dlogits over logits needs the same leading dimension", fn);
+  size_t need = 0;
+  TRY(vb_cross_entropy_workspace(p->rows, p->classes, p->dtype, &need));
+  TRY(check_ws(fn, ws, ws_bytes, need));
+  HIPCHK(launch_cross_entropy(*p, ws, (hipStream_t)stream));
+  return VB_OK;
+}
+
+namespace {
+
+// Workgroups of all tensors, or -1 for a bad size or too many.
+long long clip_blocks(int32_t n, const int64_t* sizes) {
+  long long blocks = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (sizes[i] < 0 || sizes[i] > (INT64_C(1) << 44)) return -1;
+    blocks += (sizes[i] + CLIP_CHUNK - 1) / CLIP_CHUNK;
+    if (blocks > 0x7fffffffLL) return -1;
+  }
+  return blocks;
+}
+
+}  // namespace
+
+extern "C" vb_status vb_clip_grad_norm_workspace(int32_t n_tensors, const int64_t* sizes, size_t* bytes) {
+  const char* fn = "vb_clip_grad_norm_workspace";
+  if (!bytes) return fail(VB_EINVAL, "%s: bytes is NULL", fn);
+  if (n_tensors < 0 || (n_tensors > 0 && !sizes)) return fail(VB_EINVAL, "%s: bad tensor list", fn);
+  const long long blocks = clip_blocks(n_tensors, sizes);
+  if (blocks < 0) return fail(VB_EINVAL, "%s: a size is negative or the total too large", fn);
+  *bytes = align_up(16 + (size_t)blocks * 8);
+  return VB_OK;
+}
+
+extern "C" vb_status vb_clip_grad_norm(int32_t n_tensors, const void* const* grads, void* const* out,
+                                       const int64_t* sizes, const int32_t* dtypes, float max_norm, float* norm,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "vb_clip_grad_norm";
+  if (n_tensors < 0 || (n_tensors > 0 && (!grads || !sizes || !dtypes))) return fail(VB_EINVAL, "%s: bad tensor list", fn);
+  if (!norm || ((uintptr_t)norm & 3)) return fail(VB_EINVAL, "%s: norm is NULL or misaligned", fn);
+  if (!(max_norm >= 0.f)) return fail(VB_EINVAL, "%s: max_norm must be >= 0 (got %g)", fn, max_norm);
+  size_t need = 0;
+  TRY(vb_clip_grad_norm_workspace(n_tensors, sizes, &need));
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    if (dtypes[i] < VB_F32 || dtypes[i] > VB_F16) return fail(VB_EINVAL, "%s: unknown dtype %d of tensor %d", fn, dtypes[i], i);
+    if (sizes[i] == 0) continue;
+    const uintptr_t es = elem_size(dtypes[i]);
+    if (!grads[i] || (uintptr_t)grads[i] % es || (out && (!out[i] || (uintptr_t)out[i] % es)))
+      return fail(VB_EINVAL, "%s: pointer of tensor %d is NULL or misaligned", fn, i);
+  }
+  TRY(check_ws(fn, ws, ws_bytes, need));
+  const hipStream_t st = (hipStream_t)stream;
+  float* scale = (float*)ws;
+  double* partial = (double*)((char*)ws + 16);
+  long long blocks = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long at = 0;
+    int32_t i = 0;
+    while (i < n_tensors) {
+      ClipTable t;
+      t.count = 0;
+      t.first[0] = 0;
+      for (; i < n_tensors && t.count < CLIP_TENSORS; ++i) {
+        if (sizes[i] == 0) continue;
+        const int c = t.count++;
+        t.grad[c] = grads[i];
+        t.out[c] = out ? out[i] : (void*)grads[i];
+        t.n[c] = sizes[i];
+        t.dtype[c] = (unsigned char)dtypes[i];
+        t.first[c + 1] = t.first[c] + (unsigned)((sizes[i] + CLIP_CHUNK - 1) / CLIP_CHUNK);
+      }
+      if (!t.count) break;
+      if (pass == 0) HIPCHK(launch_clip_partial(t, partial + at, st));
+      else HIPCHK(launch_clip_scale(t, scale, st));
+      at += t.first[t.count];
+    }
+    if (pass == 0) {
+      blocks = at;
+      HIPCHK(launch_clip_norm(partial, blocks, max_norm, norm, scale, st));
+    }
+  }
+  return VB_OK;
+}
