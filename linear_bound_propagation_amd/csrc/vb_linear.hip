@@ -133,6 +133,256 @@ __global__ __launch_bounds__(256) void product_kernel(Product p, int tiles_n) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// The large product C = A B^T of operands whose rows are contiguous along the
+// reduction and start on 16-byte boundaries.
+//
+// Workgroups of WM x WN wavefronts compute BM x BN tiles.  Both operands pass
+// through LDS in stages 128 bytes of the reduction deep (64 16-bit or 32 float32
+// numbers), loaded straight from global memory into LDS and double buffered: the
+// loads of stage t+1 are in flight during the products of stage t.  A wavefront
+// reads its operands in four steps of two 16-byte chunks a row, each step one
+// ahead of its MFMAs, the first step of the next stage under the last MFMAs of
+// this one, so that the barrier between stages is not waited on with idle matrix
+// cores.
+// Chunk c of row r lies at position c ^ (r & 7) of the row: the eight rows that a
+// quarter of a wavefront reads together then fall on different LDS banks.  A
+// direct load writes 64 consecutive chunks (eight rows), so the permutation is
+// done on the global side; a row's eight lanes still cover its 128 bytes.
+// Float32 uses the same bytes: MFMA step s of a chunk takes element s of it for
+// both operands, which permutes the reduction alike on both sides.
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Chunk;  // 16 bytes of a row, and the products of two chunks of each operand's rows
+template <>
+struct Chunk<float> {
+  typedef f32x4 type;
+  __device__ static f32x16 mma(f32x4 a, f32x4 b, f32x16 c) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[s], b[s], c, 0, 0, 0);
+    return c;
+  }
+};
+template <>
+struct Chunk<bf16> {
+  typedef bf16x8 type;
+  __device__ static f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Chunk<f16> {
+  typedef f16x8 type;
+  __device__ static f32x16 mma(f16x8 a, f16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// what a lane loads past the end of the reduction
+__device__ const u32x4 zero_chunk = {0, 0, 0, 0};
+
+__device__ __forceinline__ void load_to_lds(const void* g, void* l) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
+                                   (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+}
+
+// Writes VEC consecutive outputs of row m from n on: bias, residual, activation.
+// vec: 16-byte accesses (the caller has checked alignment and that all VEC exist).
+template <typename T, int VEC>
+__device__ __forceinline__ void finish(const Product& p, long long m, int n, const float* v, bool vec, int cnt) {
+  typedef T TV __attribute__((ext_vector_type(VEC)));
+  float x[VEC];
+  if (vec) {
+    TV b, r;
+    if (p.bias) b = *(const TV*)((const T*)p.bias + n);
+    if (p.res) r = *(const TV*)((const T*)p.res + m * p.ld_res + n);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      x[i] = v[i];
+      if (p.bias) x[i] += to_f32((T)b[i]);
+      if (p.res) x[i] += to_f32((T)r[i]);
+    }
+    TV o;
+    if (p.pre) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[i] = from_f32<T>(x[i]);
+      *(TV*)((T*)p.pre + m * p.ld_pre + n) = o;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o[i] = from_f32<T>(act_value<T>(x[i], p.act));
+    *(TV*)((T*)p.out + m * p.ld_out + n) = o;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    if (i >= cnt) break;
+    float w = v[i];
+    if (p.bias) w += to_f32(((const T*)p.bias)[n + i]);
+    if (p.res) w += to_f32(((const T*)p.res)[m * p.ld_res + n + i]);
+    if (p.pre) ((T*)p.pre)[m * p.ld_pre + n + i] = from_f32<T>(w);
+    ((T*)p.out)[m * p.ld_out + n + i] = from_f32<T>(act_value<T>(w, p.act));
+  }
+}
+
+// Tile of a workgroup: workgroups go round the eight XCDs in turn, so each XCD takes
+// a contiguous run of tiles, walked in bands of eight tile rows; the 32 tiles that an
+// XCD has at a time then share 8 row and 4 column panels through its L2.
+__device__ __forceinline__ void tile_of(unsigned bid, int tm, int tn, int& i, int& j) {
+  const unsigned total = (unsigned)tm * tn, q = total / 8, r = total % 8, x = bid % 8;
+  const unsigned id = x * q + min(x, r) + bid / 8;
+  const unsigned band = id / (8u * tn), in = id % (8u * tn);
+  const unsigned rows = min(8u, (unsigned)tm - band * 8);
+  i = band * 8 + in % rows;
+  j = in / rows;
+}
+
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 2 : 4) void gemm_kernel(Product p, int tm, int tn) {
+  typedef typename Chunk<T>::type C;
+  constexpr int NW = WM * WN, LA = BM / 8 / NW, LB = BN / 8 / NW, STAGE = (BM + BN) * 128;
+  constexpr int TM = BM / WM, TN = BN / WN, MT = TM / 32, NT = TN / 32;
+  __shared__ __align__(16) char lds[2 * STAGE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int ti, tj;
+  tile_of(blockIdx.x, tm, tn, ti, tj);
+  const long long m0 = (long long)ti * BM;
+  const int n0 = tj * BN;
+  const int chunks = (int)(p.K * sizeof(T) / 16), stages = (chunks + 7) / 8;
+  const char* a = (const char*)p.a + m0 * p.sam * sizeof(T);
+  const char* b = (const char*)p.b + (long long)n0 * p.sbn * sizeof(T);
+  const int lr = lane >> 3, lc = (lane & 7) ^ lr;
+  // byte offsets of this lane's chunks in the first stage; rows past the end repeat the last row
+  unsigned oa[LA], ob[LB];
+#pragma unroll
+  for (int i = 0; i < LA; ++i)
+    oa[i] = (unsigned)min((long long)((i * NW + wave) * 8 + lr), p.M - 1 - m0) * (unsigned)(p.sam * sizeof(T)) + lc * 16;
+#pragma unroll
+  for (int i = 0; i < LB; ++i)
+    ob[i] = (unsigned)min((i * NW + wave) * 8 + lr, p.N - 1 - n0) * (unsigned)(p.sbn * sizeof(T)) + lc * 16;
+  auto issue = [&](int t, int base) {
+    const char* at = a + (long long)t * 128;
+    const char* bt = b + (long long)t * 128;
+    char* l = lds + base + wave * 1024;
+    if (t * 8 + 8 <= chunks) {
+#pragma unroll
+      for (int i = 0; i < LA; ++i) load_to_lds(at + oa[i], l + i * NW * 1024);
+#pragma unroll
+      for (int i = 0; i < LB; ++i) load_to_lds(bt + ob[i], l + BM * 128 + i * NW * 1024);
+    } else {
+      const bool in = t * 8 + lc < chunks;
+#pragma unroll
+      for (int i = 0; i < LA; ++i) load_to_lds(in ? (const void*)(at + oa[i]) : &zero_chunk, l + i * NW * 1024);
+#pragma unroll
+      for (int i = 0; i < LB; ++i)
+        load_to_lds(in ? (const void*)(bt + ob[i]) : &zero_chunk, l + BM * 128 + i * NW * 1024);
+    }
+  };
+  // every load has landed and every wavefront has read what it wants of the last stage
+  auto join = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+  const int wm = wave / WN, wn = wave % WN, r32 = lane & 31, half = lane >> 5;
+  int pos[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) pos[s] = ((2 * s + half) ^ (lane & 7)) * 16;
+  const int ra = (wm * TM + r32) * 128, rb = (BM + wn * TN + r32) * 128;
+  f32x16 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+  C fa[2][MT], fb[2][NT];
+  auto fetch = [&](int base, int s, int f) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fa[f][i] = *(const C*)(lds + base + ra + i * 4096 + pos[s]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fb[f][j] = *(const C*)(lds + base + rb + j * 4096 + pos[s]);
+  };
+  auto multiply = [&](int f) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = Chunk<T>::mma(fa[f][i], fb[f][j], acc[i][j]);
+  };
+  issue(0, 0);
+  join();
+  fetch(0, 0, 0);
+  for (int t = 0; t < stages; ++t) {
+    const int cur = (t & 1) * STAGE, nxt = STAGE - cur;
+    if (t + 1 < stages) issue(t + 1, nxt);
+    fetch(cur, 1, 1);
+    multiply(0);
+    fetch(cur, 2, 0);
+    multiply(1);
+    fetch(cur, 3, 1);
+    multiply(0);
+    join();
+    fetch(nxt, 0, 0);  // of the next stage; after the last one, unused
+    multiply(1);
+  }
+  join();
+  // Outputs leave through LDS, 32 rows of the wavefront's tile at a time in its own
+  // part of it, so that a row's outputs are written as whole 128-byte pieces.
+  constexpr int LDE = TN + 4, VEC = 16 / sizeof(T), LPR = TN / VEC, RPI = 64 / LPR;
+  static_assert(NW * 32 * LDE * 4 <= 2 * STAGE, "the output staging fits the operand stages");
+  float* e = (float*)lds + wave * 32 * LDE;
+  const unsigned long long mis =
+      (unsigned long long)p.out | (unsigned long long)p.res | (unsigned long long)p.pre | (unsigned long long)p.bias |
+      (unsigned long long)((p.ld_out | p.ld_res | p.ld_pre) * (long long)sizeof(T));
+  const bool aligned = (mis & 15) == 0;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) e[(8 * (q / 4) + 4 * half + (q & 3)) * LDE + j * 32 + r32] = acc[i][j][q];
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const long long mb = m0 + wm * TM + i * 32;
+    const int nb = n0 + wn * TN;
+    if (aligned && nb + TN <= p.N) {
+#pragma unroll
+      for (int r = 0; r < 32; r += RPI) {
+        const int row = r + lane / LPR, col = (lane % LPR) * VEC;
+        if (mb + row < p.M) finish<T, VEC>(p, mb + row, nb + col, e + row * LDE + col, true, VEC);
+      }
+    } else {
+      const int cols = min(TN, p.N - nb);
+      for (int k = lane; k < 32 * TN; k += 64) {
+        const int row = k / TN, col = k % TN;
+        if (mb + row < p.M && col < cols) finish<T, 1>(p, mb + row, nb + col, e + row * LDE + col, false, 1);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+  }
+}
+
+template <typename T, int BM, int BN, int WM, int WN>
+hipError_t launch_gemm(const Product& p, hipStream_t st) {
+  const long long tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
+  if (tm * tn > 0x7fffffffLL) return hipErrorInvalidValue;
+  gemm_kernel<T, BM, BN, WM, WN><<<dim3((unsigned)(tm * tn)), 64 * WM * WN, 0, st>>>(p, (int)tm, (int)tn);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_gemm_sized(const Product& p, hipStream_t st) {
+  auto tiles = [&](int b) { return (p.M + b - 1) / b * ((p.N + b - 1) / b); };
+  if (tiles(256) >= 200) return launch_gemm<T, 256, 256, 2, 4>(p, st);
+  if (tiles(128) >= 200) return launch_gemm<T, 128, 128, 2, 2>(p, st);
+  return launch_gemm<T, 64, 64, 2, 2>(p, st);
+}
+
+// rows contiguous along the reduction, 16-byte chunks throughout, 32-bit offsets within a tile's rows
+bool chunked(const void* p, long long row, long long el, long long K, int es) {
+  return el == 1 && (uintptr_t)p % 16 == 0 && row * es % 16 == 0 && K * es % 16 == 0 && row * es <= (1 << 22);
+}
+
 // 64 columns per workgroup, four rows at a time
 template <typename T>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p) {
@@ -162,6 +412,12 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(unsigned short* p, long 
 }  // namespace
 
 hipError_t launch_product(const Product& p, int dtype, hipStream_t st) {
+  const int es = (int)elem_size(dtype);
+  if (chunked(p.a, p.sam, p.sak, p.K, es) && chunked(p.b, p.sbn, p.sbk, p.K, es)) {
+    if (dtype == VB_F32) return launch_gemm_sized<float>(p, st);
+    if (dtype == VB_BF16) return launch_gemm_sized<bf16>(p, st);
+    return launch_gemm_sized<f16>(p, st);
+  }
   const int tn = (p.N + BN - 1) / BN;
   const long long blocks = (p.M + BM - 1) / BM * tn;
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
