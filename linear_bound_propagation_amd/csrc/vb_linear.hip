@@ -138,46 +138,55 @@ __global__ __launch_bounds__(256) void product_kernel(Product p, int tiles_n) {
 // reduction and start on 16-byte boundaries.
 //
 // Workgroups of WM x WN wavefronts compute BM x BN tiles.  Both operands pass
-// through LDS in stages 128 bytes of the reduction deep (64 16-bit or 32 float32
-// numbers), loaded straight from global memory into LDS and double buffered: the
-// loads of stage t+1 are in flight during the products of stage t.  A wavefront
-// reads its operands in four steps of two 16-byte chunks a row, each step one
-// ahead of its MFMAs, the first step of the next stage under the last MFMAs of
-// this one, so that the barrier between stages is not waited on with idle matrix
-// cores.
-// Chunk c of row r lies at position c ^ (r & 7) of the row: the eight rows that a
-// quarter of a wavefront reads together then fall on different LDS banks.  A
-// direct load writes 64 consecutive chunks (eight rows), so the permutation is
-// done on the global side; a row's eight lanes still cover its 128 bytes.
+// through a ring of NS stages in LDS, each 64 bytes of the reduction deep (32 16-bit
+// or 16 float32 numbers), loaded straight from global memory.  NS - 1 stages are in
+// flight at a time: all workgroups of an XCD reach new memory together, so a stage's
+// first touch waits for HBM and needs about two microseconds of products to hide
+// (with two stages of 128 bytes the matrix cores were busy 57 % of the clocks).
+// A wavefront's tile is MT x NT blocks of 16 x 16 outputs (v_mfma 16x16x32: at this
+// size the card is limited by power, and on the same random operands, from registers,
+// the 16-wide instructions ran at 1.63 GHz against 1.52 GHz for 32x32x16).  A stage is
+// two phases: the products of the upper half of the rows, under which the lower half
+// is read from LDS; then the barrier; then the products of the lower half, under which
+// the next stage's upper half and columns are read.  No wavefront waits on the barrier
+// or on LDS with idle matrix cores.
+// Chunk c of row r lies at position c ^ ((r >> 2) & 3) of the row: the 16 rows that
+// a quarter of a wavefront reads together (256 bytes a clock) then fall on different
+// LDS banks; measured 4.1 clocks a 1 KB read, against 16 for c ^ (r & 3).  A direct
+// load writes 64 consecutive chunks (16 rows), so the permutation is done on the
+// global side; a row's four lanes still cover its 64 bytes.
 // Float32 uses the same bytes: MFMA step s of a chunk takes element s of it for
 // both operands, which permutes the reduction alike on both sides.
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
+// 16 bytes of a row; mma: the products of a wavefront's 64 chunks (16 rows x 4) of each operand
 template <typename T>
-struct Chunk;  // 16 bytes of a row, and the products of two chunks of each operand's rows
+struct Chunk;
 template <>
 struct Chunk<float> {
   typedef f32x4 type;
-  __device__ static f32x16 mma(f32x4 a, f32x4 b, f32x16 c) {
+  static constexpr int MFMAS = 4;
+  __device__ static f32x4 mma(f32x4 a, f32x4 b, f32x4 c) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[s], b[s], c, 0, 0, 0);
+    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], c, 0, 0, 0);
     return c;
   }
 };
 template <>
 struct Chunk<bf16> {
   typedef bf16x8 type;
-  __device__ static f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  static constexpr int MFMAS = 1;
+  __device__ static f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
 };
 template <>
 struct Chunk<f16> {
   typedef f16x8 type;
-  __device__ static f32x16 mma(f16x8 a, f16x8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  static constexpr int MFMAS = 1;
+  __device__ static f32x4 mma(f16x8 a, f16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
 };
 
@@ -189,42 +198,46 @@ __device__ __forceinline__ void load_to_lds(const void* g, void* l) {
                                    (__attribute__((address_space(3))) void*)l, 16, 0, 0);
 }
 
-// Writes VEC consecutive outputs of row m from n on: bias, residual, activation.
-// vec: 16-byte accesses (the caller has checked alignment and that all VEC exist).
+// The activation of VEC values; one branch for all of them.
 template <typename T, int VEC>
-__device__ __forceinline__ void finish(const Product& p, long long m, int n, const float* v, bool vec, int cnt) {
+__device__ __forceinline__ void activate(float* x, int act) {
+  if (act == VB_ACT_NONE) return;
+  if (act == VB_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = act_value<T>(x[i], VB_ACT_RELU);
+  } else if (act == VB_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = act_value<T>(x[i], VB_ACT_GELU);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = act_value<T>(x[i], VB_ACT_SILU);
+  }
+}
+
+// Bias, residual and activation of VEC consecutive outputs of row m from n on, and
+// their 2 VEC- or 4 VEC-byte accesses (VEC > 1: the caller has checked the alignment).
+template <typename T, int VEC>
+__device__ __forceinline__ void finish(const Product& p, long long m, int n, const float* v) {
   typedef T TV __attribute__((ext_vector_type(VEC)));
   float x[VEC];
-  if (vec) {
-    TV b, r;
-    if (p.bias) b = *(const TV*)((const T*)p.bias + n);
-    if (p.res) r = *(const TV*)((const T*)p.res + m * p.ld_res + n);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      x[i] = v[i];
-      if (p.bias) x[i] += to_f32((T)b[i]);
-      if (p.res) x[i] += to_f32((T)r[i]);
-    }
-    TV o;
-    if (p.pre) {
+  for (int i = 0; i < VEC; ++i) x[i] = v[i];
+  auto add = [&](const T* q) {
+    const TV t = *(const TV*)q;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) o[i] = from_f32<T>(x[i]);
-      *(TV*)((T*)p.pre + m * p.ld_pre + n) = o;
-    }
+    for (int i = 0; i < VEC; ++i) x[i] += to_f32((T)t[i]);
+  };
+  auto put = [&](T* q) {
+    TV t;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) o[i] = from_f32<T>(act_value<T>(x[i], p.act));
-    *(TV*)((T*)p.out + m * p.ld_out + n) = o;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    if (i >= cnt) break;
-    float w = v[i];
-    if (p.bias) w += to_f32(((const T*)p.bias)[n + i]);
-    if (p.res) w += to_f32(((const T*)p.res)[m * p.ld_res + n + i]);
-    if (p.pre) ((T*)p.pre)[m * p.ld_pre + n + i] = from_f32<T>(w);
-    ((T*)p.out)[m * p.ld_out + n + i] = from_f32<T>(act_value<T>(w, p.act));
-  }
+    for (int i = 0; i < VEC; ++i) t[i] = from_f32<T>(x[i]);
+    *(TV*)q = t;
+  };
+  if (p.bias) add((const T*)p.bias + n);
+  if (p.res) add((const T*)p.res + m * p.ld_res + n);
+  if (p.pre) put((T*)p.pre + m * p.ld_pre + n);
+  activate<T, VEC>(x, p.act);
+  put((T*)p.out + m * p.ld_out + n);
 }
 
 // Tile of a workgroup: workgroups go round the eight XCDs in turn, so each XCD takes
@@ -239,122 +252,168 @@ __device__ __forceinline__ void tile_of(unsigned bid, int tm, int tn, int& i, in
   j = in / rows;
 }
 
+// Scheduling of one step: M MFMAs with D LDS reads and (nl of V) loads to LDS between
+template <int M, int D, int V>
+__device__ __forceinline__ void interleave(int nl) {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (i < D) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (nl && i < V) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+  }
+}
+
 template <typename T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 2 : 4) void gemm_kernel(Product p, int tm, int tn) {
+__global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void gemm_kernel(Product p, int tm, int tn) {
   typedef typename Chunk<T>::type C;
-  constexpr int NW = WM * WN, LA = BM / 8 / NW, LB = BN / 8 / NW, STAGE = (BM + BN) * 128;
-  constexpr int TM = BM / WM, TN = BN / WN, MT = TM / 32, NT = TN / 32;
-  __shared__ __align__(16) char lds[2 * STAGE];
+  constexpr int NW = WM * WN, LA = BM / 16 / NW, LB = BN / 16 / NW, NS = 4, STAGE = (BM + BN) * 64;
+  constexpr int TM = BM / WM, TN = BN / WN, MT = TM / 16, NT = TN / 16, MH = MT / 2;
+  __shared__ __align__(16) char lds[NS * STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int ti, tj;
   tile_of(blockIdx.x, tm, tn, ti, tj);
   const long long m0 = (long long)ti * BM;
   const int n0 = tj * BN;
-  const int chunks = (int)(p.K * sizeof(T) / 16), stages = (chunks + 7) / 8;
+  const int chunks = (int)(p.K * sizeof(T) / 16), stages = (chunks + 3) / 4, full = chunks / 4;
   const char* a = (const char*)p.a + m0 * p.sam * sizeof(T);
   const char* b = (const char*)p.b + (long long)n0 * p.sbn * sizeof(T);
-  const int lr = lane >> 3, lc = (lane & 7) ^ lr;
+  const int lr = lane >> 2, lc = (lane & 3) ^ (lane >> 4);
   // byte offsets of this lane's chunks in the first stage; rows past the end repeat the last row
   unsigned oa[LA], ob[LB];
 #pragma unroll
   for (int i = 0; i < LA; ++i)
-    oa[i] = (unsigned)min((long long)((i * NW + wave) * 8 + lr), p.M - 1 - m0) * (unsigned)(p.sam * sizeof(T)) + lc * 16;
+    oa[i] = (unsigned)min((long long)((i * NW + wave) * 16 + lr), p.M - 1 - m0) * (unsigned)(p.sam * sizeof(T)) + lc * 16;
 #pragma unroll
   for (int i = 0; i < LB; ++i)
-    ob[i] = (unsigned)min((i * NW + wave) * 8 + lr, p.N - 1 - n0) * (unsigned)(p.sbn * sizeof(T)) + lc * 16;
-  auto issue = [&](int t, int base) {
-    const char* at = a + (long long)t * 128;
-    const char* bt = b + (long long)t * 128;
+    ob[i] = (unsigned)min((i * NW + wave) * 16 + lr, p.N - 1 - n0) * (unsigned)(p.sbn * sizeof(T)) + lc * 16;
+  auto issue = [&](int t, int base) {  // a stage that the reduction fills
+    const char* at = a + (long long)t * 64;
+    const char* bt = b + (long long)t * 64;
     char* l = lds + base + wave * 1024;
-    if (t * 8 + 8 <= chunks) {
 #pragma unroll
-      for (int i = 0; i < LA; ++i) load_to_lds(at + oa[i], l + i * NW * 1024);
+    for (int i = 0; i < LA; ++i) load_to_lds(at + oa[i], l + i * NW * 1024);
 #pragma unroll
-      for (int i = 0; i < LB; ++i) load_to_lds(bt + ob[i], l + BM * 128 + i * NW * 1024);
-    } else {
-      const bool in = t * 8 + lc < chunks;
-#pragma unroll
-      for (int i = 0; i < LA; ++i) load_to_lds(in ? (const void*)(at + oa[i]) : &zero_chunk, l + i * NW * 1024);
-#pragma unroll
-      for (int i = 0; i < LB; ++i)
-        load_to_lds(in ? (const void*)(bt + ob[i]) : &zero_chunk, l + BM * 128 + i * NW * 1024);
-    }
+    for (int i = 0; i < LB; ++i) load_to_lds(bt + ob[i], l + BM * 64 + i * NW * 1024);
   };
-  // every load has landed and every wavefront has read what it wants of the last stage
-  auto join = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
-
-  const int wm = wave / WN, wn = wave % WN, r32 = lane & 31, half = lane >> 5;
-  int pos[4];
+  auto issue_part = [&](int t, int base) {  // any stage: zeros past the end
+    const char* at = a + (long long)t * 64;
+    const char* bt = b + (long long)t * 64;
+    char* l = lds + base + wave * 1024;
+    const bool in = t * 4 + lc < chunks;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) pos[s] = ((2 * s + half) ^ (lane & 7)) * 16;
-  const int ra = (wm * TM + r32) * 128, rb = (BM + wn * TN + r32) * 128;
-  f32x16 acc[MT][NT];
+    for (int i = 0; i < LA; ++i) load_to_lds(in ? (const void*)(at + oa[i]) : &zero_chunk, l + i * NW * 1024);
+#pragma unroll
+    for (int i = 0; i < LB; ++i)
+      load_to_lds(in ? (const void*)(bt + ob[i]) : &zero_chunk, l + BM * 64 + i * NW * 1024);
+  };
+  // The next stage has landed (all but the loads of the NS - 2 stages after it), this
+  // wavefront has its reads of the last stage, and so have the others.
+  auto join = [] {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * (LA + LB)) : "memory");
+  };
+  auto join_all = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+  const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, quarter = lane >> 4;
+  const int pos = (quarter ^ ((lane >> 2) & 3)) * 16;
+  const int ra = (wm * TM + r16) * 64 + pos, rb = (BM + wn * TN + r16) * 64 + pos;
+  f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  C fa[MT], fb[2][NT];
+  auto fetch_a = [&](int base, int h) {
 #pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-  C fa[2][MT], fb[2][NT];
-  auto fetch = [&](int base, int s, int f) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i) fa[f][i] = *(const C*)(lds + base + ra + i * 4096 + pos[s]);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) fb[f][j] = *(const C*)(lds + base + rb + j * 4096 + pos[s]);
+    for (int i = h * MH; i < h * MH + MH; ++i) fa[i] = *(const C*)(lds + base + ra + i * 1024);
   };
-  auto multiply = [&](int f) {
+  auto fetch_b = [&](int base, int f) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = Chunk<T>::mma(fa[f][i], fb[f][j], acc[i][j]);
+    for (int j = 0; j < NT; ++j) fb[f][j] = *(const C*)(lds + base + rb + j * 1024);
   };
-  issue(0, 0);
-  join();
-  fetch(0, 0, 0);
-  for (int t = 0; t < stages; ++t) {
-    const int cur = (t & 1) * STAGE, nxt = STAGE - cur;
-    if (t + 1 < stages) issue(t + 1, nxt);
-    fetch(cur, 1, 1);
-    multiply(0);
-    fetch(cur, 2, 0);
-    multiply(1);
-    fetch(cur, 3, 1);
-    multiply(0);
-    join();
-    fetch(nxt, 0, 0);  // of the next stage; after the last one, unused
-    multiply(1);
+  auto multiply = [&](int h, int f) {
+#pragma unroll
+    for (int i = h * MH; i < h * MH + MH; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = Chunk<T>::mma(fa[i], fb[f][j], acc[i][j]);
+  };
+  auto after = [](int base, int n) {  // the ring position n stages on
+    const int x = base + n * STAGE;
+    return x >= NS * STAGE ? x - NS * STAGE : x;
+  };
+  // A stage, its columns in fb[f]: loads() starts the loads of a later stage, wait() is
+  // one of the joins.  The reads are spread between the MFMAs; left to itself the
+  // compiler sinks them to their uses to save registers.
+  auto stage = [&](int cur, int f, auto&& loads, int nl, auto&& wait) {
+    __builtin_amdgcn_sched_barrier(0);
+    loads();
+    fetch_a(cur, 1);
+    multiply(0, f);
+    interleave<MH * NT * Chunk<T>::MFMAS, MH, LA + LB>(nl);
+    __builtin_amdgcn_sched_barrier(0);
+    wait();
+    __builtin_amdgcn_sched_barrier(0);
+    const int nxt = after(cur, 1);
+    fetch_b(nxt, f ^ 1);  // after the last stage, of nothing that is used
+    fetch_a(nxt, 0);
+    multiply(1, f);
+    interleave<MH * NT * Chunk<T>::MFMAS, MH + NT, 0>(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto none = [] {};
+  for (int i = 0; i < NS - 1; ++i)
+    if (i < full) issue(i, i * STAGE);
+    else if (i < stages) issue_part(i, i * STAGE);
+  if (full >= NS - 1) join(); else join_all();
+  fetch_b(0, 0);
+  fetch_a(0, 0);
+  int t = 0, cur = 0;
+  for (; t + NS < full; t += 2) {
+    stage(cur, 0, [&] { issue(t + NS - 1, after(cur, NS - 1)); }, LA + LB, join);
+    cur = after(cur, 1);
+    stage(cur, 1, [&] { issue(t + NS, after(cur, NS - 1)); }, LA + LB, join);
+    cur = after(cur, 1);
   }
-  join();
+  for (; t < stages; t += 2) {
+    if (t + NS - 1 < stages) issue_part(t + NS - 1, after(cur, NS - 1));
+    stage(cur, 0, none, 0, join_all);
+    cur = after(cur, 1);
+    if (t + 1 == stages) break;
+    if (t + NS < stages) issue_part(t + NS, after(cur, NS - 1));
+    stage(cur, 1, none, 0, join_all);
+    cur = after(cur, 1);
+  }
+  join_all();
   // Outputs leave through LDS, 32 rows of the wavefront's tile at a time in its own
   // part of it, so that a row's outputs are written as whole 128-byte pieces.
   constexpr int LDE = TN + 4, VEC = 16 / sizeof(T), LPR = TN / VEC, RPI = 64 / LPR;
-  static_assert(NW * 32 * LDE * 4 <= 2 * STAGE, "the output staging fits the operand stages");
+  static_assert(NW * 32 * LDE * 4 <= NS * STAGE, "the output staging fits the operand stages");
   float* e = (float*)lds + wave * 32 * LDE;
   const unsigned long long mis =
       (unsigned long long)p.out | (unsigned long long)p.res | (unsigned long long)p.pre | (unsigned long long)p.bias |
       (unsigned long long)((p.ld_out | p.ld_res | p.ld_pre) * (long long)sizeof(T));
   const bool aligned = (mis & 15) == 0;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
+  for (int i = 0; i < MT; i += 2) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int q = 0; q < 16; ++q) e[(8 * (q / 4) + 4 * half + (q & 3)) * LDE + j * 32 + r32] = acc[i][j][q];
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e[(16 * h + 4 * quarter + q) * LDE + j * 16 + r16] = acc[i + h][j][q];
     __builtin_amdgcn_wave_barrier();
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const long long mb = m0 + wm * TM + i * 32;
+    const long long mb = m0 + wm * TM + i * 16;
     const int nb = n0 + wn * TN;
     if (aligned && nb + TN <= p.N) {
+      const int row = lane / LPR, col = (lane % LPR) * VEC;
 #pragma unroll
-      for (int r = 0; r < 32; r += RPI) {
-        const int row = r + lane / LPR, col = (lane % LPR) * VEC;
-        if (mb + row < p.M) finish<T, VEC>(p, mb + row, nb + col, e + row * LDE + col, true, VEC);
-      }
+      for (int r = 0; r < 32; r += RPI)
+        if (mb + r + row < p.M) finish<T, VEC>(p, mb + r + row, nb + col, e + (r + row) * LDE + col);
     } else {
       const int cols = min(TN, p.N - nb);
       for (int k = lane; k < 32 * TN; k += 64) {
         const int row = k / TN, col = k % TN;
-        if (mb + row < p.M && col < cols) finish<T, 1>(p, mb + row, nb + col, e + row * LDE + col, false, 1);
+        if (mb + row < p.M && col < cols) finish<T, 1>(p, mb + row, nb + col, e + row * LDE + col);
       }
     }
     __builtin_amdgcn_wave_barrier();
