@@ -47,7 +47,7 @@ extern "C" {
  * residual and no activation, of a pre-norm block. */
 typedef struct {
   int64_t rows;                          /* >= 0 (0: nothing is enqueued)          */
-  int32_t n_in, n_out;                   /* > 0                                    */
+  int32_t n_in, n_out;                   /* in [1, 2^20]                           */
   int32_t dtype, act;                    /* VB_F32 .., VB_ACT_NONE ..              */
   const void* x;        int64_t ld_x;    /* [rows][n_in]                           */
   const void* weight;   int64_t ld_w;    /* [n_out][n_in]                          */
@@ -84,10 +84,12 @@ typedef struct {
   void* dresidual;      int64_t ld_dres; /* [rows][n_out] or NULL   */
 } vb_linear_bwd;
 
-/* Workspace of either call for these sizes, whatever the strides and pointers
- * (backward = 0: vb_linear_forward, 1: vb_linear_backward). */
-vb_status vb_linear_workspace(int64_t rows, int32_t n_in, int32_t n_out, int32_t dtype, int32_t backward,
-                              size_t* bytes);
+/* Workspace of a call with these arguments.  Of the pointers only x, weight and dy are
+ * looked at, for their alignment (rows that do not start on 16-byte boundaries or are no
+ * whole number of 16 bytes are copied before a large product), and whether the others
+ * are NULL; nothing is read through them. */
+vb_status vb_linear_forward_workspace(const vb_linear_fwd* p, size_t* bytes);
+vb_status vb_linear_backward_workspace(const vb_linear_bwd* p, size_t* bytes);
 vb_status vb_linear_forward(const vb_linear_fwd* p, void* ws, size_t ws_bytes, void* stream);
 vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t ws_bytes, void* stream);
 

@@ -1,5 +1,8 @@
 // The fused linear layer y = act(x W^T + bias + residual) and the products of
 // its backward pass.
+#include <algorithm>
+#include <cmath>
+
 #include "vb_train_device.h"
 #include "vb_train_internal.h"
 
@@ -43,106 +46,16 @@ __device__ __forceinline__ float act_grad(float dy, float s, int act) {
   return dy;
 }
 
-constexpr int BM = 64, BN = 64, BK = 32;
-
-template <typename T>
-struct Tile;
-template <>
-struct Tile<float> {
-  static constexpr int LD = BK + 4;
-  __device__ static f32x4 mfma(const float* a, const float* b, int r, int g, f32x4 c) {
-#pragma unroll
-    for (int k = 0; k < BK; k += 4)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r * LD + k + g], b[r * LD + k + g], c, 0, 0, 0);
-    return c;
-  }
-};
-template <>
-struct Tile<bf16> {
-  static constexpr int LD = BK + 8;
-  __device__ static f32x4 mfma(const bf16* a, const bf16* b, int r, int g, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(*(const bf16x8*)(a + r * LD + 8 * g),
-                                                   *(const bf16x8*)(b + r * LD + 8 * g), c, 0, 0, 0);
-  }
-};
-template <>
-struct Tile<f16> {
-  static constexpr int LD = BK + 8;
-  __device__ static f32x4 mfma(const f16* a, const f16* b, int r, int g, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(*(const f16x8*)(a + r * LD + 8 * g),
-                                                  *(const f16x8*)(b + r * LD + 8 * g), c, 0, 0, 0);
-  }
-};
-
-// 64 x 64 outputs per workgroup of four wavefronts (32 x 32 each), operands of
-// any strides through LDS in 32-deep steps.  MFMA rows run along n and columns
-// along m, so a lane holds four consecutive n of one row of the output.
-template <typename T>
-__global__ __launch_bounds__(256) void product_kernel(Product p, int tiles_n) {
-  constexpr int LD = Tile<T>::LD;
-  __shared__ __align__(16) T as[BM * LD];
-  __shared__ __align__(16) T bs[BN * LD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const long long m0 = (long long)(blockIdx.x / tiles_n) * BM;
-  const int n0 = (int)(blockIdx.x % tiles_n) * BN;
-  const T* a = (const T*)p.a;
-  const T* b = (const T*)p.b;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  f32x4 acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (long long k0 = 0; k0 < p.K; k0 += BK) {
-    for (int e = tid; e < BM * BK; e += 256) {
-      // consecutive threads along the operand's contiguous dimension
-      const int r = p.sak == 1 ? e / BK : e % BM, k = p.sak == 1 ? e % BK : e / BM;
-      const bool ok = m0 + r < p.M && k0 + k < p.K;
-      as[r * LD + k] = ok ? a[(m0 + r) * p.sam + (k0 + k) * p.sak] : (T)0.f;
-    }
-    for (int e = tid; e < BN * BK; e += 256) {
-      const int r = p.sbk == 1 ? e / BK : e % BN, k = p.sbk == 1 ? e % BK : e / BN;
-      const bool ok = n0 + r < p.N && k0 + k < p.K;
-      bs[r * LD + k] = ok ? b[(n0 + r) * p.sbn + (k0 + k) * p.sbk] : (T)0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = Tile<T>::mfma(bs + (wn + 16 * i) * LD, as + (wm + 16 * j) * LD, r16, g, acc[i][j]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const long long m = m0 + wm + 16 * j + r16;
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + wn + 16 * i + 4 * g + q;
-        if (n >= p.N) continue;
-        float v = acc[i][j][q];
-        if (p.bias) v += to_f32(((const T*)p.bias)[n]);
-        if (p.res) v += to_f32(((const T*)p.res)[m * p.ld_res + n]);
-        if (p.pre) ((T*)p.pre)[m * p.ld_pre + n] = from_f32<T>(v);
-        ((T*)p.out)[m * p.ld_out + n] = from_f32<T>(act_value<T>(v, p.act));
-      }
-  }
-}
-
 // ---------------------------------------------------------------------------
-// The large product C = A B^T of operands whose rows are contiguous along the
-// reduction and start on 16-byte boundaries.
+// The large product C(m, n) = sum_k A(m, k) B(n, k).  An operand is stored with the
+// reduction along its rows (x and W in the forward pass) or across them (W for dx; g
+// and x for dweight); rows start on 16-byte boundaries.
 //
-// Workgroups of WM x WN wavefronts compute BM x BN tiles.  Both operands pass
-// through a ring of NS stages in LDS, each 64 bytes of the reduction deep (32 16-bit
-// or 16 float32 numbers), loaded straight from global memory.  NS - 1 stages are in
-// flight at a time: all workgroups of an XCD reach new memory together, so a stage's
-// first touch waits for HBM and needs about two microseconds of products to hide
-// (with two stages of 128 bytes the matrix cores were busy 57 % of the clocks).
+// Workgroups of WM x WN wavefronts compute BM x BN tiles.  Both operands pass through
+// a ring of NS stages in LDS, each 64 bytes of the reduction deep (32 16-bit or 16
+// float32 numbers), loaded straight from global memory.  NS - 1 stages are in flight
+// at a time: all workgroups of an XCD reach new memory together, so a stage's first
+// touch waits for HBM.
 // A wavefront's tile is MT x NT blocks of 16 x 16 outputs (v_mfma 16x16x32: at this
 // size the card is limited by power, and on the same random operands, from registers,
 // the 16-wide instructions ran at 1.63 GHz against 1.52 GHz for 32x32x16).  A stage is
@@ -150,13 +63,22 @@ __global__ __launch_bounds__(256) void product_kernel(Product p, int tiles_n) {
 // is read from LDS; then the barrier; then the products of the lower half, under which
 // the next stage's upper half and columns are read.  No wavefront waits on the barrier
 // or on LDS with idle matrix cores.
-// Chunk c of row r lies at position c ^ ((r >> 2) & 3) of the row: the 16 rows that
-// a quarter of a wavefront reads together (256 bytes a clock) then fall on different
-// LDS banks; measured 4.1 clocks a 1 KB read, against 16 for c ^ (r & 3).  A direct
-// load writes 64 consecutive chunks (16 rows), so the permutation is done on the
-// global side; a row's four lanes still cover its 64 bytes.
-// Float32 uses the same bytes: MFMA step s of a chunk takes element s of it for
-// both operands, which permutes the reduction alike on both sides.
+//
+// The MFMA wants, per lane, chunk q = lane / 16 (16 bytes along the reduction) of row
+// lane % 16.
+//  - Reduction along the rows: a stage holds 64 bytes of each row, and a lane reads its
+//    chunk.  Chunk c of row r lies at position c ^ ((r >> 2) & 3): the 16 rows that a
+//    quarter of a wavefront reads together (256 bytes a clock) then fall on different
+//    LDS banks; measured 4.1 clocks a 1 KB read, against 16 for c ^ (r & 3).
+//  - Reduction across the rows: a stage holds 64 bytes / element size rows of BM (BN)
+//    elements.  16-bit operands are turned by the transposing LDS read (a group of 16
+//    lanes reads four rows of 16 elements, lane i receives column i); float32 ones are
+//    read element by element.  The rows of such a read lie at one bank offset, so
+//    blocks of 16 columns are permuted within a row by row_swizzle.
+// A direct load writes 64 consecutive chunks of LDS, so either permutation is done on
+// the global side, within pieces of 64 bytes (along) or whole rows (across).
+// Float32 uses the same bytes: MFMA step s of a chunk takes element s of it for both
+// operands, which permutes the reduction alike on both sides.
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
@@ -252,60 +174,133 @@ __device__ __forceinline__ void tile_of(unsigned bid, int tm, int tn, int& i, in
   j = in / rows;
 }
 
-// Scheduling of one step: M MFMAs with D LDS reads and (nl of V) loads to LDS between
+// Scheduling of one phase: D LDS reads and (nl of V) loads to LDS between M MFMAs
 template <int M, int D, int V>
 __device__ __forceinline__ void interleave(int nl) {
+  constexpr int PER = (D + M - 1) / M;
 #pragma unroll
   for (int i = 0; i < M; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (i < D) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (i * PER < D) __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
     if (nl && i < V) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
   }
 }
 
-template <typename T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void gemm_kernel(Product p, int tm, int tn) {
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// One operand of a workgroup's tile: ROWS of its rows (ACROSS: columns), its loads into
+// a stage and its reads from one.
+template <typename T, int ROWS, int NW, bool ACROSS>
+struct Operand {
   typedef typename Chunk<T>::type C;
-  constexpr int NW = WM * WN, LA = BM / 16 / NW, LB = BN / 16 / NW, NS = 4, STAGE = (BM + BN) * 64;
+  static constexpr int ES = sizeof(T), L = ROWS / 16 / NW;
+  static constexpr int RB = ROWS * ES;            // bytes of a stage's row when ACROSS
+  static constexpr int PER_BLOCK = ES;            // chunks of a block of 16 elements
+  static constexpr int READS = ACROSS ? (ES == 4 ? 4 : 2) : 1;  // LDS reads of a fetch
+  const char* base;   // first stage
+  long long step;     // bytes from stage to stage
+  unsigned off[L];    // this lane's chunks in the first stage
+  int lane, wave;
+
+  // what a row k of a stage is permuted by (ACROSS), in blocks of 16 elements: the rows
+  // read together (quarter 4 q .. in float32; 8 q + 0..3 for two q in 16 bits) differ,
+  // over the 256 bytes that LDS serves at once
+  __device__ static int row_swizzle(int k) {
+    if (ES == 4) return (k >> 2) & 3;
+    if (ROWS >= 128) return (k & 3) | ((k >> 3) & 1) << 2;
+    return ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+  }
+  // row (of the stage) and chunk that lane's i-th load brings when ACROSS
+  __device__ int row_of(int i) const { return ((i * NW + wave) * 1024 + lane * 16) / RB; }
+  __device__ int chunk_of(int i) const {
+    const int at = ((i * NW + wave) * 1024 + lane * 16) % RB / 16;
+    return ((at / PER_BLOCK) ^ row_swizzle(row_of(i))) * PER_BLOCK + at % PER_BLOCK;
+  }
+  __device__ int chunk_along() const { return (lane & 3) ^ (lane >> 4); }
+
+  // rows (ACROSS: columns) from r0 on of `count`; past the end the last one is repeated
+  __device__ void init(const void* p, long long ld, long long r0, long long count, int first_stage, int w, int l) {
+    lane = l, wave = w;
+    if (ACROSS) {
+      step = ld * 64;  // 64 / ES rows of ld * ES bytes
+      base = (const char*)p + r0 * ES + first_stage * step;
+      const int last = (int)min(((count - r0) * ES + 15) / 16 - 1, (long long)(RB / 16 - 1));
+#pragma unroll
+      for (int i = 0; i < L; ++i) off[i] = (unsigned)row_of(i) * (unsigned)(ld * ES) + min(chunk_of(i), last) * 16;
+    } else {
+      step = 64;
+      base = (const char*)p + r0 * ld * ES + first_stage * step;
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        off[i] = (unsigned)min((long long)((i * NW + wave) * 16 + (lane >> 2)), count - 1 - r0) * (unsigned)(ld * ES) +
+                 chunk_along() * 16;
+    }
+  }
+  // a stage that the reduction fills
+  __device__ void load(int t, char* lds) const {
+    const char* at = base + t * step;
+#pragma unroll
+    for (int i = 0; i < L; ++i) load_to_lds(at + off[i], lds + (i * NW + wave) * 1024);
+  }
+  // any stage: zeros past the end of the reduction's K elements
+  __device__ void load_part(int t, char* lds, int K) const {
+    const char* at = base + t * step;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const bool in = ACROSS ? t * (64 / ES) + row_of(i) < K : (t * 4 + chunk_along()) * (16 / ES) < K;
+      load_to_lds(in ? (const void*)(at + off[i]) : &zero_chunk, lds + (i * NW + wave) * 1024);
+    }
+  }
+  // where a lane reads: block b of 16 rows (columns) of a stage
+  __device__ int place(int b) const {
+    const int r16 = lane & 15, quarter = lane >> 4;
+    if (!ACROSS) return (b * 16 + r16) * 64 + (quarter ^ ((lane >> 2) & 3)) * 16;
+    if (ES == 4) return quarter * 4 * RB + (b ^ quarter) * 64 + r16 * 4;
+    const int k = quarter * 8 + (r16 >> 2);
+    return k * RB + (b ^ row_swizzle(k)) * 32 + (r16 & 3) * 8;
+  }
+  __device__ static C fetch(const char* p) {
+    if constexpr (!ACROSS) {
+      return *(const C*)p;
+    } else if constexpr (ES == 4) {
+      return C{*(const float*)p, *(const float*)(p + RB), *(const float*)(p + 2 * RB), *(const float*)(p + 3 * RB)};
+    } else {
+      typedef __attribute__((address_space(3))) s16x4* lds4;
+      union {
+        s16x4 h[2];
+        C c;
+      } u;
+      u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
+      u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * RB));
+      return u.c;
+    }
+  }
+};
+
+template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB>
+__global__ __launch_bounds__(64 * WM * WN, BN == 64 || BM == 128 ? 4 : 2) void gemm_kernel(Product p, int tm, int tn) {
+  typedef typename Chunk<T>::type C;
+  constexpr int NW = WM * WN, NS = 4, STAGE = (BM + BN) * 64, KS = 64 / sizeof(T);
   constexpr int TM = BM / WM, TN = BN / WN, MT = TM / 16, NT = TN / 16, MH = MT / 2;
+  typedef Operand<T, BM, NW, XA> OA;
+  typedef Operand<T, BN, NW, XB> OB;
+  constexpr int LA = OA::L, LB = OB::L, RA = OA::READS, RB = OB::READS;
   __shared__ __align__(16) char lds[NS * STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int ti, tj;
   tile_of(blockIdx.x, tm, tn, ti, tj);
   const long long m0 = (long long)ti * BM;
   const int n0 = tj * BN;
-  const int chunks = (int)(p.K * sizeof(T) / 16), stages = (chunks + 3) / 4, full = chunks / 4;
-  const char* a = (const char*)p.a + m0 * p.sam * sizeof(T);
-  const char* b = (const char*)p.b + (long long)n0 * p.sbn * sizeof(T);
-  const int lr = lane >> 2, lc = (lane & 3) ^ (lane >> 4);
-  // byte offsets of this lane's chunks in the first stage; rows past the end repeat the last row
-  unsigned oa[LA], ob[LB];
-#pragma unroll
-  for (int i = 0; i < LA; ++i)
-    oa[i] = (unsigned)min((long long)((i * NW + wave) * 16 + lr), p.M - 1 - m0) * (unsigned)(p.sam * sizeof(T)) + lc * 16;
-#pragma unroll
-  for (int i = 0; i < LB; ++i)
-    ob[i] = (unsigned)min((i * NW + wave) * 16 + lr, p.N - 1 - n0) * (unsigned)(p.sbn * sizeof(T)) + lc * 16;
-  auto issue = [&](int t, int base) {  // a stage that the reduction fills
-    const char* at = a + (long long)t * 64;
-    const char* bt = b + (long long)t * 64;
-    char* l = lds + base + wave * 1024;
-#pragma unroll
-    for (int i = 0; i < LA; ++i) load_to_lds(at + oa[i], l + i * NW * 1024);
-#pragma unroll
-    for (int i = 0; i < LB; ++i) load_to_lds(bt + ob[i], l + BM * 64 + i * NW * 1024);
-  };
-  auto issue_part = [&](int t, int base) {  // any stage: zeros past the end
-    const char* at = a + (long long)t * 64;
-    const char* bt = b + (long long)t * 64;
-    char* l = lds + base + wave * 1024;
-    const bool in = t * 4 + lc < chunks;
-#pragma unroll
-    for (int i = 0; i < LA; ++i) load_to_lds(in ? (const void*)(at + oa[i]) : &zero_chunk, l + i * NW * 1024);
-#pragma unroll
-    for (int i = 0; i < LB; ++i)
-      load_to_lds(in ? (const void*)(bt + ob[i]) : &zero_chunk, l + BM * 64 + i * NW * 1024);
-  };
+  // this workgroup's part of the reduction
+  const int first = blockIdx.y * p.split_stages;
+  const int K = (int)min(p.K - (long long)first * KS, (long long)p.split_stages * KS);
+  const int stages = (K + KS - 1) / KS, full = K / KS;
+  OA a;
+  OB b;
+  a.init(p.a, p.lda, m0, p.M, first, wave, lane);
+  b.init(p.b, p.ldb, n0, p.N, first, wave, lane);
+  auto issue = [&](int t, int base) { a.load(t, lds + base), b.load(t, lds + base + BM * 64); };
+  auto issue_part = [&](int t, int base) { a.load_part(t, lds + base, K), b.load_part(t, lds + base + BM * 64, K); };
   // The next stage has landed (all but the loads of the NS - 2 stages after it), this
   // wavefront has its reads of the last stage, and so have the others.
   auto join = [] {
@@ -314,8 +309,11 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void gemm_kernel(Pr
   auto join_all = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
   const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, quarter = lane >> 4;
-  const int pos = (quarter ^ ((lane >> 2) & 3)) * 16;
-  const int ra = (wm * TM + r16) * 64 + pos, rb = (BM + wn * TN + r16) * 64 + pos;
+  int pa[MT], pb[NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) pa[i] = a.place(wm * MT + i);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) pb[j] = BM * 64 + b.place(wn * NT + j);
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -324,11 +322,11 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void gemm_kernel(Pr
   C fa[MT], fb[2][NT];
   auto fetch_a = [&](int base, int h) {
 #pragma unroll
-    for (int i = h * MH; i < h * MH + MH; ++i) fa[i] = *(const C*)(lds + base + ra + i * 1024);
+    for (int i = h * MH; i < h * MH + MH; ++i) fa[i] = OA::fetch(lds + base + pa[i]);
   };
   auto fetch_b = [&](int base, int f) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) fb[f][j] = *(const C*)(lds + base + rb + j * 1024);
+    for (int j = 0; j < NT; ++j) fb[f][j] = OB::fetch(lds + base + pb[j]);
   };
   auto multiply = [&](int h, int f) {
 #pragma unroll
@@ -348,7 +346,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void gemm_kernel(Pr
     loads();
     fetch_a(cur, 1);
     multiply(0, f);
-    interleave<MH * NT * Chunk<T>::MFMAS, MH, LA + LB>(nl);
+    interleave<MH * NT * Chunk<T>::MFMAS, MH * RA, LA + LB>(nl);
     __builtin_amdgcn_sched_barrier(0);
     wait();
     __builtin_amdgcn_sched_barrier(0);
@@ -356,7 +354,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void gemm_kernel(Pr
     fetch_b(nxt, f ^ 1);  // after the last stage, of nothing that is used
     fetch_a(nxt, 0);
     multiply(1, f);
-    interleave<MH * NT * Chunk<T>::MFMAS, MH + NT, 0>(0);
+    interleave<MH * NT * Chunk<T>::MFMAS, MH * RA + NT * RB, 0>(0);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto none = [] {};
@@ -404,7 +402,15 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void gemm_kernel(Pr
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const long long mb = m0 + wm * TM + i * 16;
     const int nb = n0 + wn * TN;
-    if (aligned && nb + TN <= p.N) {
+    if (p.partial) {
+      // float32 sums of this part, rows of N rounded up to four
+      float* part = p.partial + (blockIdx.y * p.M + mb) * (long long)p.ld_partial + nb;
+      const int row = lane / (TN / 4), col = lane % (TN / 4) * 4;
+#pragma unroll
+      for (int r = 0; r < 32; r += 256 / TN)
+        if (mb + r + row < p.M && nb + col < p.N)
+          *(f32x4*)(part + (r + row) * (long long)p.ld_partial + col) = *(const f32x4*)(e + (r + row) * LDE + col);
+    } else if (aligned && nb + TN <= p.N) {
       const int row = lane / LPR, col = (lane % LPR) * VEC;
 #pragma unroll
       for (int r = 0; r < 32; r += RPI)
@@ -421,46 +427,341 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void gemm_kernel(Pr
   }
 }
 
-template <typename T, int BM, int BN, int WM, int WN>
-hipError_t launch_gemm(const Product& p, hipStream_t st) {
-  const long long tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
-  if (tm * tn > 0x7fffffffLL) return hipErrorInvalidValue;
-  gemm_kernel<T, BM, BN, WM, WN><<<dim3((unsigned)(tm * tn)), 64 * WM * WN, 0, st>>>(p, (int)tm, (int)tn);
+// ---------------------------------------------------------------------------
+// Few rows: the weights are read once and their reading is the time.  Rows may
+// start anywhere; 16-byte loads at element alignment are ordinary loads here, which
+// cost extra only where a line is crossed.
+
+template <typename T>
+struct Loose;  // 16 bytes of consecutive elements at element alignment
+template <>
+struct Loose<float> {
+  typedef f32x4 type __attribute__((aligned(4)));
+};
+template <>
+struct Loose<bf16> {
+  typedef bf16x8 type __attribute__((aligned(2)));
+};
+template <>
+struct Loose<f16> {
+  typedef f16x8 type __attribute__((aligned(2)));
+};
+
+template <typename T>
+__device__ __forceinline__ typename Chunk<T>::type load_loose(const T* p) {
+  return *(const typename Loose<T>::type*)p;
+}
+
+// Up to four rows: R weight rows per workgroup, whose four wavefronts take the chunks
+// of the reduction in turn (1 KB of a row per load, R loads and a chunk of each x row,
+// which stay in the L1 cache, per step); float32 multiply-adds on the vector units.
+template <typename T, int MR, int R>
+__global__ __launch_bounds__(256) void rows_kernel(Product p) {
+  typedef typename Chunk<T>::type C;
+  constexpr int EC = 16 / sizeof(T);
+  __shared__ float red[4][R * MR];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * R, chunks = (int)(p.K / EC), tail = (int)(p.K % EC);
+  const T* w[R];
+  const T* x[MR];
+#pragma unroll
+  for (int r = 0; r < R; ++r) w[r] = (const T*)p.b + (long long)min(n0 + r, p.N - 1) * p.ldb;
+#pragma unroll
+  for (int m = 0; m < MR; ++m) x[m] = (const T*)p.a + min((long long)m, p.M - 1) * p.lda;
+  float acc[R][MR];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MR; ++m) acc[r][m] = 0.f;
+#pragma unroll 2
+  for (int c = threadIdx.x; c < chunks; c += 256) {
+    C wv[R], xv[MR];
+#pragma unroll
+    for (int r = 0; r < R; ++r) wv[r] = load_loose(w[r] + (long long)c * EC);
+#pragma unroll
+    for (int m = 0; m < MR; ++m) xv[m] = load_loose(x[m] + (long long)c * EC);
+#pragma unroll
+    for (int e = 0; e < EC; ++e)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < MR; ++m) acc[r][m] = fmaf(to_f32((T)wv[r][e]), to_f32((T)xv[m][e]), acc[r][m]);
+  }
+  if ((int)threadIdx.x < tail) {
+    const long long k = (long long)chunks * EC + threadIdx.x;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int m = 0; m < MR; ++m) acc[r][m] = fmaf(to_f32(w[r][k]), to_f32(x[m][k]), acc[r][m]);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+      const float s = wave_sum(acc[r][m]);
+      if (lane == 0) red[wave][m * R + r] = s;
+    }
+  __syncthreads();
+  const int t = threadIdx.x, m = t / R, n = n0 + t % R;
+  if (t < R * MR && m < p.M && n < p.N) {
+    const float v = (red[0][t] + red[1][t]) + (red[2][t] + red[3][t]);
+    finish<T, 1>(p, m, n, &v);
+  }
+}
+
+// Up to 16 MB rows: 16 weight rows per workgroup along the MFMA rows, the x rows along
+// its columns; the 16 wavefronts take runs of 128 bytes of the reduction in turn (two
+// MFMA steps) and their sums meet in LDS.  Measured at 8 x 4096 -> 16384, bf16: 29.2 us;
+// with eight wavefronts 29.4 (and 63.7 against 60.7 us in float32), with longer runs
+// 30.3, with 32 weight rows per workgroup 61.
+template <typename T, int MB>
+__global__ __launch_bounds__(1024) void narrow_kernel(Product p) {
+  typedef typename Chunk<T>::type C;
+  constexpr int EC = 16 / sizeof(T), U = 2, NW = 16;
+  __shared__ __align__(16) float red[NW][MB * 256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, quarter = lane >> 4;
+  const int n0 = blockIdx.x * 16, chunks = (int)(p.K / EC), tail = (int)(p.K % EC);
+  const T* w = (const T*)p.b + (long long)min(n0 + r16, p.N - 1) * p.ldb;
+  const T* x[MB];
+#pragma unroll
+  for (int m = 0; m < MB; ++m) x[m] = (const T*)p.a + min((long long)(16 * m + r16), p.M - 1) * p.lda;
+  f32x4 acc[MB];
+#pragma unroll
+  for (int m = 0; m < MB; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int runs = chunks / (4 * U);
+  for (int s = wave; s < runs; s += NW) {
+    C wv[U], xv[U][MB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) wv[u] = load_loose(w + (long long)(s * (4 * U) + u * 4 + quarter) * EC);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) xv[u][m] = load_loose(x[m] + (long long)(s * (4 * U) + u * 4 + quarter) * EC);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) acc[m] = Chunk<T>::mma(wv[u], xv[u][m], acc[m]);
+  }
+  // what is left of the reduction, a step of four chunks per wavefront, zeros past its end
+  auto part = [&](const T* q, int c) {
+    C v;
+#pragma unroll
+    for (int e = 0; e < EC; ++e) v[e] = (T)0.f;
+    if (c < chunks) {
+      v = load_loose(q + (long long)c * EC);
+    } else if (c == chunks) {
+#pragma unroll
+      for (int e = 0; e < EC; ++e)
+        if (e < tail) v[e] = q[(long long)c * EC + e];
+    }
+    return v;
+  };
+  for (int c0 = runs * 4 * U + wave * 4; c0 < chunks + (tail > 0); c0 += 4 * NW) {
+    const C wv = part(w, c0 + quarter);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) acc[m] = Chunk<T>::mma(wv, part(x[m], c0 + quarter), acc[m]);
+  }
+#pragma unroll
+  for (int m = 0; m < MB; ++m) *(f32x4*)&red[wave][m * 256 + lane * 4] = acc[m];
+  __syncthreads();
+  const int o = threadIdx.x;
+  if (o < MB * 256) {
+    const int n = o % 16, m = o / 16;
+    const int at = (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) v += red[k][at];
+    if (m < p.M && n0 + n < p.N) finish<T, 1>(p, m, n0 + n, &v);
+  }
+}
+
+template <typename T, int MR>
+hipError_t launch_rows(const Product& p, hipStream_t st) {
+  // four workgroups a CU before a workgroup takes more weight rows; four rows of x are
+  // a little faster here than in narrow_kernel in float32 (53 against 61 us at 4096 ->
+  // 16384), a little slower in 16 bits (31.7 against 29.2)
+  if (p.N >= 4096) rows_kernel<T, MR, 4><<<(p.N + 3) / 4, 256, 0, st>>>(p);
+  else if (p.N >= 2048) rows_kernel<T, MR, 2><<<(p.N + 1) / 2, 256, 0, st>>>(p);
+  else rows_kernel<T, MR, 1><<<p.N, 256, 0, st>>>(p);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t launch_gemm_sized(const Product& p, hipStream_t st) {
-  auto tiles = [&](int b) { return (p.M + b - 1) / b * ((p.N + b - 1) / b); };
-  if (tiles(256) >= 200) return launch_gemm<T, 256, 256, 2, 4>(p, st);
-  if (tiles(128) >= 200) return launch_gemm<T, 128, 128, 2, 2>(p, st);
-  return launch_gemm<T, 64, 64, 2, 2>(p, st);
+hipError_t launch_narrow(const Product& p, hipStream_t st) {
+  if (p.M == 1) return launch_rows<T, 1>(p, st);
+  if (p.M == 2) return launch_rows<T, 2>(p, st);
+  if (p.M <= 4) return launch_rows<T, 4>(p, st);
+  if (p.M <= 16) narrow_kernel<T, 1><<<(p.N + 15) / 16, 1024, 0, st>>>(p);
+  else narrow_kernel<T, 2><<<(p.N + 15) / 16, 1024, 0, st>>>(p);
+  return hipGetLastError();
 }
 
-// rows contiguous along the reduction, 16-byte chunks throughout, 32-bit offsets within a tile's rows
-bool chunked(const void* p, long long row, long long el, long long K, int es) {
-  return el == 1 && (uintptr_t)p % 16 == 0 && row * es % 16 == 0 && K * es % 16 == 0 && row * es <= (1 << 22);
-}
-
-// 64 columns per workgroup, four rows at a time
+// Adds the parts of a split reduction, in order, and finishes the outputs: four of a row
+// per thread.
 template <typename T>
+__global__ __launch_bounds__(256) void join_kernel(Product p, int splits) {
+  const int quads = p.ld_partial / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long m = i / quads;
+  const int n = (int)(i % quads) * 4;
+  if (m >= p.M) return;
+  const float* q = p.partial + m * p.ld_partial + n;
+  f32x4 v = *(const f32x4*)q;
+  for (int s = 1; s < splits; ++s) v += *(const f32x4*)(q + s * p.M * p.ld_partial);
+  const unsigned long long mis =
+      (unsigned long long)p.out | (unsigned long long)p.res | (unsigned long long)p.pre | (unsigned long long)p.bias |
+      (unsigned long long)((p.ld_out | p.ld_res | p.ld_pre) * (long long)sizeof(T));
+  const float x[4] = {v[0], v[1], v[2], v[3]};
+  if ((mis & 15) == 0 && n + 4 <= p.N) {
+    finish<T, 4>(p, m, n, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (n + k < p.N) finish<T, 1>(p, m, n + k, x + k);
+  }
+}
+
+template <typename T, int BM, int BN, int WM, int WN>
+hipError_t launch_gemm(const Product& p, int splits, hipStream_t st) {
+  const long long tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
+  if (tm * tn > 0x7fffffffLL) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)(tm * tn), splits);
+  constexpr int threads = 64 * WM * WN;
+  if (p.across_a) gemm_kernel<T, BM, BN, WM, WN, true, true><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+  else if (p.across_b) gemm_kernel<T, BM, BN, WM, WN, false, true><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+  else gemm_kernel<T, BM, BN, WM, WN, false, false><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
+  const int stages = (int)((p.K * (long long)sizeof(T) + 63) / 64);
+  p.split_stages = (stages + t.splits - 1) / t.splits;
+  const int splits = (stages + p.split_stages - 1) / p.split_stages;
+  if (splits == 1) p.partial = nullptr;
+  p.ld_partial = (p.N + 3) / 4 * 4;
+  hipError_t e;
+  if constexpr (sizeof(T) == 2) {
+    if (t.bm == 256 && t.bn == 256) e = launch_gemm<T, 256, 256, 2, 4>(p, splits, st);
+    else if (t.bm == 256) e = launch_gemm<T, 256, 128, 4, 2>(p, splits, st);
+    else if (t.bm == 128) e = launch_gemm<T, 128, 128, 2, 4>(p, splits, st);
+    else e = launch_gemm<T, 64, 64, 2, 2>(p, splits, st);
+  } else {
+    if (t.bm == 256) e = launch_gemm<T, 256, 128, 4, 2>(p, splits, st);
+    else if (t.bm == 128) e = launch_gemm<T, 128, 128, 2, 4>(p, splits, st);
+    else e = launch_gemm<T, 64, 64, 2, 2>(p, splits, st);
+  }
+  if (e != hipSuccess || splits == 1) return e;
+  const long long quads = p.M * (p.ld_partial / 4), blocks = (quads + 255) / 256;
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  join_kernel<T><<<dim3((unsigned)blocks), 256, 0, st>>>(p, splits);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Rows that do not start on 16-byte boundaries or end in part of a chunk are copied to
+// rows that do, zeros to the end of the chunk, before a large product.
+template <typename T>
+__global__ __launch_bounds__(256) void pack_kernel(const T* src, long long ld, long long rows, int n, T* dst,
+                                                   int chunks) {
+  typedef typename Chunk<T>::type C;
+  constexpr int EC = 16 / sizeof(T);
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long r = i / chunks;
+  const int c = (int)(i % chunks);
+  if (r >= rows) return;
+  const T* q = src + r * ld + (long long)c * EC;
+  C v;
+  if ((c + 1) * EC <= n) {
+    v = load_loose(q);
+  } else {
+#pragma unroll
+    for (int e = 0; e < EC; ++e) v[e] = c * EC + e < n ? q[e] : (T)0.f;
+  }
+  *(C*)(dst + i * EC) = v;
+}
+
+// g = dy act'(saved), its copies and its column sums.  A thread has one chunk of columns
+// and every eighth of ROWS rows (16-byte accesses at any alignment); the workgroup's 32
+// chunks of columns are summed over its rows in LDS, one float32 per column and
+// workgroup.
+constexpr int SUM_ROWS = 64;
+
+template <typename T, int ACT>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p) {
+  typedef typename Chunk<T>::type C;
+  typedef typename Loose<T>::type LC;
+  constexpr int EC = 16 / sizeof(T);
+  __shared__ float red[8][32 * EC + 1];
+  const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int n = (blockIdx.x * 32 + c) * EC;
+  const long long m0 = (long long)blockIdx.y * SUM_ROWS;
+  const T* dy = (const T*)p.dy;
+  const T* saved = (const T*)p.saved;
+  float sum[EC];
+#pragma unroll
+  for (int e = 0; e < EC; ++e) sum[e] = 0.f;
+  const int have = p.n - n;  // columns from this chunk on
+  for (long long m = m0 + w; m < min(m0 + SUM_ROWS, p.rows) && have > 0; m += 8) {
+    C d, s;
+    if (have >= EC) {
+      d = load_loose(dy + m * p.ld_dy + n);
+      if (ACT != VB_ACT_NONE) s = load_loose(saved + m * p.ld_saved + n);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EC; ++e) {
+        d[e] = e < have ? dy[m * p.ld_dy + n + e] : (T)0.f;
+        if (ACT != VB_ACT_NONE) s[e] = e < have ? saved[m * p.ld_saved + n + e] : (T)0.f;
+      }
+    }
+    C v;
+#pragma unroll
+    for (int e = 0; e < EC; ++e) {
+      const float x = act_grad<T>(to_f32((T)d[e]), ACT == VB_ACT_NONE ? 0.f : to_f32((T)s[e]), ACT);
+      sum[e] += x;
+      v[e] = from_f32<T>(x);
+    }
+    if (p.g) *(C*)((T*)p.g + m * p.ld_g + n) = v;
+    if (p.dres) {
+      T* o = (T*)p.dres + m * p.ld_dres + n;
+      if (have >= EC) {
+        *(LC*)o = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < EC; ++e)
+          if (e < have) o[e] = v[e];
+      }
+    }
+  }
+  if (!p.dbias) return;
+#pragma unroll
+  for (int e = 0; e < EC; ++e) red[w][c * EC + e] = sum[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * EC; i += 256) {
+    const int col = blockIdx.x * 32 * EC + i;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += red[k][i];
+    if (col < p.n) {
+      if (!p.partial) ((T*)p.dbias)[col] = from_f32<T>(s);
+      else p.partial[(long long)blockIdx.y * p.n + col] = s;
+    }
+  }
+}
+
+// dbias from the workgroups' sums: 64 columns per workgroup, whose four wavefronts take
+// the sums in turn
+template <typename T>
+__global__ __launch_bounds__(256) void column_sum_kernel(const float* partial, int parts, int n, T* out) {
   __shared__ float red[4][64];
   const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int n = blockIdx.x * 64 + c;
-  float sum = 0.f;
-  if (n < p.n)
-    for (long long m = w; m < p.rows; m += 4) {
-      const float s = p.saved ? to_f32(((const T*)p.saved)[m * p.ld_saved + n]) : 0.f;
-      const float v = act_grad<T>(to_f32(((const T*)p.dy)[m * p.ld_dy + n]), s, p.act);
-      if (p.g) ((T*)p.g)[m * p.ld_g + n] = from_f32<T>(v);
-      if (p.dres) ((T*)p.dres)[m * p.ld_dres + n] = from_f32<T>(v);
-      sum += v;
-    }
-  red[w][c] = sum;
+  const int col = blockIdx.x * 64 + c;
+  float s = 0.f;
+  if (col < n)
+    for (int i = w; i < parts; i += 4) s += partial[(long long)i * n + col];
+  red[w][c] = s;
   __syncthreads();
-  if (w == 0 && n < p.n && p.dbias)
-    ((T*)p.dbias)[n] = from_f32<T>((red[0][c] + red[1][c]) + (red[2][c] + red[3][c]));
+  if (w == 0 && col < n) out[col] = from_f32<T>((red[0][c] + red[1][c]) + (red[2][c] + red[3][c]));
 }
 
 __global__ __launch_bounds__(256) void fill_zero_kernel(unsigned short* p, long long rows, long long n, long long ld) {
@@ -468,30 +769,116 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(unsigned short* p, long 
   if (i < rows * n) p[i / n * ld + i % n] = 0;
 }
 
-}  // namespace
-
-hipError_t launch_product(const Product& p, int dtype, hipStream_t st) {
-  const int es = (int)elem_size(dtype);
-  if (chunked(p.a, p.sam, p.sak, p.K, es) && chunked(p.b, p.sbn, p.sbk, p.K, es)) {
-    if (dtype == VB_F32) return launch_gemm_sized<float>(p, st);
-    if (dtype == VB_BF16) return launch_gemm_sized<bf16>(p, st);
-    return launch_gemm_sized<f16>(p, st);
+template <typename T>
+hipError_t launch_act_grad_typed(const ActGrad& p, hipStream_t st) {
+  constexpr int EC = 16 / sizeof(T);
+  const long long parts = (p.rows + SUM_ROWS - 1) / SUM_ROWS;
+  // the rows go along the second grid dimension, 65535 parts at most a launch
+  for (long long at = 0; at < parts; at += 65535) {
+    const long long m = at * SUM_ROWS;
+    ActGrad q = p;
+    q.dy = (const T*)p.dy + m * p.ld_dy;
+    if (p.saved) q.saved = (const T*)p.saved + m * p.ld_saved;
+    if (p.g) q.g = (T*)p.g + m * p.ld_g;
+    if (p.dres) q.dres = (T*)p.dres + m * p.ld_dres;
+    q.rows = p.rows - m;
+    q.partial = parts > 1 && p.dbias ? p.partial + at * p.n : nullptr;
+    const dim3 grid((p.n + 32 * EC - 1) / (32 * EC), (unsigned)std::min(parts - at, 65535LL));
+    if (p.act == VB_ACT_NONE) act_grad_kernel<T, VB_ACT_NONE><<<grid, 256, 0, st>>>(q);
+    else if (p.act == VB_ACT_RELU) act_grad_kernel<T, VB_ACT_RELU><<<grid, 256, 0, st>>>(q);
+    else if (p.act == VB_ACT_GELU) act_grad_kernel<T, VB_ACT_GELU><<<grid, 256, 0, st>>>(q);
+    else act_grad_kernel<T, VB_ACT_SILU><<<grid, 256, 0, st>>>(q);
   }
-  const int tn = (p.N + BN - 1) / BN;
-  const long long blocks = (p.M + BM - 1) / BM * tn;
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-  if (dtype == VB_F32) product_kernel<float><<<dim3((unsigned)blocks), 256, 0, st>>>(p, tn);
-  else if (dtype == VB_BF16) product_kernel<bf16><<<dim3((unsigned)blocks), 256, 0, st>>>(p, tn);
-  else product_kernel<f16><<<dim3((unsigned)blocks), 256, 0, st>>>(p, tn);
+  if (p.dbias && parts > 1)
+    column_sum_kernel<T><<<(p.n + 63) / 64, 256, 0, st>>>(p.partial, (int)parts, p.n, (T*)p.dbias);
   return hipGetLastError();
 }
 
-hipError_t launch_act_grad(const ActGrad& p, int dtype, hipStream_t st) {
-  const unsigned blocks = (unsigned)((p.n + 63) / 64);
-  if (dtype == VB_F32) act_grad_kernel<float><<<blocks, 256, 0, st>>>(p);
-  else if (dtype == VB_BF16) act_grad_kernel<bf16><<<blocks, 256, 0, st>>>(p);
-  else act_grad_kernel<f16><<<blocks, 256, 0, st>>>(p);
+}  // namespace
+
+// Tile and split of a large product by the time they would take: rounds of workgroups
+// over 256 CUs, each a run of stages and a fixed part.  A stage takes `latency`
+// microseconds for a tile that has its CU to itself and `share` for each of several; both
+// were measured per tile size (4096 x 4096 x 8192 and 1024 x 1024 x 1024, and 64 x 4096 x
+// 4096 for the small ones).  A split costs the writing and reading of its float32 parts
+// at 4 TB/s and another launch.
+Tiling choose_tiling(int dtype, long long M, int N, long long K) {
+  struct Kind {
+    int bm, bn, per_cu;
+    double latency, share;
+  };
+  static const Kind k16[] = {{256, 256, 1, 0.62, 0.80}, {256, 128, 1, 0.42, 0.52}, {128, 128, 2, 0.30, 0.30},
+                             {64, 64, 4, 0.14, 0.125}};
+  static const Kind k32[] = {{256, 128, 1, 1.90, 1.90}, {128, 128, 2, 1.02, 0.98}, {64, 64, 4, 0.31, 0.30}};
+  const Kind* kinds = dtype == VB_F32 ? k32 : k16;
+  const int nk = dtype == VB_F32 ? 3 : 4;
+  const long long stages = (K * (long long)elem_size(dtype) + 63) / 64;
+  Tiling best{64, 64, 1};
+  double best_us = 1e30;
+  for (int k = 0; k < nk; ++k) {
+    const Kind& c = kinds[k];
+    const double tiles = (double)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    for (int s = 1; s <= 32 && s * 4 <= stages; s *= 2) {
+      const double blocks = tiles * s, slots = 256.0 * c.per_cu;
+      const double full = std::floor(blocks / slots), rest = blocks - full * slots;
+      auto stage = [&](double on_cu) { return std::fmax(c.latency, on_cu * c.share); };
+      const double run = (double)((stages + s - 1) / s);
+      double us = full * (run * stage(c.per_cu) + 3.0);
+      if (rest > 0) us += run * stage(std::ceil(rest / 256.0)) + 3.0;
+      if (s > 1) us += 3.0 + (2.0 * s * M * N * 4.0) / 4e6;
+      if (us < best_us) best_us = us, best = Tiling{c.bm, c.bn, s};
+    }
+  }
+  return best;
+}
+
+size_t tiling_bytes(const Tiling& t, long long M, int N) {
+  return t.splits > 1 ? (size_t)t.splits * M * ((N + 3) / 4 * 4) * 4 : 0;
+}
+
+bool product_is_narrow(const Product& p) { return p.M <= 32 && !p.across_a && !p.across_b; }
+
+size_t product_bytes(const Product& p, int dtype) {
+  if (product_is_narrow(p)) return 0;
+  return tiling_bytes(choose_tiling(dtype, p.M, p.N, p.K), p.M, p.N);
+}
+
+hipError_t launch_product(const Product& p, int dtype, hipStream_t st) {
+  if (product_is_narrow(p)) {
+    if (dtype == VB_F32) return launch_narrow<float>(p, st);
+    if (dtype == VB_BF16) return launch_narrow<bf16>(p, st);
+    return launch_narrow<f16>(p, st);
+  }
+  const Tiling t = choose_tiling(dtype, p.M, p.N, p.K);
+  if (dtype == VB_F32) return launch_tiled<float>(p, t, st);
+  if (dtype == VB_BF16) return launch_tiled<bf16>(p, t, st);
+  return launch_tiled<f16>(p, t, st);
+}
+
+bool is_chunked(const void* p, long long ld, long long n, int dtype) {
+  const long long es = (long long)elem_size(dtype);
+  return (uintptr_t)p % 16 == 0 && ld * es % 16 == 0 && n * es % 16 == 0 && ld * es <= MAX_CHUNKED_ROW;
+}
+
+hipError_t launch_pack(const void* src, long long ld, long long rows, int n, void* dst, int dtype, hipStream_t st) {
+  const int chunks = (int)(chunked_row(n, dtype) / 16);
+  const long long blocks = (rows * chunks + 255) / 256;
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)blocks);
+  if (dtype == VB_F32) pack_kernel<float><<<grid, 256, 0, st>>>((const float*)src, ld, rows, n, (float*)dst, chunks);
+  else if (dtype == VB_BF16) pack_kernel<bf16><<<grid, 256, 0, st>>>((const bf16*)src, ld, rows, n, (bf16*)dst, chunks);
+  else pack_kernel<f16><<<grid, 256, 0, st>>>((const f16*)src, ld, rows, n, (f16*)dst, chunks);
   return hipGetLastError();
+}
+
+size_t act_grad_bytes(long long rows, int n) {
+  return rows > SUM_ROWS ? (size_t)((rows + SUM_ROWS - 1) / SUM_ROWS) * n * 4 : 0;
+}
+
+hipError_t launch_act_grad(const ActGrad& p, int dtype, hipStream_t st) {
+  if (dtype == VB_F32) return launch_act_grad_typed<float>(p, st);
+  if (dtype == VB_BF16) return launch_act_grad_typed<bf16>(p, st);
+  return launch_act_grad_typed<f16>(p, st);
 }
 
 hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long long ld_bytes, hipStream_t st) {

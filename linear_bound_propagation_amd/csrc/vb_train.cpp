@@ -28,13 +28,18 @@ vb_status fail(vb_status s, const char* fmt, ...) {
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Rows and leading dimensions are bounded so that byte offsets within a matrix
-// fit 62 bits and row counts fit a grid dimension.
+// Bounds that keep byte offsets within a matrix below 2^62, row counts within a grid
+// dimension and, for the layers, a row within MAX_CHUNKED_ROW bytes.
 constexpr int64_t MAX_ROWS = 0x7fffffff, MAX_LD = INT64_C(1) << 30;
+constexpr int32_t MAX_WIDTH = 1 << 20, MAX_CLASSES = 1 << 30;
+static_assert(MAX_WIDTH * 4LL <= MAX_CHUNKED_ROW, "packed rows fit the product's offsets");
 
-vb_status check_sizes(const char* fn, int64_t rows, int32_t n_in, int32_t n_out, int32_t dtype) {
+vb_status check_sizes(const char* fn, int64_t rows, int32_t n_in, int32_t n_out, int32_t dtype,
+                      int32_t most = MAX_WIDTH) {
   if (rows < 0 || rows > MAX_ROWS) return fail(VB_EINVAL, "%s: rows must be in [0, 2^31) (got %lld)", fn, (long long)rows);
   if (n_in <= 0 || n_out <= 0) return fail(VB_EINVAL, "%s: sizes must be positive (got %d, %d)", fn, n_in, n_out);
+  if (n_in > most || n_out > most)
+    return fail(VB_EUNSUPPORTED, "%s: sizes above %d are not supported (got %d, %d)", fn, most, n_in, n_out);
   if (dtype < VB_F32 || dtype > VB_F16) return fail(VB_EINVAL, "%s: unknown dtype %d", fn, dtype);
   return VB_OK;
 }
@@ -62,11 +67,96 @@ vb_status check_ws(const char* fn, const void* ws, size_t ws_bytes, size_t need)
 
 }  // namespace
 
-extern "C" vb_status vb_linear_workspace(int64_t rows, int32_t n_in, int32_t n_out, int32_t dtype, int32_t backward,
-                                         size_t* bytes) {
-  if (!bytes) return fail(VB_EINVAL, "vb_linear_workspace: bytes is NULL");
-  TRY(check_sizes("vb_linear_workspace", rows, n_in, n_out, dtype));
-  *bytes = backward ? align_up((size_t)rows * n_out * elem_size(dtype)) : 0;
+namespace {
+
+// A part of the workspace: its offset, or none.
+struct Part {
+  size_t at = 0;
+  bool used = false;
+  void take(size_t& total, size_t bytes) {
+    if (!bytes) return;
+    at = total, used = true;
+    total += align_up(bytes);
+  }
+  void* in(void* ws) const { return used ? (char*)ws + at : nullptr; }
+};
+
+// The forward product, and copies of operands whose rows a large product cannot read.
+struct ForwardPlan {
+  Product d{};
+  Part x, w, partial;
+  size_t total = 0;
+};
+
+ForwardPlan plan_forward(const vb_linear_fwd& p) {
+  ForwardPlan f;
+  Product& d = f.d;
+  d.a = p.x, d.lda = p.ld_x;
+  d.b = p.weight, d.ldb = p.ld_w;
+  d.M = p.rows, d.N = p.n_out, d.K = p.n_in;
+  d.bias = p.bias, d.res = p.residual, d.ld_res = p.ld_res;
+  d.out = p.y, d.ld_out = p.ld_y, d.pre = p.pre, d.ld_pre = p.ld_pre, d.act = p.act;
+  if (p.rows == 0 || product_is_narrow(d)) return f;
+  const size_t row = chunked_row(p.n_in, p.dtype);
+  if (!is_chunked(p.x, p.ld_x, p.n_in, p.dtype)) f.x.take(f.total, p.rows * row);
+  if (!is_chunked(p.weight, p.ld_w, p.n_in, p.dtype)) f.w.take(f.total, p.n_out * row);
+  f.partial.take(f.total, product_bytes(d, p.dtype));
+  return f;
+}
+
+// The backward products.  g is dy itself without an activation, else (or if dy's rows
+// cannot be read by a large product) a copy.
+struct BackwardPlan {
+  Product dx{}, dw{};
+  Part g, x, w, sums, partial;
+  size_t total = 0;
+};
+
+BackwardPlan plan_backward(const vb_linear_bwd& p) {
+  BackwardPlan f;
+  if (p.rows == 0) return f;
+  const int dt = p.dtype;
+  Product& a = f.dx;
+  a.lda = p.ld_dy, a.a = p.dy;
+  a.b = p.weight, a.ldb = p.ld_w, a.across_b = true;
+  a.M = p.rows, a.N = p.n_in, a.K = p.n_out;
+  a.out = p.dx, a.ld_out = p.ld_dx;
+  Product& b = f.dw;
+  b.a = p.dy, b.lda = p.ld_dy, b.across_a = true;
+  b.b = p.x, b.ldb = p.ld_x, b.across_b = true;
+  b.M = p.n_out, b.N = p.n_in, b.K = p.rows;
+  b.out = p.dweight, b.ld_out = p.ld_dw;
+  if ((p.dx || p.dweight) && (p.act != VB_ACT_NONE || !is_chunked(p.dy, p.ld_dy, p.n_out, dt)))
+    f.g.take(f.total, p.rows * chunked_row(p.n_out, dt));
+  const size_t row = chunked_row(p.n_in, dt);
+  if (p.dweight && !is_chunked(p.x, p.ld_x, p.n_in, dt)) f.x.take(f.total, p.rows * row);
+  if (p.dx && !is_chunked(p.weight, p.ld_w, p.n_in, dt)) f.w.take(f.total, p.n_out * row);
+  if (p.dbias) f.sums.take(f.total, act_grad_bytes(p.rows, p.n_out));
+  size_t parts = 0;  // the products run one after the other
+  if (p.dx) parts = product_bytes(a, dt);
+  if (p.dweight) {
+    const size_t q = product_bytes(b, dt);
+    if (q > parts) parts = q;
+  }
+  f.partial.take(f.total, parts);
+  return f;
+}
+
+}  // namespace
+
+extern "C" vb_status vb_linear_forward_workspace(const vb_linear_fwd* p, size_t* bytes) {
+  const char* fn = "vb_linear_forward_workspace";
+  if (!p || !bytes) return fail(VB_EINVAL, "%s: NULL argument", fn);
+  TRY(check_sizes(fn, p->rows, p->n_in, p->n_out, p->dtype));
+  *bytes = plan_forward(*p).total;
+  return VB_OK;
+}
+
+extern "C" vb_status vb_linear_backward_workspace(const vb_linear_bwd* p, size_t* bytes) {
+  const char* fn = "vb_linear_backward_workspace";
+  if (!p || !bytes) return fail(VB_EINVAL, "%s: NULL argument", fn);
+  TRY(check_sizes(fn, p->rows, p->n_in, p->n_out, p->dtype));
+  *bytes = plan_backward(*p).total;
   return VB_OK;
 }
 
@@ -83,16 +173,20 @@ extern "C" vb_status vb_linear_forward(const vb_linear_fwd* p, void* ws, size_t 
   TRY(check_matrix(fn, "y", p->y, p->ld_y, p->n_out, p->dtype, true));
   TRY(check_matrix(fn, "pre", p->pre, p->ld_pre, p->n_out, p->dtype, false));
   if (p->residual == p->y && p->ld_res != p->ld_y) return fail(VB_ESHAPE, "%s: y over residual needs the same leading dimension", fn);
-  size_t need = 0;
-  TRY(vb_linear_workspace(p->rows, p->n_in, p->n_out, p->dtype, 0, &need));
-  TRY(check_ws(fn, ws, ws_bytes, need));
-  Product d{};
-  d.a = p->x, d.sam = p->ld_x, d.sak = 1;
-  d.b = p->weight, d.sbn = p->ld_w, d.sbk = 1;
-  d.M = p->rows, d.N = p->n_out, d.K = p->n_in;
-  d.bias = p->bias, d.res = p->residual, d.ld_res = p->ld_res;
-  d.out = p->y, d.ld_out = p->ld_y, d.pre = p->pre, d.ld_pre = p->ld_pre, d.act = p->act;
-  HIPCHK(launch_product(d, p->dtype, (hipStream_t)stream));
+  ForwardPlan f = plan_forward(*p);
+  TRY(check_ws(fn, ws, ws_bytes, f.total));
+  const hipStream_t st = (hipStream_t)stream;
+  const long long ld = (long long)(chunked_row(p->n_in, p->dtype) / elem_size(p->dtype));
+  if (f.x.used) {
+    HIPCHK(launch_pack(p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws), p->dtype, st));
+    f.d.a = f.x.in(ws), f.d.lda = ld;
+  }
+  if (f.w.used) {
+    HIPCHK(launch_pack(p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws), p->dtype, st));
+    f.d.b = f.w.in(ws), f.d.ldb = ld;
+  }
+  f.d.partial = (float*)f.partial.in(ws);
+  HIPCHK(launch_product(f.d, p->dtype, st));
   return VB_OK;
 }
 
@@ -114,51 +208,48 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
   if (p->dresidual == p->dy && p->dy && p->ld_dres != p->ld_dy)
     return fail(VB_ESHAPE, "%s: dresidual over dy needs the same leading dimension", fn);
   const hipStream_t st = (hipStream_t)stream;
-  const size_t es = elem_size(p->dtype);
+  const long long es = (long long)elem_size(p->dtype);
   if (!some) {
-    if (p->dweight) HIPCHK(launch_fill_zero(p->dweight, p->n_out, p->n_in * (long long)es, p->ld_dw * es, st));
-    if (p->dbias) HIPCHK(launch_fill_zero(p->dbias, 1, p->n_out * (long long)es, p->n_out * (long long)es, st));
+    if (p->dweight) HIPCHK(launch_fill_zero(p->dweight, p->n_out, p->n_in * es, p->ld_dw * es, st));
+    if (p->dbias) HIPCHK(launch_fill_zero(p->dbias, 1, p->n_out * es, p->n_out * es, st));
     return VB_OK;
   }
-  size_t need = 0;
-  TRY(vb_linear_workspace(p->rows, p->n_in, p->n_out, p->dtype, 1, &need));
-  TRY(check_ws(fn, ws, ws_bytes, need));
-  const bool products = p->dx || p->dweight;
-  const bool own_g = products && p->act != VB_ACT_NONE;
-  if (own_g || p->dbias || p->dresidual) {
+  BackwardPlan f = plan_backward(*p);
+  TRY(check_ws(fn, ws, ws_bytes, f.total));
+  if (f.g.used || p->dbias || p->dresidual) {
     ActGrad g{};
     g.dy = p->dy, g.ld_dy = p->ld_dy;
     g.saved = p->act == VB_ACT_NONE ? nullptr : p->saved, g.ld_saved = p->ld_saved;
-    g.g = own_g ? ws : nullptr, g.ld_g = p->n_out;
+    g.g = f.g.in(ws), g.ld_g = (long long)chunked_row(p->n_out, p->dtype) / es;
     g.dres = p->dresidual, g.ld_dres = p->ld_dres;
-    g.dbias = p->dbias;
+    g.dbias = p->dbias, g.partial = (float*)f.sums.in(ws);
     g.rows = p->rows, g.n = p->n_out, g.act = p->act;
     HIPCHK(launch_act_grad(g, p->dtype, st));
+    if (f.g.used) f.dx.a = f.dw.a = g.g, f.dx.lda = f.dw.lda = g.ld_g;
   }
-  const void* g = own_g ? ws : p->dy;
-  const int64_t ld_g = own_g ? p->n_out : p->ld_dy;
+  const long long ld = (long long)chunked_row(p->n_in, p->dtype) / es;
   if (p->dx) {
-    Product d{};
-    d.a = g, d.sam = ld_g, d.sak = 1;
-    d.b = p->weight, d.sbn = 1, d.sbk = p->ld_w;
-    d.M = p->rows, d.N = p->n_in, d.K = p->n_out;
-    d.out = p->dx, d.ld_out = p->ld_dx;
-    HIPCHK(launch_product(d, p->dtype, st));
+    if (f.w.used) {
+      HIPCHK(launch_pack(p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws), p->dtype, st));
+      f.dx.b = f.w.in(ws), f.dx.ldb = ld;
+    }
+    f.dx.partial = (float*)f.partial.in(ws);
+    HIPCHK(launch_product(f.dx, p->dtype, st));
   }
   if (p->dweight) {
-    Product d{};
-    d.a = g, d.sam = 1, d.sak = ld_g;
-    d.b = p->x, d.sbn = 1, d.sbk = p->ld_x;
-    d.M = p->n_out, d.N = p->n_in, d.K = p->rows;
-    d.out = p->dweight, d.ld_out = p->ld_dw;
-    HIPCHK(launch_product(d, p->dtype, st));
+    if (f.x.used) {
+      HIPCHK(launch_pack(p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws), p->dtype, st));
+      f.dw.b = f.x.in(ws), f.dw.ldb = ld;
+    }
+    f.dw.partial = (float*)f.partial.in(ws);
+    HIPCHK(launch_product(f.dw, p->dtype, st));
   }
   return VB_OK;
 }
 
 extern "C" vb_status vb_cross_entropy_workspace(int64_t rows, int32_t classes, int32_t dtype, size_t* bytes) {
   if (!bytes) return fail(VB_EINVAL, "vb_cross_entropy_workspace: bytes is NULL");
-  TRY(check_sizes("vb_cross_entropy_workspace", rows, classes, classes, dtype));
+  TRY(check_sizes("vb_cross_entropy_workspace", rows, classes, classes, dtype, MAX_CLASSES));
   *bytes = align_up(16 + (size_t)rows * 4);
   return VB_OK;
 }
@@ -166,7 +257,7 @@ extern "C" vb_status vb_cross_entropy_workspace(int64_t rows, int32_t classes, i
 extern "C" vb_status vb_cross_entropy(const vb_cross_entropy_args* p, void* ws, size_t ws_bytes, void* stream) {
   const char* fn = "vb_cross_entropy";
   if (!p) return fail(VB_EINVAL, "%s: NULL argument", fn);
-  TRY(check_sizes(fn, p->rows, p->classes, p->classes, p->dtype));
+  TRY(check_sizes(fn, p->rows, p->classes, p->classes, p->dtype, MAX_CLASSES));
   const bool some = p->rows > 0;
   TRY(check_matrix(fn, "logits", p->logits, p->ld, p->classes, p->dtype, some));
   TRY(check_matrix(fn, "dlogits", p->dlogits, p->ld_d, p->classes, p->dtype, false));

@@ -15,12 +15,15 @@ vb_status set_error(vb_status s, const char* msg) noexcept;
 
 inline size_t elem_size(int dtype) { return dtype == VB_F32 ? 4 : 2; }
 
-// C[m][n] = sum_k A(m, k) B(n, k), with A(m, k) = a[m * sam + k * sak] and
-// B(n, k) = b[n * sbn + k * sbk] (one stride of each operand is 1).
+// C(m, n) = sum_k A(m, k) B(n, k) with A(m, k) = a[m * lda + k], or a[k * lda + m] when
+// across_a (likewise b); across_a implies across_b.  With more than 32 rows, or an
+// operand stored across, both operands are chunked (is_chunked over their rows as
+// stored; a row along the reduction may also be one that launch_pack filled with zeros).
 struct Product {
   const void* a;
   const void* b;
-  long long sam, sak, sbn, sbk;
+  long long lda, ldb;
+  bool across_a, across_b;
   long long M;
   int N;
   long long K;
@@ -33,11 +36,29 @@ struct Product {
   void* pre;
   long long ld_pre;
   int act;
+  // workspace of product_bytes: float32 parts of a reduction split over workgroups
+  float* partial;
+  // set by launch_product
+  int ld_partial, split_stages;
 };
+struct Tiling {
+  int bm, bn, splits;
+};
+bool product_is_narrow(const Product& p);
+size_t product_bytes(const Product& p, int dtype);
 hipError_t launch_product(const Product& p, int dtype, hipStream_t st);
 
-// g = dy * act'(saved) -> g and dres (each optional), and the column sums of the
-// unrounded g -> dbias (optional).
+// Rows of n elements that start on 16-byte boundaries, end on one, and are near enough
+// for 32-bit offsets within a tile.
+constexpr long long MAX_CHUNKED_ROW = 1 << 22;
+bool is_chunked(const void* p, long long ld, long long n, int dtype);
+// Bytes of a row of n elements rounded up to 16.
+inline size_t chunked_row(long long n, int dtype) { return (n * elem_size(dtype) + 15) / 16 * 16; }
+hipError_t launch_pack(const void* src, long long ld, long long rows, int n, void* dst, int dtype, hipStream_t st);
+
+// v = dy * act'(saved), in float32: g = v (rows of ld_g elements that start on 16-byte
+// boundaries, zeros to the end of the last chunk), dres = v, dbias = column sums of v;
+// each optional.  partial: act_grad_bytes of workspace for dbias.
 struct ActGrad {
   const void* dy;
   const void* saved;
@@ -47,10 +68,12 @@ struct ActGrad {
   void* dres;
   long long ld_dres;
   void* dbias;
+  float* partial;
   long long rows;
   int n;
   int act;
 };
+size_t act_grad_bytes(long long rows, int n);
 hipError_t launch_act_grad(const ActGrad& p, int dtype, hipStream_t st);
 hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long long ld_bytes, hipStream_t st);
 

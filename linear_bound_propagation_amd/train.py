@@ -16,8 +16,8 @@ import torch
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
-EXPORTS = ["vb_linear_workspace", "vb_linear_forward", "vb_linear_backward", "vb_cross_entropy_workspace",
-           "vb_cross_entropy", "vb_clip_grad_norm_workspace", "vb_clip_grad_norm"]
+EXPORTS = ["vb_linear_forward_workspace", "vb_linear_backward_workspace", "vb_linear_forward",
+           "vb_linear_backward", "vb_cross_entropy_workspace", "vb_cross_entropy", "vb_clip_grad_norm_workspace", "vb_clip_grad_norm"]
 
 _P, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 
@@ -44,7 +44,8 @@ class vb_cross_entropy_args(ctypes.Structure):
 def declare(lib: ctypes.CDLL) -> None:
     """Argument types of the calls of vb_train.h."""
     psz = ctypes.POINTER(_sz)
-    for name, args in (("vb_linear_workspace", [_i64, _i32, _i32, _i32, _i32, psz]),
+    for name, args in (("vb_linear_forward_workspace", [ctypes.POINTER(vb_linear_fwd), psz]),
+                       ("vb_linear_backward_workspace", [ctypes.POINTER(vb_linear_bwd), psz]),
                        ("vb_linear_forward", [ctypes.POINTER(vb_linear_fwd), _P, _sz, _P]),
                        ("vb_linear_backward", [ctypes.POINTER(vb_linear_bwd), _P, _sz, _P]),
                        ("vb_cross_entropy_workspace", [_i64, _i32, _i32, psz]),
@@ -96,24 +97,34 @@ def _bytes(n: int, device) -> Optional[torch.Tensor]:
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
-def _workspace(ws: Optional[torch.Tensor], need, device):
-    """(pointer, bytes, tensor): the caller's workspace, or a new one of need() bytes."""
+def _workspace(ws: Optional[torch.Tensor], need: int, device):
+    """(pointer, bytes, tensor): the caller's workspace, or a new one of `need` bytes."""
     if ws is None:
-        ws = _bytes(need(), device)
+        ws = _bytes(need, device)
     return (None, 0, None) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size(), ws)
 
 
-def _linear_bytes(rows, n_in, n_out, dtype, backward) -> int:
+def _size(fn: str, *args) -> int:
     pkg = _pkg()
     out = _sz(0)
-    pkg._check(pkg.lib().vb_linear_workspace(rows, n_in, n_out, dtype, int(backward), ctypes.byref(out)),
-               "vb_linear_workspace")
+    pkg._check(getattr(pkg.lib(), fn)(*args, ctypes.byref(out)), fn)
     return out.value
 
 
 def linear_workspace(x: torch.Tensor, weight: torch.Tensor, backward: bool = False) -> torch.Tensor:
-    """A workspace for `linear` (or `linear_backward`) calls of these sizes, to keep between calls."""
-    n = _linear_bytes(x.shape[0], x.shape[1], weight.shape[0], _dtype(x), backward)
+    """A workspace for `linear` calls (or `linear_backward` calls, with any activation and all
+    gradients) on tensors of these sizes and strides, to keep between calls."""
+    _device(x)
+    rows, n_in = x.shape
+    n_out = weight.shape[0]
+    ld_x, ld_w = _matrix("x", x, rows, n_in, x), _matrix("weight", weight, n_out, n_in, x)
+    if backward:
+        p = vb_linear_bwd(rows, n_in, n_out, _dtype(x), ACTS["silu"], None, n_out, x.data_ptr(), ld_x,
+                          weight.data_ptr(), ld_w, None, n_out, 16, n_in, 16, n_in, 16, 16, n_out)
+        n = _size("vb_linear_backward_workspace", ctypes.byref(p))
+    else:
+        p = vb_linear_fwd(rows, n_in, n_out, _dtype(x), 0, x.data_ptr(), ld_x, weight.data_ptr(), ld_w)
+        n = _size("vb_linear_forward_workspace", ctypes.byref(p))
     return torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
 
 
@@ -141,10 +152,10 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     y = torch.empty(rows, n_out, dtype=x.dtype, device=x.device) if out is None else out
     ld_y = n_out if out is None else _matrix("out", out, rows, n_out, x)
     pre = torch.empty(rows, n_out, dtype=x.dtype, device=x.device) if want_pre else None
-    wp, wn, keep = _workspace(ws, lambda: _linear_bytes(rows, n_in, n_out, dt, 0), x.device)
     p = vb_linear_fwd(rows, n_in, n_out, dt, ACTS[act], x.data_ptr(), ld_x, weight.data_ptr(), ld_w,
                       None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
                       ld_res, y.data_ptr(), ld_y, None if pre is None else pre.data_ptr(), n_out)
+    wp, wn, keep = _workspace(ws, _size("vb_linear_forward_workspace", ctypes.byref(p)) if ws is None else 0, x.device)
     pkg._check(pkg.lib().vb_linear_forward(ctypes.byref(p), wp, wn, pkg._stream()), "vb_linear_forward")
     return (y, pre) if want_pre else y
 
@@ -175,26 +186,18 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act
 
     dx, dw, db, dr = (new(want_x, rows, n_in), new(want_weight, n_out, n_in), new(want_bias, n_out),
                       new(want_residual, rows, n_out))
-    wp, wn, keep = _workspace(ws, lambda: _linear_bytes(rows, n_in, n_out, dt, 1), x.device)
     p = vb_linear_bwd(rows, n_in, n_out, dt, ACTS[act], dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, weight.data_ptr(),
                       ld_w, None if saved is None else saved.data_ptr(), ld_s, None if dx is None else dx.data_ptr(),
                       n_in, None if dw is None else dw.data_ptr(), n_in, None if db is None else db.data_ptr(),
                       None if dr is None else dr.data_ptr(), n_out)
+    wp, wn, keep = _workspace(ws, _size("vb_linear_backward_workspace", ctypes.byref(p)) if ws is None else 0, x.device)
     pkg._check(pkg.lib().vb_linear_backward(ctypes.byref(p), wp, wn, pkg._stream()), "vb_linear_backward")
     return dx, dw, db, dr
 
 
-def _loss_bytes(rows, classes, dtype) -> int:
-    pkg = _pkg()
-    out = _sz(0)
-    pkg._check(pkg.lib().vb_cross_entropy_workspace(rows, classes, dtype, ctypes.byref(out)),
-               "vb_cross_entropy_workspace")
-    return out.value
-
-
 def cross_entropy_workspace(logits: torch.Tensor) -> torch.Tensor:
     """A workspace for `cross_entropy` calls of these sizes, to keep between calls."""
-    return _bytes(_loss_bytes(logits.shape[0], logits.shape[1], _dtype(logits)), logits.device)
+    return _bytes(_size("vb_cross_entropy_workspace", logits.shape[0], logits.shape[1], _dtype(logits)), logits.device)
 
 
 def cross_entropy(logits: torch.Tensor, labels: torch.Tensor, ignore_index: int = -100,
@@ -222,7 +225,8 @@ def cross_entropy(logits: torch.Tensor, labels: torch.Tensor, ignore_index: int 
         ld_d = _matrix("dlogits", dlogits, rows, classes, logits)
     both = torch.empty(rows + 1, dtype=torch.float32, device=logits.device)
     base = both.data_ptr()
-    wp, wn, keep = _workspace(ws, lambda: _loss_bytes(rows, classes, dt), logits.device)
+    wp, wn, keep = _workspace(ws, _size("vb_cross_entropy_workspace", rows, classes, dt) if ws is None else 0,
+                              logits.device)
     p = vb_cross_entropy_args(rows, classes, dt, logits.data_ptr(), ld, labels.data_ptr(), ignore_index,
                               label_smoothing, grad_scale, base + 4 * rows, base,
                               None if dlogits is None else dlogits.data_ptr(), ld_d)
@@ -235,16 +239,9 @@ def _clip_arrays(grads: Sequence[torch.Tensor]):
     return n, (_i64 * max(n, 1))(*[g.numel() for g in grads])
 
 
-def _clip_bytes(n, sizes) -> int:
-    pkg = _pkg()
-    out = _sz(0)
-    pkg._check(pkg.lib().vb_clip_grad_norm_workspace(n, sizes, ctypes.byref(out)), "vb_clip_grad_norm_workspace")
-    return out.value
-
-
 def clip_grad_norm_workspace(grads: Sequence[torch.Tensor]) -> torch.Tensor:
     """A workspace for `clip_grad_norm` calls on tensors of these sizes, to keep between calls."""
-    return _bytes(_clip_bytes(*_clip_arrays(grads)), grads[0].device if grads else "cuda")
+    return _bytes(_size("vb_clip_grad_norm_workspace", *_clip_arrays(grads)), grads[0].device if grads else "cuda")
 
 
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
@@ -270,7 +267,7 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     src = (_P * max(n, 1))(*[g.data_ptr() for g in grads])
     dst = None if out is None else (_P * max(n, 1))(*[o.data_ptr() for o in out])
     norm = torch.empty(1, dtype=torch.float32, device=dev)
-    wp, wn, keep = _workspace(ws, lambda: _clip_bytes(n, sizes), dev)
+    wp, wn, keep = _workspace(ws, _size("vb_clip_grad_norm_workspace", n, sizes) if ws is None else 0, dev)
     pkg._check(pkg.lib().vb_clip_grad_norm(n, src, dst, sizes, dts, max_norm, norm.data_ptr(), wp, wn, pkg._stream()),
                "vb_clip_grad_norm")
     return norm, list(grads if out is None else out)

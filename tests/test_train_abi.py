@@ -35,7 +35,7 @@ def test_linear_forward_refusals():
     assert L.vb_linear_forward(None, None, 0, None) == EINVAL
     for kw, want, text in (
             (dict(rows=-1), EINVAL, "rows"), (dict(rows=2 ** 31), EINVAL, "rows"), (dict(n_in=0), EINVAL, "sizes"),
-            (dict(n_out=-3), EINVAL, "sizes"), (dict(dtype=3), EINVAL, "dtype"), (dict(dtype=-1), EINVAL, "dtype"),
+            (dict(n_out=-3), EINVAL, "sizes"), (dict(n_in=2 ** 20 + 1), -5, "not supported"), (dict(dtype=3), EINVAL, "dtype"), (dict(dtype=-1), EINVAL, "dtype"),
             (dict(act=4), EINVAL, "activation"), (dict(x=None), EINVAL, "x is NULL"),
             (dict(weight=None), EINVAL, "weight is NULL"), (dict(y=None), EINVAL, "y is NULL"),
             (dict(x=4098), EINVAL, "aligned"), (dict(dtype=1, bias=4097), EINVAL, "bias is not aligned"),
@@ -75,13 +75,28 @@ def test_linear_backward_refusals():
 
 
 def test_linear_workspace():
-    assert size(L.vb_linear_workspace, 8, 12, 10, 0, 1)[0] == 0
-    assert size(L.vb_linear_workspace, 0, 12, 10, 0, 1)[0] == 0
-    assert L.vb_linear_workspace(8, 12, 10, 0, 1, None) == EINVAL
-    assert size(L.vb_linear_workspace, -8, 12, 10, 0, 1)[0] == EINVAL
-    assert size(L.vb_linear_workspace, 8, 12, 10, 9, 1)[0] == EINVAL
-    st, n = size(L.vb_linear_workspace, 2 ** 31 - 1, 8192, 16384, 1, 1)     # no 32-bit overflow
-    assert st == 0 and n >= (2 ** 31 - 1) * 16384 * 2
+    def need(fn, cls, **kw):
+        d = dict(rows=100, n_in=64, n_out=40, dtype=0, act=1, x=4096, ld_x=64, weight=8192, ld_w=64)
+        if cls is train.vb_linear_bwd:
+            d.update(dy=4096, ld_dy=40, dx=16, dweight=16, dbias=16)
+        d.update(kw)
+        return size(fn, ctypes.byref(cls(**d)))
+
+    fwd, bwd = (L.vb_linear_forward_workspace, train.vb_linear_fwd), (L.vb_linear_backward_workspace, train.vb_linear_bwd)
+    for fn, cls in (fwd, bwd):
+        assert need(fn, cls)[0] == 0 and need(fn, cls, rows=0) == (0, 0)
+        assert fn(None, ctypes.byref(ctypes.c_size_t(0))) == EINVAL
+        assert fn(ctypes.byref(cls(rows=1, n_in=1, n_out=1)), None) == EINVAL
+        assert need(fn, cls, rows=-8)[0] == EINVAL and need(fn, cls, dtype=9)[0] == EINVAL
+        assert need(fn, cls, n_in=2 ** 20 + 1)[0] == -5
+        # rows that a large product cannot read are copied
+        base = need(fn, cls)[1]
+        assert need(fn, cls, x=4100)[1] >= base + 100 * 64 * 4
+        assert need(fn, cls, ld_w=65)[1] >= base + 40 * 64 * 4
+        assert need(fn, cls, n_in=63)[1] >= base
+    assert need(*fwd, rows=5, x=4100)[1] == 0          # few rows: no copy
+    st, n = need(*bwd, rows=2 ** 31 - 1, n_in=8192, n_out=16384, dtype=1, ld_x=8192, ld_w=8192, ld_dy=16384)
+    assert st == 0 and n >= (2 ** 31 - 1) * 16384 * 2   # no 32-bit overflow
 
 
 def loss(ws=65536, ws_bytes=1 << 20, **kw):
