@@ -177,53 +177,89 @@ __device__ __forceinline__ float one_row(const vb_cross_entropy_args& p, long lo
 // thread rescales its sum when its maximum grows), the gradient in a second.
 template <typename T>
 __device__ __forceinline__ float one_row_twice(const vb_cross_entropy_args& p, long long r, float scale, float* red) {
-  constexpr int TH = 1024, U = 8;
+  typedef typename Vec<T>::type V;
+  typedef typename Vec<T>::loose LV;
+  constexpr int TH = 1024, U = 4, EC = Vec<T>::EC;
   const T* z = (const T*)p.logits + r * p.ld;
   T* d = p.dlogits ? (T*)p.dlogits + r * p.ld_d : nullptr;
   const int n = p.classes, tid = threadIdx.x;
+  const int lead = (int)((uintptr_t)z % 16 / sizeof(T)), chunks = (lead + n + EC - 1) / EC;
   const int64_t t = p.labels[r];
-  if (t == p.ignore_index) {
-    if (d)
-      for (int i = tid; i < n; i += TH) d[i] = (T)0.f;
-    return 0.f;
-  }
-  const bool bad = t < 0 || t >= n;
+  const bool ignored = t == p.ignore_index, bad = t < 0 || t >= n;
+  if (ignored && !d) return 0.f;
   const float zt = bad ? NAN : to_f32(z[t]);
   const float eps = p.label_smoothing, rn = 1.f / (float)n;
+  auto chunk = [&](int c) {
+    const int i0 = c * EC - lead;
+    V v;
+    if (c < chunks && i0 >= 0 && i0 + EC <= n) {
+      v = *(const V*)(z + i0);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EC; ++e) v[e] = i0 + e >= 0 && i0 + e < n ? z[i0 + e] : (T)(-INFINITY);
+    }
+    return v;
+  };
   // The running maximum starts at the lowest finite number: a thread without a finite
   // logit then holds a sum of zeros (or NaN from +inf or NaN), not -inf minus -inf.
   constexpr float LOW = -3.402823466e38f;
   float top = LOW, sum = 0.f, mean = 0.f;
-  for (long long i0 = tid; i0 < n; i0 += U * TH) {
-    float v[U];
+  if (!ignored) {
+    for (int c = tid; c < chunks; c += U * TH) {
+      V v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = i0 + u * TH < n ? to_f32(z[i0 + u * TH]) : -INFINITY;
-    float m = top;
+      for (int u = 0; u < U; ++u) v[u] = chunk(c + u * TH);
+      float m = top;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      m = fmaxf(m, v[u]);
-      if (i0 + u * TH < n) mean += v[u] * rn;
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < EC; ++e) m = fmaxf(m, to_f32((T)v[u][e]));
+      sum *= exp_of<T>(top - m);
+      top = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < EC; ++e) {
+          const float x = to_f32((T)v[u][e]);
+          const int i = (c + u * TH) * EC - lead + e;
+          sum += exp_of<T>(x - m);
+          if (eps > 0.f && i >= 0 && i < n) mean += x * rn;
+        }
     }
-    sum *= exp_of<T>(top - m);
-#pragma unroll
-    for (int u = 0; u < U; ++u) sum += exp_of<T>(v[u] - m);
-    top = m;
+    const float all = over_row<Maximum, TH>(top, red);
+    sum = over_row<Sum, TH>(sum * exp_of<T>(top - all), red);
+    if (sum == 0.f) sum = NAN;  // no finite logit at all: 0 / 0, as the formula
+    top = all;
   }
-  const float all = over_row<Maximum, TH>(top, red);
-  sum = over_row<Sum, TH>(sum * exp_of<T>(top - all), red);
-  // no finite logit at all: 0 / 0, as the formula
-  if (sum == 0.f) sum = NAN;
-  top = all;
   const float lse = logf(sum);
   float loss = (1.f - eps) * (lse + (top - zt));
   if (eps > 0.f) loss += eps * (lse + (top - over_row<Sum, TH>(mean, red)));
+  if (ignored) loss = 0.f;
   if (!d) return loss;
   const float s = bad ? NAN : scale, inv = 1.f / sum, off = eps / (float)n;
-#pragma unroll 8
-  for (int i = tid; i < n; i += TH) {
-    float g = exp_of<T>(to_f32(z[i]) - top) * inv - off;
-    if (i == t) g -= 1.f - eps;
-    d[i] = from_f32<T>(g * s);
+  for (int c = tid; c < chunks; c += U * TH) {
+    V v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = chunk(c + u * TH);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i0 = (c + u * TH) * EC - lead;
+      if (i0 >= n) break;
+      V o;
+#pragma unroll
+      for (int e = 0; e < EC; ++e) {
+        float g = exp_of<T>(to_f32((T)v[u][e]) - top) * inv - off;
+        if (i0 + e == t) g -= 1.f - eps;
+        o[e] = ignored ? (T)0.f : from_f32<T>(g * s);
+      }
+      if (i0 >= 0 && i0 + EC <= n) {
+        *(LV*)(d + i0) = o;
+      } else {
+#pragma unroll
+        for (int e = 0; e < EC; ++e)
+          if (i0 + e >= 0 && i0 + e < n) d[i0 + e] = o[e];
+      }
+    }
   }
   return loss;
 }
@@ -270,8 +306,10 @@ __global__ __launch_bounds__(1024) void loss_mean_kernel(const float* row_loss, 
   mean_loss(row_loss, rows, *count, loss);
 }
 
+// Rows of up to 128 KB leave registers for two rows per CU at a time, so that one loads
+// while the other computes.
 template <typename T, int TH, int CH>
-__global__ __launch_bounds__(TH < 256 ? 256 : TH) void loss_rows_kernel(vb_cross_entropy_args p,
+__global__ __launch_bounds__(TH < 256 ? 256 : TH, CH <= 8 ? 8 : 4) void loss_rows_kernel(vb_cross_entropy_args p,
                                                                         const long long* count, float* row_loss) {
   __shared__ float red[16];
   constexpr int PER = TH < 256 ? 256 / TH : 1;
@@ -317,6 +355,8 @@ hipError_t launch_typed(const vb_cross_entropy_args& p, void* ws, hipStream_t st
     else if (chunks <= 2048) loss_rows_kernel<T, 256, 8><<<rows, 256, 0, st>>>(p, count, row_loss);
     else if (chunks <= 4096) loss_rows_kernel<T, 1024, 4><<<rows, 1024, 0, st>>>(p, count, row_loss);
     else if (chunks <= 8192) loss_rows_kernel<T, 1024, 8><<<rows, 1024, 0, st>>>(p, count, row_loss);
+    else if (chunks <= 10240) loss_rows_kernel<T, 1024, 10><<<rows, 1024, 0, st>>>(p, count, row_loss);
+    else if (chunks <= 12288) loss_rows_kernel<T, 1024, 12><<<rows, 1024, 0, st>>>(p, count, row_loss);
     else if (chunks <= 16384) loss_rows_kernel<T, 1024, 16><<<rows, 1024, 0, st>>>(p, count, row_loss);
     else loss_rows_kernel<T, 1024, 0><<<rows, 1024, 0, st>>>(p, count, row_loss);
   }

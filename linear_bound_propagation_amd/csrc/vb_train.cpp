@@ -319,34 +319,40 @@ extern "C" vb_status vb_clip_grad_norm(int32_t n_tensors, const void* const* gra
   }
   TRY(check_ws(fn, ws, ws_bytes, need));
   const hipStream_t st = (hipStream_t)stream;
+  // the next tensors, from number i on, in chunks of `chunk`
+  int32_t i = 0;
+  auto fill = [&](ClipTable& t, int chunk) {
+    t.count = 0;
+    t.chunk = chunk;
+    t.first[0] = 0;
+    for (; i < n_tensors && t.count < CLIP_TENSORS; ++i) {
+      if (sizes[i] == 0) continue;
+      const int c = t.count++;
+      t.grad[c] = grads[i];
+      t.out[c] = out ? out[i] : (void*)grads[i];
+      t.n[c] = sizes[i];
+      t.dtype[c] = (unsigned char)dtypes[i];
+      t.first[c + 1] = t.first[c] + (unsigned)((sizes[i] + chunk - 1) / chunk);
+    }
+    return t.count > 0;
+  };
+  ClipTable t;
+  long long total = 0;
+  for (int32_t k = 0; k < n_tensors; ++k) total += sizes[k];
+  if (total <= CLIP_SMALL && n_tensors <= CLIP_TENSORS) {
+    fill(t, CLIP_SMALL_CHUNK);
+    HIPCHK(launch_clip_small(t, max_norm, norm, st));
+    return VB_OK;
+  }
   float* scale = (float*)ws;
   double* partial = (double*)((char*)ws + 16);
-  long long blocks = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long at = 0;
-    int32_t i = 0;
-    while (i < n_tensors) {
-      ClipTable t;
-      t.count = 0;
-      t.first[0] = 0;
-      for (; i < n_tensors && t.count < CLIP_TENSORS; ++i) {
-        if (sizes[i] == 0) continue;
-        const int c = t.count++;
-        t.grad[c] = grads[i];
-        t.out[c] = out ? out[i] : (void*)grads[i];
-        t.n[c] = sizes[i];
-        t.dtype[c] = (unsigned char)dtypes[i];
-        t.first[c + 1] = t.first[c] + (unsigned)((sizes[i] + CLIP_CHUNK - 1) / CLIP_CHUNK);
-      }
-      if (!t.count) break;
-      if (pass == 0) HIPCHK(launch_clip_partial(t, partial + at, st));
-      else HIPCHK(launch_clip_scale(t, scale, st));
-      at += t.first[t.count];
-    }
-    if (pass == 0) {
-      blocks = at;
-      HIPCHK(launch_clip_norm(partial, blocks, max_norm, norm, scale, st));
-    }
+  long long at = 0;
+  while (fill(t, CLIP_CHUNK)) {
+    HIPCHK(launch_clip_partial(t, partial + at, st));
+    at += t.first[t.count];
   }
+  HIPCHK(launch_clip_norm(partial, at, max_norm, norm, scale, st));
+  i = 0;
+  while (fill(t, CLIP_CHUNK)) HIPCHK(launch_clip_scale(t, scale, st));
   return VB_OK;
 }

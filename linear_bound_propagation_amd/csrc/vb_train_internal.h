@@ -80,20 +80,24 @@ hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long l
 // ws: one int64 (count of the rows that are not ignored)
 hipError_t launch_cross_entropy(const vb_cross_entropy_args& p, void* ws, hipStream_t st);
 
-// Gradient tensors in the kernels' argument block: CLIP_TENSORS of them at a time.
+// Gradient tensors in the kernels' argument block: CLIP_TENSORS of them at a time, cut
+// into chunks of `chunk` elements.
 constexpr int CLIP_TENSORS = 112;
-constexpr int CLIP_CHUNK = 16384;  // elements of one workgroup
+constexpr int CLIP_CHUNK = 16384;          // of a workgroup of 256
+constexpr int CLIP_SMALL_CHUNK = 2048;     // of a wavefront, when one workgroup does all:
+constexpr long long CLIP_SMALL = 160 * 1024;  // up to this many elements
 struct ClipTable {
   const void* grad[CLIP_TENSORS];
   void* out[CLIP_TENSORS];
   long long n[CLIP_TENSORS];
-  unsigned first[CLIP_TENSORS + 1];  // workgroups before tensor i of this launch
+  unsigned first[CLIP_TENSORS + 1];  // chunks before tensor i of this launch
   unsigned char dtype[CLIP_TENSORS];
-  int count;
+  int count, chunk;
 };
 hipError_t launch_clip_partial(const ClipTable& t, double* partial, hipStream_t st);
 hipError_t launch_clip_norm(const double* partial, long long n, float max_norm, float* norm, float* scale,
                             hipStream_t st);
 hipError_t launch_clip_scale(const ClipTable& t, const float* scale, hipStream_t st);
+hipError_t launch_clip_small(const ClipTable& t, float max_norm, float* norm, hipStream_t st);
 
 }  // namespace vb
