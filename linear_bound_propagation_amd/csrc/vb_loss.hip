@@ -237,6 +237,7 @@ __device__ __forceinline__ float one_row_twice(const vb_cross_entropy_args& p, l
   if (ignored) loss = 0.f;
   if (!d) return loss;
   const float s = bad ? NAN : scale, inv = 1.f / sum, off = eps / (float)n;
+  const int at = bad ? -1 - EC : (int)t;
   for (int c = tid; c < chunks; c += U * TH) {
     V v[U];
 #pragma unroll
@@ -249,7 +250,7 @@ __device__ __forceinline__ float one_row_twice(const vb_cross_entropy_args& p, l
 #pragma unroll
       for (int e = 0; e < EC; ++e) {
         float g = exp_of<T>(to_f32((T)v[u][e]) - top) * inv - off;
-        if (i0 + e == t) g -= 1.f - eps;
+        if (i0 + e == at) g -= 1.f - eps;
         o[e] = ignored ? (T)0.f : from_f32<T>(g * s);
       }
       if (i0 >= 0 && i0 + EC <= n) {

@@ -9,6 +9,8 @@ Matrices may have any row stride; elements of a row are contiguous.
 from __future__ import annotations
 
 import ctypes
+import struct
+from array import array
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -41,26 +43,52 @@ class vb_cross_entropy_args(ctypes.Structure):
                 ("row_loss", _P), ("dlogits", _P), ("ld_d", _i64)]
 
 
+_FWD = struct.Struct("qiiiiQqQqQQqQqQq")    # vb_linear_fwd
+_BWD = struct.Struct("qiiiiQqQqQqQqQqQqQQq")  # vb_linear_bwd
+_LOSS = struct.Struct("qiiQqQqffQQQq")      # vb_cross_entropy_args
+assert (_FWD.size, _BWD.size, _LOSS.size) == tuple(
+    ctypes.sizeof(c) for c in (vb_linear_fwd, vb_linear_bwd, vb_cross_entropy_args))
+
+_call = None    # the declared functions, by name
+
+
 def declare(lib: ctypes.CDLL) -> None:
-    """Argument types of the calls of vb_train.h."""
+    """Argument types of the calls of vb_train.h (argument blocks are passed by address)."""
     psz = ctypes.POINTER(_sz)
-    for name, args in (("vb_linear_forward_workspace", [ctypes.POINTER(vb_linear_fwd), psz]),
-                       ("vb_linear_backward_workspace", [ctypes.POINTER(vb_linear_bwd), psz]),
-                       ("vb_linear_forward", [ctypes.POINTER(vb_linear_fwd), _P, _sz, _P]),
-                       ("vb_linear_backward", [ctypes.POINTER(vb_linear_bwd), _P, _sz, _P]),
+    for name, args in (("vb_linear_forward_workspace", [_P, psz]),
+                       ("vb_linear_backward_workspace", [_P, psz]),
+                       ("vb_linear_forward", [_P, _P, _sz, _P]),
+                       ("vb_linear_backward", [_P, _P, _sz, _P]),
                        ("vb_cross_entropy_workspace", [_i64, _i32, _i32, psz]),
-                       ("vb_cross_entropy", [ctypes.POINTER(vb_cross_entropy_args), _P, _sz, _P]),
-                       ("vb_clip_grad_norm_workspace", [_i32, ctypes.POINTER(_i64), psz]),
-                       ("vb_clip_grad_norm", [_i32, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_i64),
-                                              ctypes.POINTER(_i32), _f32, _P, _P, _sz, _P])):
+                       ("vb_cross_entropy", [_P, _P, _sz, _P]),
+                       ("vb_clip_grad_norm_workspace", [_i32, _P, psz]),
+                       ("vb_clip_grad_norm", [_i32, _P, _P, _P, _P, _f32, _P, _P, _sz, _P])):
         fn = getattr(lib, name)
         fn.restype = _i32
         fn.argtypes = args
 
 
-def _pkg():
-    import linear_bound_propagation_amd as pkg
-    return pkg
+def _run(name: str, *args) -> None:
+    """Calls a library function; its status becomes an exception."""
+    global _call
+    if _call is None:
+        import linear_bound_propagation_amd as pkg
+        lib = pkg.lib()
+        _call = {n: getattr(lib, n) for n in EXPORTS}
+    status = _call[name](*args)
+    if status:
+        import linear_bound_propagation_amd as pkg
+        pkg._check(status, name)
+
+
+def _size(name: str, *args) -> int:
+    out = _sz(0)
+    _run(name, *args, ctypes.byref(out))
+    return out.value
+
+
+def _stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -70,45 +98,41 @@ def _dtype(t: torch.Tensor) -> int:
     return code
 
 
+def _device(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current GPU, got {t.device}")
+    return dev
+
+
 def _matrix(name: str, t: torch.Tensor, rows: int, cols: int, like: torch.Tensor) -> int:
     """Leading dimension of a [rows][cols] operand (checked against `like`'s type and device)."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}][{cols}], got {tuple(t.shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
+    if t.dtype is not like.dtype or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"the elements of a row of {name} must be contiguous")
-    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
+    return ld if rows > 1 else max(cols, ld)
 
 
 def _vector(name: str, t: torch.Tensor, n: int, like: torch.Tensor) -> None:
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{n}], got {tuple(t.shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
+    if t.dtype is not like.dtype or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
 
 
-def _device(t: torch.Tensor) -> None:
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current GPU, got {t.device}")
+def _act(act: str) -> int:
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    return code
 
 
-def _bytes(n: int, device) -> Optional[torch.Tensor]:
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
-
-
-def _workspace(ws: Optional[torch.Tensor], need: int, device):
-    """(pointer, bytes, tensor): the caller's workspace, or a new one of `need` bytes."""
-    if ws is None:
-        ws = _bytes(need, device)
-    return (None, 0, None) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size(), ws)
-
-
-def _size(fn: str, *args) -> int:
-    pkg = _pkg()
-    out = _sz(0)
-    pkg._check(getattr(pkg.lib(), fn)(*args, ctypes.byref(out)), fn)
-    return out.value
+def _workspace(n: int, device) -> torch.Tensor:
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
 def linear_workspace(x: torch.Tensor, weight: torch.Tensor, backward: bool = False) -> torch.Tensor:
@@ -118,14 +142,13 @@ def linear_workspace(x: torch.Tensor, weight: torch.Tensor, backward: bool = Fal
     rows, n_in = x.shape
     n_out = weight.shape[0]
     ld_x, ld_w = _matrix("x", x, rows, n_in, x), _matrix("weight", weight, n_out, n_in, x)
+    head = (rows, n_in, n_out, _dtype(x))
     if backward:
-        p = vb_linear_bwd(rows, n_in, n_out, _dtype(x), ACTS["silu"], None, n_out, x.data_ptr(), ld_x,
-                          weight.data_ptr(), ld_w, None, n_out, 16, n_in, 16, n_in, 16, 16, n_out)
-        n = _size("vb_linear_backward_workspace", ctypes.byref(p))
-    else:
-        p = vb_linear_fwd(rows, n_in, n_out, _dtype(x), 0, x.data_ptr(), ld_x, weight.data_ptr(), ld_w)
-        n = _size("vb_linear_forward_workspace", ctypes.byref(p))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
+        p = _BWD.pack(*head, ACTS["silu"], 0, n_out, x.data_ptr(), ld_x, weight.data_ptr(), ld_w, 0, n_out, 16, n_in,
+                      16, n_in, 16, 16, n_out)
+        return _workspace(_size("vb_linear_backward_workspace", p), x.device)
+    p = _FWD.pack(*head, 0, x.data_ptr(), ld_x, weight.data_ptr(), ld_w, 0, 0, n_out, 16, n_out, 0, n_out)
+    return _workspace(_size("vb_linear_forward_workspace", p), x.device)
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -135,28 +158,28 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     [n_out][n_in], bias [n_out], residual [rows][n_out]; act one of none, relu, gelu, silu.
     With want_pre also the value before the activation, which linear_backward needs for
     gelu and silu: (y, pre).  `out` may be the residual itself."""
-    pkg = _pkg()
-    _device(x)
+    dev = _device(x)
     dt = _dtype(x)
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x and weight must be matrices")
     rows, n_in = x.shape
     n_out = weight.shape[0]
-    if act not in ACTS:
-        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
     ld_x = _matrix("x", x, rows, n_in, x)
     ld_w = _matrix("weight", weight, n_out, n_in, x)
     if bias is not None:
         _vector("bias", bias, n_out, x)
-    ld_res = 0 if residual is None else _matrix("residual", residual, rows, n_out, x)
-    y = torch.empty(rows, n_out, dtype=x.dtype, device=x.device) if out is None else out
-    ld_y = n_out if out is None else _matrix("out", out, rows, n_out, x)
-    pre = torch.empty(rows, n_out, dtype=x.dtype, device=x.device) if want_pre else None
-    p = vb_linear_fwd(rows, n_in, n_out, dt, ACTS[act], x.data_ptr(), ld_x, weight.data_ptr(), ld_w,
-                      None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
-                      ld_res, y.data_ptr(), ld_y, None if pre is None else pre.data_ptr(), n_out)
-    wp, wn, keep = _workspace(ws, _size("vb_linear_forward_workspace", ctypes.byref(p)) if ws is None else 0, x.device)
-    pkg._check(pkg.lib().vb_linear_forward(ctypes.byref(p), wp, wn, pkg._stream()), "vb_linear_forward")
+    ld_res = n_out if residual is None else _matrix("residual", residual, rows, n_out, x)
+    if out is None:
+        y, ld_y = x.new_empty((rows, n_out)), n_out
+    else:
+        y, ld_y = out, _matrix("out", out, rows, n_out, x)
+    pre = x.new_empty((rows, n_out)) if want_pre else None
+    p = _FWD.pack(rows, n_in, n_out, dt, _act(act), x.data_ptr(), ld_x, weight.data_ptr(), ld_w,
+                  0 if bias is None else bias.data_ptr(), 0 if residual is None else residual.data_ptr(), ld_res,
+                  y.data_ptr(), ld_y, 0 if pre is None else pre.data_ptr(), n_out)
+    if ws is None:
+        ws = _workspace(_size("vb_linear_forward_workspace", p), x.device)
+    _run("vb_linear_forward", p, ws.data_ptr(), ws.nbytes, _stream(dev))
     return (y, pre) if want_pre else y
 
 
@@ -165,39 +188,37 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act
                     want_bias: bool = True, want_residual: bool = False, ws: Optional[torch.Tensor] = None):
     """Gradients of `linear` (vb_linear_backward) for the gradient dy of y: (dx, dweight, dbias,
     dresidual), None where not wanted.  saved: y for relu, pre for gelu and silu."""
-    pkg = _pkg()
-    _device(x)
+    dev = _device(x)
     dt = _dtype(x)
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x and weight must be matrices")
     rows, n_in = x.shape
     n_out = weight.shape[0]
-    if act not in ACTS:
-        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
-    if (saved is None) != (act == "none"):
+    code = _act(act)
+    if (saved is None) != (code == 0):
         raise ValueError("saved is the forward pass's y (relu) or pre (gelu, silu), and None without an activation")
     ld_dy = _matrix("dy", dy, rows, n_out, x)
     ld_x = _matrix("x", x, rows, n_in, x)
     ld_w = _matrix("weight", weight, n_out, n_in, x)
-    ld_s = 0 if saved is None else _matrix("saved", saved, rows, n_out, x)
-
-    def new(want, *shape):
-        return torch.empty(shape, dtype=x.dtype, device=x.device) if want else None
-
-    dx, dw, db, dr = (new(want_x, rows, n_in), new(want_weight, n_out, n_in), new(want_bias, n_out),
-                      new(want_residual, rows, n_out))
-    p = vb_linear_bwd(rows, n_in, n_out, dt, ACTS[act], dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, weight.data_ptr(),
-                      ld_w, None if saved is None else saved.data_ptr(), ld_s, None if dx is None else dx.data_ptr(),
-                      n_in, None if dw is None else dw.data_ptr(), n_in, None if db is None else db.data_ptr(),
-                      None if dr is None else dr.data_ptr(), n_out)
-    wp, wn, keep = _workspace(ws, _size("vb_linear_backward_workspace", ctypes.byref(p)) if ws is None else 0, x.device)
-    pkg._check(pkg.lib().vb_linear_backward(ctypes.byref(p), wp, wn, pkg._stream()), "vb_linear_backward")
+    ld_s = n_out if saved is None else _matrix("saved", saved, rows, n_out, x)
+    dx = x.new_empty((rows, n_in)) if want_x else None
+    dw = x.new_empty((n_out, n_in)) if want_weight else None
+    db = x.new_empty((n_out,)) if want_bias else None
+    dr = x.new_empty((rows, n_out)) if want_residual else None
+    p = _BWD.pack(rows, n_in, n_out, dt, code, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, weight.data_ptr(), ld_w,
+                  0 if saved is None else saved.data_ptr(), ld_s, 0 if dx is None else dx.data_ptr(), n_in,
+                  0 if dw is None else dw.data_ptr(), n_in, 0 if db is None else db.data_ptr(),
+                  0 if dr is None else dr.data_ptr(), n_out)
+    if ws is None:
+        ws = _workspace(_size("vb_linear_backward_workspace", p), x.device)
+    _run("vb_linear_backward", p, ws.data_ptr(), ws.nbytes, _stream(dev))
     return dx, dw, db, dr
 
 
 def cross_entropy_workspace(logits: torch.Tensor) -> torch.Tensor:
     """A workspace for `cross_entropy` calls of these sizes, to keep between calls."""
-    return _bytes(_size("vb_cross_entropy_workspace", logits.shape[0], logits.shape[1], _dtype(logits)), logits.device)
+    rows, classes = logits.shape
+    return _workspace(_size("vb_cross_entropy_workspace", rows, classes, _dtype(logits)), logits.device)
 
 
 def cross_entropy(logits: torch.Tensor, labels: torch.Tensor, ignore_index: int = -100,
@@ -207,41 +228,35 @@ def cross_entropy(logits: torch.Tensor, labels: torch.Tensor, ignore_index: int 
     """Softmax cross entropy of labels [rows] (int64) and its gradient (vb_cross_entropy): (loss [1],
     row_loss [rows], dlogits [rows][classes] or None).  loss is the mean over the rows whose label
     is not ignore_index; `dlogits` may be the logits themselves."""
-    pkg = _pkg()
-    _device(logits)
+    dev = _device(logits)
     dt = _dtype(logits)
     if logits.dim() != 2:
         raise ValueError("logits must be a matrix")
     rows, classes = logits.shape
     ld = _matrix("logits", logits, rows, classes, logits)
-    if labels.dtype != torch.int64 or labels.shape != (rows,) or labels.device != logits.device \
+    if labels.dtype is not torch.int64 or labels.shape != (rows,) or labels.get_device() != dev \
             or not labels.is_contiguous():
         raise ValueError(f"labels must be contiguous int64 [{rows}] on {logits.device}")
-    if dlogits is None:
-        ld_d = classes
-        if want_grad:
-            dlogits = torch.empty(rows, classes, dtype=logits.dtype, device=logits.device)
-    else:
+    ld_d = classes
+    if dlogits is not None:
         ld_d = _matrix("dlogits", dlogits, rows, classes, logits)
+    elif want_grad:
+        dlogits = logits.new_empty((rows, classes))
     both = torch.empty(rows + 1, dtype=torch.float32, device=logits.device)
     base = both.data_ptr()
-    wp, wn, keep = _workspace(ws, _size("vb_cross_entropy_workspace", rows, classes, dt) if ws is None else 0,
-                              logits.device)
-    p = vb_cross_entropy_args(rows, classes, dt, logits.data_ptr(), ld, labels.data_ptr(), ignore_index,
-                              label_smoothing, grad_scale, base + 4 * rows, base,
-                              None if dlogits is None else dlogits.data_ptr(), ld_d)
-    pkg._check(pkg.lib().vb_cross_entropy(ctypes.byref(p), wp, wn, pkg._stream()), "vb_cross_entropy")
+    if ws is None:
+        ws = cross_entropy_workspace(logits)
+    p = _LOSS.pack(rows, classes, dt, logits.data_ptr(), ld, labels.data_ptr(), ignore_index, label_smoothing,
+                   grad_scale, base + 4 * rows, base, 0 if dlogits is None else dlogits.data_ptr(), ld_d)
+    _run("vb_cross_entropy", p, ws.data_ptr(), ws.nbytes, _stream(dev))
     return both[rows:], both[:rows], dlogits
-
-
-def _clip_arrays(grads: Sequence[torch.Tensor]):
-    n = len(grads)
-    return n, (_i64 * max(n, 1))(*[g.numel() for g in grads])
 
 
 def clip_grad_norm_workspace(grads: Sequence[torch.Tensor]) -> torch.Tensor:
     """A workspace for `clip_grad_norm` calls on tensors of these sizes, to keep between calls."""
-    return _bytes(_size("vb_clip_grad_norm_workspace", *_clip_arrays(grads)), grads[0].device if grads else "cuda")
+    sizes = array("q", [g.numel() for g in grads])
+    return _workspace(_size("vb_clip_grad_norm_workspace", len(sizes), sizes.buffer_info()[0]),
+                      grads[0].device if len(grads) else "cuda")
 
 
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
@@ -249,25 +264,30 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     """Global norm of the gradients, and the gradients clipped to max_norm (vb_clip_grad_norm):
     (norm [1] float32, out).  In place without `out`; a norm that is not finite clips nothing.
     Tensors are contiguous, of any mix of the three types."""
-    pkg = _pkg()
-    n, sizes = _clip_arrays(grads)
-    dev = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current GPU, got {dev}")
-    if out is not None and len(out) != n:
-        raise ValueError(f"{len(out)} outputs for {n} gradients")
+    n = len(grads)
+    dev = _device(grads[0]) if n else torch.cuda.current_device()
+    try:
+        types = array("i", [DTYPES[g.dtype] for g in grads])
+    except KeyError:
+        raise ValueError("gradients must be float32, bfloat16 or float16") from None
     for i, g in enumerate(grads):
-        if not g.is_contiguous() or g.device != dev:
-            raise ValueError(f"gradient {i} must be contiguous, on {dev}")
-        if out is not None:
-            o = out[i]
-            if o.shape != g.shape or o.dtype != g.dtype or o.device != dev or not o.is_contiguous():
-                raise ValueError(f"output {i} must be like its gradient: contiguous {g.dtype} {tuple(g.shape)} on {dev}")
-    dts = (_i32 * max(n, 1))(*[_dtype(g) for g in grads])
-    src = (_P * max(n, 1))(*[g.data_ptr() for g in grads])
-    dst = None if out is None else (_P * max(n, 1))(*[o.data_ptr() for o in out])
-    norm = torch.empty(1, dtype=torch.float32, device=dev)
-    wp, wn, keep = _workspace(ws, _size("vb_clip_grad_norm_workspace", n, sizes) if ws is None else 0, dev)
-    pkg._check(pkg.lib().vb_clip_grad_norm(n, src, dst, sizes, dts, max_norm, norm.data_ptr(), wp, wn, pkg._stream()),
-               "vb_clip_grad_norm")
+        if g.get_device() != dev or not g.is_contiguous():
+            raise ValueError(f"gradient {i} must be contiguous, on the device of the first")
+    sizes = array("q", [g.numel() for g in grads])
+    src = array("Q", [g.data_ptr() for g in grads])
+    dst = 0
+    if out is not None:
+        if len(out) != n:
+            raise ValueError(f"{len(out)} outputs for {n} gradients")
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if o is not g and (o.shape != g.shape or o.dtype is not g.dtype or o.get_device() != dev
+                               or not o.is_contiguous()):
+                raise ValueError(f"output {i} must be like its gradient: contiguous {g.dtype} {tuple(g.shape)}")
+        outs = array("Q", [o.data_ptr() for o in out])
+        dst = outs.buffer_info()[0]
+    norm = torch.empty(1, dtype=torch.float32, device=torch.device("cuda", dev))
+    if ws is None:
+        ws = _workspace(_size("vb_clip_grad_norm_workspace", n, sizes.buffer_info()[0]), norm.device)
+    _run("vb_clip_grad_norm", n, src.buffer_info()[0], dst or None, sizes.buffer_info()[0], types.buffer_info()[0],
+         max_norm, norm.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(dev))
     return norm, list(grads if out is None else out)
