@@ -658,32 +658,40 @@ hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
 
 // ---------------------------------------------------------------------------
 // Rows that do not start on 16-byte boundaries or end in part of a chunk are copied to
-// rows that do, zeros to the end of the chunk, before a large product.
+// rows that do, zeros to the end of the chunk, before a large product; both operands of
+// a call in one launch.
 template <typename T>
-__global__ __launch_bounds__(256) void pack_kernel(const T* src, long long ld, long long rows, int n, T* dst,
-                                                   int chunks) {
+__global__ __launch_bounds__(256) void pack_kernel(PackJob j0, PackJob j1) {
   typedef typename Chunk<T>::type C;
   constexpr int EC = 16 / sizeof(T);
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long r = i / chunks;
-  const int c = (int)(i % chunks);
-  if (r >= rows) return;
-  const T* q = src + r * ld + (long long)c * EC;
+  const bool second = blockIdx.x >= j0.blocks;
+  const PackJob& j = second ? j1 : j0;
+  const long long i = (long long)(blockIdx.x - (second ? j0.blocks : 0)) * 256 + threadIdx.x;
+  const long long r = i / j.chunks;
+  const int c = (int)(i % j.chunks);
+  if (r >= j.rows) return;
+  const T* q = (const T*)j.src + r * j.ld + (long long)c * EC;
   C v;
-  if ((c + 1) * EC <= n) {
+  if ((c + 1) * EC <= j.n) {
     v = load_loose(q);
   } else {
 #pragma unroll
-    for (int e = 0; e < EC; ++e) v[e] = c * EC + e < n ? q[e] : (T)0.f;
+    for (int e = 0; e < EC; ++e) v[e] = c * EC + e < j.n ? q[e] : (T)0.f;
   }
-  *(C*)(dst + i * EC) = v;
+  *(C*)((T*)j.dst + i * EC) = v;
 }
 
 // g = dy act'(saved), its copies and its column sums.  A thread has one chunk of columns
-// and every eighth of ROWS rows (16-byte accesses at any alignment); the workgroup's 32
-// chunks of columns are summed over its rows in LDS, one float32 per column and
-// workgroup.
-constexpr int SUM_ROWS = 64;
+// and every eighth of the workgroup's rows (16-byte accesses at any alignment); the
+// workgroup's 32 chunks of columns are summed over its rows in LDS, one float32 per
+// column and workgroup.  Workgroups have 64 rows, or as few as 8 while there would be
+// less than two workgroups a CU (1037 x 999 in float16: 13 us with 64 rows).
+int sum_rows(long long rows, int n, int chunk) {
+  const long long across = (n + 32 * chunk - 1) / (32 * chunk);
+  int r = 64;
+  while (r > 8 && across * ((rows + r - 1) / r) < 512) r /= 2;
+  return r;
+}
 
 template <typename T, int ACT>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p) {
@@ -693,14 +701,14 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p) {
   __shared__ float red[8][32 * EC + 1];
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int n = (blockIdx.x * 32 + c) * EC;
-  const long long m0 = (long long)blockIdx.y * SUM_ROWS;
+  const long long m0 = (long long)blockIdx.y * p.part_rows;
   const T* dy = (const T*)p.dy;
   const T* saved = (const T*)p.saved;
   float sum[EC];
 #pragma unroll
   for (int e = 0; e < EC; ++e) sum[e] = 0.f;
   const int have = p.n - n;  // columns from this chunk on
-  for (long long m = m0 + w; m < min(m0 + SUM_ROWS, p.rows) && have > 0; m += 8) {
+  for (long long m = m0 + w; m < min(m0 + p.part_rows, p.rows) && have > 0; m += 8) {
     C d, s;
     if (have >= EC) {
       d = load_loose(dy + m * p.ld_dy + n);
@@ -747,19 +755,24 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p) {
   }
 }
 
-// dbias from the workgroups' sums: 64 columns per workgroup, whose four wavefronts take
+// dbias from the workgroups' sums: 64 columns per workgroup, whose 16 wavefronts take
 // the sums in turn
 template <typename T>
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* partial, int parts, int n, T* out) {
-  __shared__ float red[4][64];
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int parts, int n, T* out) {
+  __shared__ float red[16][64];
   const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int col = blockIdx.x * 64 + c;
   float s = 0.f;
   if (col < n)
-    for (int i = w; i < parts; i += 4) s += partial[(long long)i * n + col];
+    for (int i = w; i < parts; i += 16) s += partial[(long long)i * n + col];
   red[w][c] = s;
   __syncthreads();
-  if (w == 0 && col < n) out[col] = from_f32<T>((red[0][c] + red[1][c]) + (red[2][c] + red[3][c]));
+  if (w == 0 && col < n) {
+    s = red[0][c];
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += red[k][c];
+    out[col] = from_f32<T>(s);
+  }
 }
 
 __global__ __launch_bounds__(256) void fill_zero_kernel(unsigned short* p, long long rows, long long n, long long ld) {
@@ -770,16 +783,18 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(unsigned short* p, long 
 template <typename T>
 hipError_t launch_act_grad_typed(const ActGrad& p, hipStream_t st) {
   constexpr int EC = 16 / sizeof(T);
-  const long long parts = (p.rows + SUM_ROWS - 1) / SUM_ROWS;
+  const int per = sum_rows(p.rows, p.n, EC);
+  const long long parts = (p.rows + per - 1) / per;
   // the rows go along the second grid dimension, 65535 parts at most a launch
   for (long long at = 0; at < parts; at += 65535) {
-    const long long m = at * SUM_ROWS;
+    const long long m = at * per;
     ActGrad q = p;
     q.dy = (const T*)p.dy + m * p.ld_dy;
     if (p.saved) q.saved = (const T*)p.saved + m * p.ld_saved;
     if (p.g) q.g = (T*)p.g + m * p.ld_g;
     if (p.dres) q.dres = (T*)p.dres + m * p.ld_dres;
     q.rows = p.rows - m;
+    q.part_rows = per;
     q.partial = parts > 1 && p.dbias ? p.partial + at * p.n : nullptr;
     const dim3 grid((p.n + 32 * EC - 1) / (32 * EC), (unsigned)std::min(parts - at, 65535LL));
     if (p.act == VB_ACT_NONE) act_grad_kernel<T, VB_ACT_NONE><<<grid, 256, 0, st>>>(q);
@@ -788,7 +803,7 @@ hipError_t launch_act_grad_typed(const ActGrad& p, hipStream_t st) {
     else act_grad_kernel<T, VB_ACT_SILU><<<grid, 256, 0, st>>>(q);
   }
   if (p.dbias && parts > 1)
-    column_sum_kernel<T><<<(p.n + 63) / 64, 256, 0, st>>>(p.partial, (int)parts, p.n, (T*)p.dbias);
+    column_sum_kernel<T><<<(p.n + 63) / 64, 1024, 0, st>>>(p.partial, (int)parts, p.n, (T*)p.dbias);
   return hipGetLastError();
 }
 
@@ -858,19 +873,27 @@ bool is_chunked(const void* p, long long ld, long long n, int dtype) {
   return (uintptr_t)p % 16 == 0 && ld * es % 16 == 0 && n * es % 16 == 0 && ld * es <= MAX_CHUNKED_ROW;
 }
 
-hipError_t launch_pack(const void* src, long long ld, long long rows, int n, void* dst, int dtype, hipStream_t st) {
-  const int chunks = (int)(chunked_row(n, dtype) / 16);
-  const long long blocks = (rows * chunks + 255) / 256;
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+hipError_t launch_pack(PackJob j0, PackJob j1, int dtype, hipStream_t st) {
+  long long blocks = 0;
+  for (PackJob* j : {&j0, &j1}) {
+    if (!j->dst) j->rows = 0;
+    j->chunks = (int)(chunked_row(j->n, dtype) / 16);
+    const long long b = (j->rows * j->chunks + 255) / 256;
+    blocks += b;
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    j->blocks = (unsigned)b;
+  }
+  if (!blocks) return hipSuccess;
   const dim3 grid((unsigned)blocks);
-  if (dtype == VB_F32) pack_kernel<float><<<grid, 256, 0, st>>>((const float*)src, ld, rows, n, (float*)dst, chunks);
-  else if (dtype == VB_BF16) pack_kernel<bf16><<<grid, 256, 0, st>>>((const bf16*)src, ld, rows, n, (bf16*)dst, chunks);
-  else pack_kernel<f16><<<grid, 256, 0, st>>>((const f16*)src, ld, rows, n, (f16*)dst, chunks);
+  if (dtype == VB_F32) pack_kernel<float><<<grid, 256, 0, st>>>(j0, j1);
+  else if (dtype == VB_BF16) pack_kernel<bf16><<<grid, 256, 0, st>>>(j0, j1);
+  else pack_kernel<f16><<<grid, 256, 0, st>>>(j0, j1);
   return hipGetLastError();
 }
 
-size_t act_grad_bytes(long long rows, int n) {
-  return rows > SUM_ROWS ? (size_t)((rows + SUM_ROWS - 1) / SUM_ROWS) * n * 4 : 0;
+size_t act_grad_bytes(long long rows, int n, int dtype) {
+  const int per = sum_rows(rows, n, 16 / (int)elem_size(dtype));
+  return rows > per ? (size_t)((rows + per - 1) / per) * n * 4 : 0;
 }
 
 hipError_t launch_act_grad(const ActGrad& p, int dtype, hipStream_t st) {

@@ -131,7 +131,7 @@ BackwardPlan plan_backward(const vb_linear_bwd& p) {
   const size_t row = chunked_row(p.n_in, dt);
   if (p.dweight && !is_chunked(p.x, p.ld_x, p.n_in, dt)) f.x.take(f.total, p.rows * row);
   if (p.dx && !is_chunked(p.weight, p.ld_w, p.n_in, dt)) f.w.take(f.total, p.n_out * row);
-  if (p.dbias) f.sums.take(f.total, act_grad_bytes(p.rows, p.n_out));
+  if (p.dbias) f.sums.take(f.total, act_grad_bytes(p.rows, p.n_out, dt));
   size_t parts = 0;  // the products run one after the other
   if (p.dx) parts = product_bytes(a, dt);
   if (p.dweight) {
@@ -177,14 +177,10 @@ extern "C" vb_status vb_linear_forward(const vb_linear_fwd* p, void* ws, size_t 
   TRY(check_ws(fn, ws, ws_bytes, f.total));
   const hipStream_t st = (hipStream_t)stream;
   const long long ld = (long long)(chunked_row(p->n_in, p->dtype) / elem_size(p->dtype));
-  if (f.x.used) {
-    HIPCHK(launch_pack(p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws), p->dtype, st));
-    f.d.a = f.x.in(ws), f.d.lda = ld;
-  }
-  if (f.w.used) {
-    HIPCHK(launch_pack(p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws), p->dtype, st));
-    f.d.b = f.w.in(ws), f.d.ldb = ld;
-  }
+  HIPCHK(launch_pack({p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws)}, {p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws)},
+                     p->dtype, st));
+  if (f.x.used) f.d.a = f.x.in(ws), f.d.lda = ld;
+  if (f.w.used) f.d.b = f.w.in(ws), f.d.ldb = ld;
   f.d.partial = (float*)f.partial.in(ws);
   HIPCHK(launch_product(f.d, p->dtype, st));
   return VB_OK;
@@ -228,22 +224,13 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
     if (f.g.used) f.dx.a = f.dw.a = g.g, f.dx.lda = f.dw.lda = g.ld_g;
   }
   const long long ld = (long long)chunked_row(p->n_in, p->dtype) / es;
-  if (p->dx) {
-    if (f.w.used) {
-      HIPCHK(launch_pack(p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws), p->dtype, st));
-      f.dx.b = f.w.in(ws), f.dx.ldb = ld;
-    }
-    f.dx.partial = (float*)f.partial.in(ws);
-    HIPCHK(launch_product(f.dx, p->dtype, st));
-  }
-  if (p->dweight) {
-    if (f.x.used) {
-      HIPCHK(launch_pack(p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws), p->dtype, st));
-      f.dw.b = f.x.in(ws), f.dw.ldb = ld;
-    }
-    f.dw.partial = (float*)f.partial.in(ws);
-    HIPCHK(launch_product(f.dw, p->dtype, st));
-  }
+  HIPCHK(launch_pack({p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws)}, {p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws)},
+                     p->dtype, st));
+  if (f.w.used) f.dx.b = f.w.in(ws), f.dx.ldb = ld;
+  if (f.x.used) f.dw.b = f.x.in(ws), f.dw.ldb = ld;
+  f.dx.partial = f.dw.partial = (float*)f.partial.in(ws);
+  if (p->dx) HIPCHK(launch_product(f.dx, p->dtype, st));
+  if (p->dweight) HIPCHK(launch_product(f.dw, p->dtype, st));
   return VB_OK;
 }
 

@@ -54,7 +54,18 @@ constexpr long long MAX_CHUNKED_ROW = 1 << 22;
 bool is_chunked(const void* p, long long ld, long long n, int dtype);
 // Bytes of a row of n elements rounded up to 16.
 inline size_t chunked_row(long long n, int dtype) { return (n * elem_size(dtype) + 15) / 16 * 16; }
-hipError_t launch_pack(const void* src, long long ld, long long rows, int n, void* dst, int dtype, hipStream_t st);
+// Copies rows of n elements to chunked rows, zeros to the end of the last chunk; two
+// matrices at once (dst NULL: none).
+struct PackJob {
+  const void* src;
+  long long ld, rows;
+  int n;
+  void* dst;
+  // set by launch_pack
+  int chunks;
+  unsigned blocks;
+};
+hipError_t launch_pack(PackJob j0, PackJob j1, int dtype, hipStream_t st);
 
 // v = dy * act'(saved), in float32: g = v (rows of ld_g elements that start on 16-byte
 // boundaries, zeros to the end of the last chunk), dres = v, dbias = column sums of v;
@@ -72,8 +83,9 @@ struct ActGrad {
   long long rows;
   int n;
   int act;
+  int part_rows;  // set by launch_act_grad: rows of a workgroup
 };
-size_t act_grad_bytes(long long rows, int n);
+size_t act_grad_bytes(long long rows, int n, int dtype);
 hipError_t launch_act_grad(const ActGrad& p, int dtype, hipStream_t st);
 hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long long ld_bytes, hipStream_t st);
 
