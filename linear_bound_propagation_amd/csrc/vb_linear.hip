@@ -115,9 +115,21 @@ struct Chunk<f16> {
 // what a lane loads past the end of the reduction
 __device__ const u32x4 zero_chunk = {0, 0, 0, 0};
 
-__device__ __forceinline__ void load_to_lds(const void* g, void* l) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
-                                   (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+// 16 bytes per lane from global memory to LDS, lane after lane from l on (uniform).  In
+// assembly, since the compiler, which cannot tell the stages of the ring apart, would
+// wait for every such load before the next transposing read; nothing is returned in
+// registers, and the kernels wait for the loads themselves (join).  The instruction
+// takes the LDS address from M0, a wait state after it is written; M0 is a reserved
+// register, which the compiler keeps nothing in for these kernels (they index no
+// registers and use no other instruction that reads it).
+__device__ __forceinline__ unsigned lds_address(const void* l) {
+  return __builtin_amdgcn_readfirstlane((unsigned)(unsigned long long)(__attribute__((address_space(3))) const void*)l);
+}
+__device__ __forceinline__ void load_to_lds(const void* base, unsigned off, const void* l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_address(l)), "v"(off), "s"(base));
+}
+__device__ __forceinline__ void load_to_lds(const void* g, const void* l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_address(l)), "v"(g));
 }
 
 // The activation of VEC values; one branch for all of them.
@@ -243,7 +255,7 @@ struct Operand {
   __device__ void load(int t, char* lds) const {
     const char* at = base + t * step;
 #pragma unroll
-    for (int i = 0; i < L; ++i) load_to_lds(at + off[i], lds + (i * NW + wave) * 1024);
+    for (int i = 0; i < L; ++i) load_to_lds(at, off[i], lds + (i * NW + wave) * 1024);
   }
   // any stage: zeros past the end of the reduction's K elements
   __device__ void load_part(int t, char* lds, int K) const {
