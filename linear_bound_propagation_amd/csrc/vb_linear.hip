@@ -189,15 +189,14 @@ __device__ __forceinline__ void tile_of(unsigned bid, int tm, int tn, int& i, in
   j = in / rows;
 }
 
-// Scheduling of one phase: D LDS reads and (nl of V) loads to LDS between M MFMAs
-template <int M, int D, int V>
-__device__ __forceinline__ void interleave(int nl) {
+// Scheduling of one phase: D LDS reads between M MFMAs
+template <int M, int D>
+__device__ __forceinline__ void interleave() {
   constexpr int PER = (D + M - 1) / M;
 #pragma unroll
   for (int i = 0; i < M; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     if (i * PER < D) __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
-    if (nl && i < V) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
   }
 }
 
@@ -205,10 +204,12 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // One operand of a workgroup's tile: ROWS of its rows (ACROSS: columns), its loads into
 // a stage and its reads from one.
-template <typename T, int ROWS, int NW, bool ACROSS>
+template <typename T, int ROWS, int NW, bool ACROSS, int DEPTH>
 struct Operand {
   typedef typename Chunk<T>::type C;
-  static constexpr int ES = sizeof(T), L = ROWS / 16 / NW;
+  static constexpr int ES = sizeof(T), L = ROWS * DEPTH / 1024 / NW;
+  static constexpr int STEP_ROWS = 64 / ES;       // rows of a 64-byte step when ACROSS
+  static constexpr int RPL = 1024 / DEPTH;        // rows of a load otherwise
   static constexpr int RB = ROWS * ES;            // bytes of a stage's row when ACROSS
   static constexpr int PER_BLOCK = ES;            // chunks of a block of 16 elements
   static constexpr int READS = ACROSS ? (ES == 4 ? 4 : 2) : 1;  // LDS reads of a fetch
@@ -231,23 +232,28 @@ struct Operand {
     const int at = ((i * NW + wave) * 1024 + lane * 16) % RB / 16;
     return ((at / PER_BLOCK) ^ row_swizzle(row_of(i))) * PER_BLOCK + at % PER_BLOCK;
   }
-  __device__ int chunk_along() const { return (lane & 3) ^ (lane >> 4); }
+  // position of chunk c of row r otherwise: rows of a quarter wavefront on different banks
+  __device__ static int along_swizzle(int r) { return DEPTH == 64 ? (r >> 2) & 3 : (r >> 1) & 7; }
+  __device__ int chunk_along() const {  // the rows of all of a wavefront's loads are alike to the swizzle
+    return (lane % (DEPTH / 16)) ^ along_swizzle(wave * RPL + lane / (DEPTH / 16));
+  }
 
   // rows (ACROSS: columns) from r0 on of `count`; past the end the last one is repeated
   __device__ void init(const void* p, long long ld, long long r0, long long count, int first_stage, int w, int l) {
     lane = l, wave = w;
     if (ACROSS) {
-      step = ld * 64;  // 64 / ES rows of ld * ES bytes
+      step = ld * DEPTH;  // DEPTH / ES rows of ld * ES bytes
       base = (const char*)p + r0 * ES + first_stage * step;
       const int last = (int)min(((count - r0) * ES + 15) / 16 - 1, (long long)(RB / 16 - 1));
 #pragma unroll
       for (int i = 0; i < L; ++i) off[i] = (unsigned)row_of(i) * (unsigned)(ld * ES) + min(chunk_of(i), last) * 16;
     } else {
-      step = 64;
+      step = DEPTH;
       base = (const char*)p + r0 * ld * ES + first_stage * step;
 #pragma unroll
       for (int i = 0; i < L; ++i)
-        off[i] = (unsigned)min((long long)((i * NW + wave) * 16 + (lane >> 2)), count - 1 - r0) * (unsigned)(ld * ES) +
+        off[i] = (unsigned)min((long long)((i * NW + wave) * RPL + lane / (DEPTH / 16)), count - 1 - r0) *
+                     (unsigned)(ld * ES) +
                  chunk_along() * 16;
     }
   }
@@ -262,19 +268,21 @@ struct Operand {
     const char* at = base + t * step;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      const bool in = ACROSS ? t * (64 / ES) + row_of(i) < K : (t * 4 + chunk_along()) * (16 / ES) < K;
+      const bool in = ACROSS ? t * (DEPTH / ES) + row_of(i) < K : (t * (DEPTH / 16) + chunk_along()) * (16 / ES) < K;
       load_to_lds(in ? (const void*)(at + off[i]) : &zero_chunk, lds + (i * NW + wave) * 1024);
     }
   }
-  // where a lane reads: block b of 16 rows (columns) of a stage
+  // where a lane reads: block b of 16 rows (columns) in the first step of a stage
   __device__ int place(int b) const {
     const int r16 = lane & 15, quarter = lane >> 4;
-    if (!ACROSS) return (b * 16 + r16) * 64 + (quarter ^ ((lane >> 2) & 3)) * 16;
+    if (!ACROSS) return (b * 16 + r16) * DEPTH + (quarter ^ along_swizzle(r16)) * 16;
     if (ES == 4) return quarter * 4 * RB + (b ^ quarter) * 64 + r16 * 4;
     const int k = quarter * 8 + (r16 >> 2);
     return k * RB + (b ^ row_swizzle(k)) * 32 + (r16 & 3) * 8;
   }
-  __device__ static C fetch(const char* p) {
+  // from there, in step u (0 or, with a depth of 128, 1)
+  __device__ static C fetch(const char* lds, int at, int u) {
+    const char* p = lds + (ACROSS ? at + u * STEP_ROWS * RB : u ? at ^ 64 : at);
     if constexpr (!ACROSS) {
       return *(const C*)p;
     } else if constexpr (ES == 4) {
@@ -295,10 +303,12 @@ struct Operand {
 template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB>
 __global__ __launch_bounds__(64 * WM * WN, BN == 64 || BM == 128 ? 4 : 2) void gemm_kernel(Product p, int tm, int tn) {
   typedef typename Chunk<T>::type C;
-  constexpr int NW = WM * WN, NS = 4, STAGE = (BM + BN) * 64, KS = 64 / sizeof(T);
+  // the largest tiles with an operand along: 128-byte rows, whose loads take whole lines
+  constexpr int DEPTH = BM == 256 && BN == 256 && !(XA && XB) ? 128 : 64;
+  constexpr int NW = WM * WN, NS = DEPTH == 128 ? 2 : 4, STAGE = (BM + BN) * DEPTH, KS = DEPTH / sizeof(T);
   constexpr int TM = BM / WM, TN = BN / WN, MT = TM / 16, NT = TN / 16, MH = MT / 2;
-  typedef Operand<T, BM, NW, XA> OA;
-  typedef Operand<T, BN, NW, XB> OB;
+  typedef Operand<T, BM, NW, XA, DEPTH> OA;
+  typedef Operand<T, BN, NW, XB, DEPTH> OB;
   constexpr int LA = OA::L, LB = OB::L, RA = OA::READS, RB = OB::READS;
   __shared__ __align__(16) char lds[NS * STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -307,15 +317,15 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 || BM == 128 ? 4 : 2) void g
   const long long m0 = (long long)ti * BM;
   const int n0 = tj * BN;
   // this workgroup's part of the reduction
-  const int first = blockIdx.y * p.split_stages;
-  const int K = (int)min(p.K - (long long)first * KS, (long long)p.split_stages * KS);
+  const int first = blockIdx.y * (p.split_steps * 64 / DEPTH);
+  const int K = (int)min(p.K - (long long)first * KS, (long long)p.split_steps * (64 / (int)sizeof(T)));
   const int stages = (K + KS - 1) / KS, full = K / KS;
   OA a;
   OB b;
   a.init(p.a, p.lda, m0, p.M, first, wave, lane);
   b.init(p.b, p.ldb, n0, p.N, first, wave, lane);
-  auto issue = [&](int t, int base) { a.load(t, lds + base), b.load(t, lds + base + BM * 64); };
-  auto issue_part = [&](int t, int base) { a.load_part(t, lds + base, K), b.load_part(t, lds + base + BM * 64, K); };
+  auto issue = [&](int t, int base) { a.load(t, lds + base), b.load(t, lds + base + BM * DEPTH); };
+  auto issue_part = [&](int t, int base) { a.load_part(t, lds + base, K), b.load_part(t, lds + base + BM * DEPTH, K); };
   // The next stage has landed (all but the loads of the NS - 2 stages after it), this
   // wavefront has its reads of the last stage, and so have the others.
   auto join = [] {
@@ -328,20 +338,20 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 || BM == 128 ? 4 : 2) void g
 #pragma unroll
   for (int i = 0; i < MT; ++i) pa[i] = a.place(wm * MT + i);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) pb[j] = BM * 64 + b.place(wn * NT + j);
+  for (int j = 0; j < NT; ++j) pb[j] = BM * DEPTH + b.place(wn * NT + j);
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   C fa[MT], fb[2][NT];
-  auto fetch_a = [&](int base, int h) {
+  auto fetch_a = [&](int base, int u, int h) {
 #pragma unroll
-    for (int i = h * MH; i < h * MH + MH; ++i) fa[i] = OA::fetch(lds + base + pa[i]);
+    for (int i = h * MH; i < h * MH + MH; ++i) fa[i] = OA::fetch(lds + base, pa[i], u);
   };
-  auto fetch_b = [&](int base, int f) {
+  auto fetch_b = [&](int base, int u, int f) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) fb[f][j] = OB::fetch(lds + base + pb[j]);
+    for (int j = 0; j < NT; ++j) fb[f][j] = OB::fetch(lds + base, pb[j], u);
   };
   auto multiply = [&](int h, int f) {
 #pragma unroll
@@ -353,23 +363,25 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 || BM == 128 ? 4 : 2) void g
     const int x = base + n * STAGE;
     return x >= NS * STAGE ? x - NS * STAGE : x;
   };
-  // A stage, its columns in fb[f]: loads() starts the loads of a later stage, wait() is
-  // one of the joins.  The reads are spread between the MFMAs; left to itself the
-  // compiler sinks them to their uses to save registers.
-  auto stage = [&](int cur, int f, auto&& loads, int nl, auto&& wait) {
+  // A step of 64 bytes (u of its stage), its columns in fb[f]: loads() starts the loads of
+  // a later stage, wait() is one of the joins after the last step of a stage.  The reads
+  // are spread between the MFMAs; left to itself the compiler sinks them to their uses to
+  // save registers.
+  auto step = [&](int cur, int u, int f, auto&& loads, auto&& wait) {
     __builtin_amdgcn_sched_barrier(0);
     loads();
-    fetch_a(cur, 1);
+    fetch_a(cur, u, 1);
     multiply(0, f);
-    interleave<MH * NT * Chunk<T>::MFMAS, MH * RA, LA + LB>(nl);
+    interleave<MH * NT * Chunk<T>::MFMAS, MH * RA>();
     __builtin_amdgcn_sched_barrier(0);
-    wait();
+    const bool last = u == DEPTH / 64 - 1;
+    if (last) wait();
     __builtin_amdgcn_sched_barrier(0);
-    const int nxt = after(cur, 1);
-    fetch_b(nxt, f ^ 1);  // after the last stage, of nothing that is used
-    fetch_a(nxt, 0);
+    const int nxt = last ? after(cur, 1) : cur;
+    fetch_b(nxt, last ? 0 : u + 1, f ^ 1);  // after the last stage, of nothing that is used
+    fetch_a(nxt, last ? 0 : u + 1, 0);
     multiply(1, f);
-    interleave<MH * NT * Chunk<T>::MFMAS, MH * RA + NT * RB, 0>(0);
+    interleave<MH * NT * Chunk<T>::MFMAS, MH * RA + NT * RB>();
     __builtin_amdgcn_sched_barrier(0);
   };
   auto none = [] {};
@@ -377,23 +389,37 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 || BM == 128 ? 4 : 2) void g
     if (i < full) issue(i, i * STAGE);
     else if (i < stages) issue_part(i, i * STAGE);
   if (full >= NS - 1) join(); else join_all();
-  fetch_b(0, 0);
-  fetch_a(0, 0);
+  fetch_b(0, 0, 0);
+  fetch_a(0, 0, 0);
   int t = 0, cur = 0;
-  for (; t + NS < full; t += 2) {
-    stage(cur, 0, [&] { issue(t + NS - 1, after(cur, NS - 1)); }, LA + LB, join);
-    cur = after(cur, 1);
-    stage(cur, 1, [&] { issue(t + NS, after(cur, NS - 1)); }, LA + LB, join);
-    cur = after(cur, 1);
-  }
-  for (; t < stages; t += 2) {
-    if (t + NS - 1 < stages) issue_part(t + NS - 1, after(cur, NS - 1));
-    stage(cur, 0, none, 0, join_all);
-    cur = after(cur, 1);
-    if (t + 1 == stages) break;
-    if (t + NS < stages) issue_part(t + NS, after(cur, NS - 1));
-    stage(cur, 1, none, 0, join_all);
-    cur = after(cur, 1);
+  if constexpr (DEPTH == 128) {
+    for (; t + NS - 1 < full; ++t) {
+      step(cur, 0, 0, [&] { issue(t + NS - 1, after(cur, NS - 1)); }, none);
+      step(cur, 1, 1, none, join);
+      cur = after(cur, 1);
+    }
+    for (; t < stages; ++t) {
+      if (t + NS - 1 < stages) issue_part(t + NS - 1, after(cur, NS - 1));
+      step(cur, 0, 0, none, none);
+      step(cur, 1, 1, none, join_all);
+      cur = after(cur, 1);
+    }
+  } else {
+    for (; t + NS < full; t += 2) {
+      step(cur, 0, 0, [&] { issue(t + NS - 1, after(cur, NS - 1)); }, join);
+      cur = after(cur, 1);
+      step(cur, 0, 1, [&] { issue(t + NS, after(cur, NS - 1)); }, join);
+      cur = after(cur, 1);
+    }
+    for (; t < stages; t += 2) {
+      if (t + NS - 1 < stages) issue_part(t + NS - 1, after(cur, NS - 1));
+      step(cur, 0, 0, none, join_all);
+      cur = after(cur, 1);
+      if (t + 1 == stages) break;
+      if (t + NS < stages) issue_part(t + NS, after(cur, NS - 1));
+      step(cur, 0, 1, none, join_all);
+      cur = after(cur, 1);
+    }
   }
   join_all();
   // Outputs leave through LDS, 32 rows of the wavefront's tile at a time in its own
@@ -645,9 +671,10 @@ hipError_t launch_gemm(const Product& p, int splits, hipStream_t st) {
 
 template <typename T>
 hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
-  const int stages = (int)((p.K * (long long)sizeof(T) + 63) / 64);
-  p.split_stages = (stages + t.splits - 1) / t.splits;
-  const int splits = (stages + p.split_stages - 1) / p.split_stages;
+  // in steps of 64 bytes, an even number of them to a part
+  const int steps = (int)((p.K * (long long)sizeof(T) + 63) / 64);
+  p.split_steps = ((steps + t.splits - 1) / t.splits + 1) / 2 * 2;
+  const int splits = (steps + p.split_steps - 1) / p.split_steps;
   if (splits == 1) p.partial = nullptr;
   p.ld_partial = (p.N + 3) / 4 * 4;
   hipError_t e;

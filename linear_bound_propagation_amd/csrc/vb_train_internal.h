@@ -39,7 +39,7 @@ struct Product {
   // workspace of product_bytes: float32 parts of a reduction split over workgroups
   float* partial;
   // set by launch_product
-  int ld_partial, split_stages;
+  int ld_partial, split_steps;
 };
 struct Tiling {
   int bm, bn, splits;

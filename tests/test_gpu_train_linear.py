@@ -246,3 +246,19 @@ def test_captured_in_a_graph(lbp, size, dtype):
         torch.cuda.synchronize()
         for a, c in zip(outs, step()):
             assert torch.equal(a, c), i
+
+
+@pytest.mark.parametrize("size, dtype", [((4090, 4088, 4080), BF16), ((4090, 4088, 4080), F16), ((4091, 1001, 4085), BF16),
+                                         ((8190, 72, 2056), F16), ((4090, 400, 4088), F32), ((2041, 1019, 2045), F32),
+                                         ((70, 8192, 72), BF16), ((90, 4100, 260), F32), ((2050, 2000, 1030), BF16)],
+                         ids=str)
+def test_large_products(lbp, size, dtype):
+    """Sizes that take the largest tiles (all three products) and split reductions, none of them a
+    whole number of tiles or stages."""
+    rows, n_in, n_out = size
+    print(f"large {size} {dtype}", flush=True)
+    x, w, b, r = case(*size, dtype, seed=70)
+    check_forward(lbp, x, w, b, r, "relu", f"large {size}")
+    dy = normal(gen(71), rows, n_out, std=rows ** -0.5, dtype=dtype)
+    check_backward(lbp, dy, x, w, None, "none", f"large {size}")
+    check_backward(lbp, dy, x, w, r, "silu", f"large {size}")
