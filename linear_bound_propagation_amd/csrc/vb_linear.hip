@@ -301,11 +301,14 @@ struct Operand {
 };
 
 template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB>
-__global__ __launch_bounds__(64 * WM * WN, BN == 64 || BM == 128 ? 4 : 2) void gemm_kernel(Product p, int tm, int tn) {
+__global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Product p, int tm, int tn) {
   typedef typename Chunk<T>::type C;
-  // the largest tiles with an operand along: 128-byte rows, whose loads take whole lines
-  constexpr int DEPTH = BM == 256 && BN == 256 && !(XA && XB) ? 128 : 64;
-  constexpr int NW = WM * WN, NS = DEPTH == 128 ? 2 : 4, STAGE = (BM + BN) * DEPTH, KS = DEPTH / sizeof(T);
+  // Stages of 128 bytes (whole lines of an operand along: 192 us against 210 with 64 at
+  // 4096 x 8192 -> 4096, bf16), three of them, or two for the largest tiles; those have
+  // four of 64 bytes when both operands lie across, whose loads are whole lines anyway.
+  constexpr bool LARGE = BM == 256 && BN == 256;
+  constexpr int DEPTH = LARGE && XA && XB ? 64 : 128, NS = !LARGE ? 3 : DEPTH == 128 ? 2 : 4;
+  constexpr int NW = WM * WN, STAGE = (BM + BN) * DEPTH, KS = DEPTH / sizeof(T);
   constexpr int TM = BM / WM, TN = BN / WN, MT = TM / 16, NT = TN / 16, MH = MT / 2;
   typedef Operand<T, BM, NW, XA, DEPTH> OA;
   typedef Operand<T, BN, NW, XB, DEPTH> OB;
@@ -849,19 +852,21 @@ hipError_t launch_act_grad_typed(const ActGrad& p, hipStream_t st) {
 }  // namespace
 
 // Tile and split of a large product by the time they would take: rounds of workgroups
-// over 256 CUs, each a run of stages and a fixed part.  A stage takes `latency`
-// microseconds for a tile that has its CU to itself and `share` for each of several; both
-// were measured per tile size (4096 x 4096 x 8192 and 1024 x 1024 x 1024, and 64 x 4096 x
-// 4096 for the small ones).  A split costs the writing and reading of its float32 parts
-// at 4 TB/s and another launch.
+// over 256 CUs, each a run of 64-byte steps and a fixed part.  A step takes `latency`
+// microseconds for a tile that has its CU to itself and `share` for each of several,
+// measured per tile size at 1024 x 1024 x 1024 and 4096 x 4096 x 4096: at the first the
+// 64-wide tiles win (7.2 us; 128 10.8, 256 26), at the second the 256-wide (113 us; 256 x
+// 128 122, 128 140, 64 197), at 2048 x 4096 x 4096 those of 256 x 128 (61 us; 256 92, 128
+// 85, 64 111).  A split costs the writing and reading of its float32 parts at 4 TB/s and
+// another launch.
 Tiling choose_tiling(int dtype, long long M, int N, long long K) {
   struct Kind {
     int bm, bn, per_cu;
     double latency, share;
   };
-  static const Kind k16[] = {{256, 256, 1, 0.62, 0.80}, {256, 128, 1, 0.42, 0.52}, {128, 128, 2, 0.30, 0.30},
-                             {64, 64, 4, 0.14, 0.125}};
-  static const Kind k32[] = {{256, 128, 1, 1.90, 1.90}, {128, 128, 2, 1.02, 0.98}, {64, 64, 4, 0.31, 0.30}};
+  static const Kind k16[] = {{256, 256, 1, 0.70, 0.83}, {256, 128, 1, 0.39, 0.46}, {128, 128, 1, 0.25, 0.27},
+                             {64, 64, 3, 0.13, 0.09}};
+  static const Kind k32[] = {{256, 128, 1, 1.90, 1.90}, {128, 128, 1, 1.01, 1.01}, {64, 64, 3, 0.285, 0.27}};
   const Kind* kinds = dtype == VB_F32 ? k32 : k16;
   const int nk = dtype == VB_F32 ? 3 : 4;
   const long long stages = (K * (long long)elem_size(dtype) + 63) / 64;
