@@ -556,52 +556,63 @@ __global__ __launch_bounds__(256) void rows_kernel(Product p) {
 // MFMA steps) and their sums meet in LDS.  Measured at 8 x 4096 -> 16384, bf16: 29.2 us;
 // with eight wavefronts 29.4 (and 63.7 against 60.7 us in float32), with longer runs
 // 30.3, with 32 weight rows per workgroup 61.
+// Weight rows are read in chunks that lie on 16-byte boundaries of memory, wherever the
+// rows start: rows `period` apart (1, 2, 4 or 8) start at one distance `lead` from a
+// boundary, a workgroup takes rows of one distance, and its x chunks start as much
+// earlier.  (7 x 5001 -> 3999 in float16: 20.6 us with weight chunks from the rows' starts,
+// which cross a line every other time.)
 template <typename T, int MB>
-__global__ __launch_bounds__(1024) void narrow_kernel(Product p) {
+__global__ __launch_bounds__(1024) void narrow_kernel(Product p, int period) {
   typedef typename Chunk<T>::type C;
   constexpr int EC = 16 / sizeof(T), U = 2, NW = 16;
   __shared__ __align__(16) float red[NW][MB * 256];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, quarter = lane >> 4;
-  const int n0 = blockIdx.x * 16, chunks = (int)(p.K / EC), tail = (int)(p.K % EC);
-  const T* w = (const T*)p.b + (long long)min(n0 + r16, p.N - 1) * p.ldb;
+  const int like = blockIdx.x % period, n0 = blockIdx.x / period * 16 * period + like;
+  if (like >= p.N) return;  // the whole workgroup
+  const int last = p.N - 1 - (p.N - 1 - like) % period;
+  const T* w = (const T*)p.b + (long long)min(n0 + r16 * period, last) * p.ldb;
+  const int lead = __builtin_amdgcn_readfirstlane((int)((uintptr_t)w % 16 / sizeof(T)));
   const T* x[MB];
 #pragma unroll
   for (int m = 0; m < MB; ++m) x[m] = (const T*)p.a + min((long long)(16 * m + r16), p.M - 1) * p.lda;
   f32x4 acc[MB];
 #pragma unroll
   for (int m = 0; m < MB; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int runs = chunks / (4 * U);
+  // whole chunks first .. end - 1 (chunk c holds elements c EC - lead on), of which runs
+  const int K = (int)p.K, first = lead > 0, end = (lead + K) / EC;
+  const int runs = max(end - first, 0) / (4 * U);
   for (int s = wave; s < runs; s += NW) {
     C wv[U], xv[U][MB];
+    const long long k0 = (long long)(first + s * (4 * U) + quarter) * EC - lead;
 #pragma unroll
-    for (int u = 0; u < U; ++u) wv[u] = load_loose(w + (long long)(s * (4 * U) + u * 4 + quarter) * EC);
+    for (int u = 0; u < U; ++u) wv[u] = *(const C*)(w + k0 + u * 4 * EC);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int m = 0; m < MB; ++m) xv[u][m] = load_loose(x[m] + (long long)(s * (4 * U) + u * 4 + quarter) * EC);
+      for (int m = 0; m < MB; ++m) xv[u][m] = load_loose(x[m] + k0 + u * 4 * EC);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int m = 0; m < MB; ++m) acc[m] = Chunk<T>::mma(wv[u], xv[u][m], acc[m]);
   }
-  // what is left of the reduction, a step of four chunks per wavefront, zeros past its end
-  auto part = [&](const T* q, int c) {
+  // the chunks left over and those that the row fills in part (the first one comes last),
+  // zeros elsewhere, a step of four per wavefront
+  const int rest = first + runs * 4 * U, total = (lead + K + EC - 1) / EC - rest + first;
+  auto part = [&](const T* q, int i) {
+    const int c = i == total - 1 && first ? 0 : rest + i, k0 = c * EC - lead;
     C v;
+    if (i < total && k0 >= 0 && k0 + EC <= K) {
+      v = load_loose(q + k0);
+    } else {
 #pragma unroll
-    for (int e = 0; e < EC; ++e) v[e] = (T)0.f;
-    if (c < chunks) {
-      v = load_loose(q + (long long)c * EC);
-    } else if (c == chunks) {
-#pragma unroll
-      for (int e = 0; e < EC; ++e)
-        if (e < tail) v[e] = q[(long long)c * EC + e];
+      for (int e = 0; e < EC; ++e) v[e] = i < total && k0 + e >= 0 && k0 + e < K ? q[k0 + e] : (T)0.f;
     }
     return v;
   };
-  for (int c0 = runs * 4 * U + wave * 4; c0 < chunks + (tail > 0); c0 += 4 * NW) {
-    const C wv = part(w, c0 + quarter);
+  for (int i0 = wave * 4; i0 < total; i0 += 4 * NW) {
+    const C wv = part(w, i0 + quarter);
 #pragma unroll
-    for (int m = 0; m < MB; ++m) acc[m] = Chunk<T>::mma(wv, part(x[m], c0 + quarter), acc[m]);
+    for (int m = 0; m < MB; ++m) acc[m] = Chunk<T>::mma(wv, part(x[m], i0 + quarter), acc[m]);
   }
 #pragma unroll
   for (int m = 0; m < MB; ++m) *(f32x4*)&red[wave][m * 256 + lane * 4] = acc[m];
@@ -613,15 +624,13 @@ __global__ __launch_bounds__(1024) void narrow_kernel(Product p) {
     float v = 0.f;
 #pragma unroll
     for (int k = 0; k < NW; ++k) v += red[k][at];
-    if (m < p.M && n0 + n < p.N) finish<T, 1>(p, m, n0 + n, &v);
+    if (m < p.M && n0 + n * period < p.N) finish<T, 1>(p, m, n0 + n * period, &v);
   }
 }
 
 template <typename T, int MR>
 hipError_t launch_rows(const Product& p, hipStream_t st) {
-  // four workgroups a CU before a workgroup takes more weight rows; four rows of x are
-  // a little faster here than in narrow_kernel in float32 (53 against 61 us at 4096 ->
-  // 16384), a little slower in 16 bits (31.7 against 29.2)
+  // four workgroups a CU before a workgroup takes more weight rows
   if (p.N >= 4096) rows_kernel<T, MR, 4><<<(p.N + 3) / 4, 256, 0, st>>>(p);
   else if (p.N >= 2048) rows_kernel<T, MR, 2><<<(p.N + 1) / 2, 256, 0, st>>>(p);
   else rows_kernel<T, MR, 1><<<p.N, 256, 0, st>>>(p);
@@ -630,11 +639,20 @@ hipError_t launch_rows(const Product& p, hipStream_t st) {
 
 template <typename T>
 hipError_t launch_narrow(const Product& p, hipStream_t st) {
-  if (p.M == 1) return launch_rows<T, 1>(p, st);
-  if (p.M == 2) return launch_rows<T, 2>(p, st);
-  if (p.M <= 4) return launch_rows<T, 4>(p, st);
-  if (p.M <= 16) narrow_kernel<T, 1><<<(p.N + 15) / 16, 1024, 0, st>>>(p);
-  else narrow_kernel<T, 2><<<(p.N + 15) / 16, 1024, 0, st>>>(p);
+  // One or two rows on the vector units where a row occupies the workgroup (two rows of
+  // 1024 16-bit numbers -> 8192: 8.2 us against 6.1), up to four where there are few
+  // workgroups of the other kind (4 x 8192 -> 1000 in bf16: 8.0 against 14.4 us, 4 x 4096 ->
+  // 4096: 12.9 against 10.2).
+  if (p.M <= 4 && (p.N <= 2048 || (p.M <= 2 && p.K * (long long)sizeof(T) >= 4096))) {
+    if (p.M == 1) return launch_rows<T, 1>(p, st);
+    if (p.M == 2) return launch_rows<T, 2>(p, st);
+    return launch_rows<T, 4>(p, st);
+  }
+  int period = 1;
+  while (period < 16 / (int)sizeof(T) && p.ldb * sizeof(T) * period % 16) period *= 2;
+  const unsigned blocks = (unsigned)(((long long)p.N + 16 * period - 1) / (16 * period) * period);
+  if (p.M <= 16) narrow_kernel<T, 1><<<blocks, 1024, 0, st>>>(p, period);
+  else narrow_kernel<T, 2><<<blocks, 1024, 0, st>>>(p, period);
   return hipGetLastError();
 }
 
@@ -893,15 +911,20 @@ size_t tiling_bytes(const Tiling& t, long long M, int N) {
   return t.splits > 1 ? (size_t)t.splits * M * ((N + 3) / 4 * 4) * 4 : 0;
 }
 
-bool product_is_narrow(const Product& p) { return p.M <= 32 && !p.across_a && !p.across_b; }
+// Up to 16 rows, and up to 32 where the weights are few (24 x 1024 -> 1024 in bf16: 5.2
+// against 7.7 us; 24 x 4096 -> 4096: 14.7 against 13.2).
+bool product_is_narrow(const Product& p, int dtype) {
+  if (p.across_a || p.across_b) return false;
+  return p.M <= 16 || (p.M <= 32 && p.N * p.K * (long long)elem_size(dtype) <= 8 << 20);
+}
 
 size_t product_bytes(const Product& p, int dtype) {
-  if (product_is_narrow(p)) return 0;
+  if (product_is_narrow(p, dtype)) return 0;
   return tiling_bytes(choose_tiling(dtype, p.M, p.N, p.K), p.M, p.N);
 }
 
 hipError_t launch_product(const Product& p, int dtype, hipStream_t st) {
-  if (product_is_narrow(p)) {
+  if (product_is_narrow(p, dtype)) {
     if (dtype == VB_F32) return launch_narrow<float>(p, st);
     if (dtype == VB_BF16) return launch_narrow<bf16>(p, st);
     return launch_narrow<f16>(p, st);

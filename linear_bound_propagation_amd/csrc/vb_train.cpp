@@ -96,7 +96,7 @@ ForwardPlan plan_forward(const vb_linear_fwd& p) {
   d.M = p.rows, d.N = p.n_out, d.K = p.n_in;
   d.bias = p.bias, d.res = p.residual, d.ld_res = p.ld_res;
   d.out = p.y, d.ld_out = p.ld_y, d.pre = p.pre, d.ld_pre = p.ld_pre, d.act = p.act;
-  if (p.rows == 0 || product_is_narrow(d)) return f;
+  if (p.rows == 0 || product_is_narrow(d, p.dtype)) return f;
   const size_t row = chunked_row(p.n_in, p.dtype);
   if (!is_chunked(p.x, p.ld_x, p.n_in, p.dtype)) f.x.take(f.total, p.rows * row);
   if (!is_chunked(p.weight, p.ld_w, p.n_in, p.dtype)) f.w.take(f.total, p.n_out * row);

@@ -16,8 +16,8 @@ vb_status set_error(vb_status s, const char* msg) noexcept;
 inline size_t elem_size(int dtype) { return dtype == VB_F32 ? 4 : 2; }
 
 // C(m, n) = sum_k A(m, k) B(n, k) with A(m, k) = a[m * lda + k], or a[k * lda + m] when
-// across_a (likewise b); across_a implies across_b.  With more than 32 rows, or an
-// operand stored across, both operands are chunked (is_chunked over their rows as
+// across_a (likewise b); across_a implies across_b.  Unless
+// product_is_narrow, both operands are chunked (is_chunked over their rows as
 // stored; a row along the reduction may also be one that launch_pack filled with zeros).
 struct Product {
   const void* a;
@@ -44,7 +44,7 @@ struct Product {
 struct Tiling {
   int bm, bn, splits;
 };
-bool product_is_narrow(const Product& p);
+bool product_is_narrow(const Product& p, int dtype);
 size_t product_bytes(const Product& p, int dtype);
 hipError_t launch_product(const Product& p, int dtype, hipStream_t st);
 

@@ -248,6 +248,24 @@ def test_captured_in_a_graph(lbp, size, dtype):
             assert torch.equal(a, c), i
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 16, 17, 32, 33])
+def test_few_rows_at_every_alignment(lbp, rows, dtype):
+    """Weight rows at every distance from a 16-byte boundary, widths about a whole number of chunks
+    and runs, more and fewer weight rows than a period."""
+    for n_in in (1, 3, 7, 8, 9, 63, 130, 1031, 2303):
+        for n_out in (1, 3, 40, 129, 2100):
+            for shift in (0, 1, 3):
+                if n_out == 2100 and (n_in > 200 or shift):
+                    continue
+                x, w, b, r = case(rows, n_in, n_out, dtype, seed=n_in + n_out)
+                buf = torch.full((n_out * n_in + 16,), float("nan"), dtype=dtype, device="cuda")
+                wv = buf[shift:shift + n_out * n_in].view(n_out, n_in)
+                wv.copy_(w)
+                check_forward(lbp, x, wv, b, r, "none", f"few rows {rows} {n_in} {n_out} {shift} {dtype}")
+    print(f"few rows {rows} {dtype}", flush=True)
+
+
 @pytest.mark.parametrize("size, dtype", [((4090, 4088, 4080), BF16), ((4090, 4088, 4080), F16), ((4091, 1001, 4085), BF16),
                                          ((8190, 72, 2056), F16), ((4090, 400, 4088), F32), ((2041, 1019, 2045), F32),
                                          ((70, 8192, 72), BF16), ((90, 4100, 260), F32), ((2050, 2000, 1030), BF16)],
