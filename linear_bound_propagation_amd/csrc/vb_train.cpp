@@ -265,15 +265,19 @@ extern "C" vb_status vb_cross_entropy(const vb_cross_entropy_args* p, void* ws, 
 
 namespace {
 
-// Workgroups of all tensors, or -1 for a bad size or too many.
-long long clip_blocks(int32_t n, const int64_t* sizes) {
-  long long blocks = 0;
-  for (int32_t i = 0; i < n; ++i) {
-    if (sizes[i] < 0 || sizes[i] > (INT64_C(1) << 44)) return -1;
-    blocks += (sizes[i] + CLIP_CHUNK - 1) / CLIP_CHUNK;
-    if (blocks > 0x7fffffffLL) return -1;
+// Chunks of all tensors, or -1 for a bad size or too many; their size.
+long long clip_chunks(int32_t n, const int64_t* sizes, int& chunk) {
+  for (int c : {CLIP_FEW_CHUNK, CLIP_CHUNK}) {
+    long long count = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      if (sizes[i] < 0 || sizes[i] > (INT64_C(1) << 44)) return -1;
+      count += (sizes[i] + c - 1) / c;
+      if (count > 0x7fffffffLL && c == CLIP_CHUNK) return -1;
+    }
+    chunk = c;
+    if (c == CLIP_CHUNK || count <= CLIP_FEW) return count;
   }
-  return blocks;
+  return -1;
 }
 
 }  // namespace
@@ -282,9 +286,10 @@ extern "C" vb_status vb_clip_grad_norm_workspace(int32_t n_tensors, const int64_
   const char* fn = "vb_clip_grad_norm_workspace";
   if (!bytes) return fail(VB_EINVAL, "%s: bytes is NULL", fn);
   if (n_tensors < 0 || (n_tensors > 0 && !sizes)) return fail(VB_EINVAL, "%s: bad tensor list", fn);
-  const long long blocks = clip_blocks(n_tensors, sizes);
-  if (blocks < 0) return fail(VB_EINVAL, "%s: a size is negative or the total too large", fn);
-  *bytes = align_up(16 + (size_t)blocks * 8);
+  int chunk = 0;
+  const long long chunks = clip_chunks(n_tensors, sizes, chunk);
+  if (chunks < 0) return fail(VB_EINVAL, "%s: a size is negative or the total too large", fn);
+  *bytes = align_up(16 + (size_t)chunks * 8);
   return VB_OK;
 }
 
@@ -331,15 +336,19 @@ extern "C" vb_status vb_clip_grad_norm(int32_t n_tensors, const void* const* gra
     HIPCHK(launch_clip_small(t, max_norm, norm, st));
     return VB_OK;
   }
+  int chunk = 0;
+  const long long chunks = clip_chunks(n_tensors, sizes, chunk);
   float* scale = (float*)ws;
   double* partial = (double*)((char*)ws + 16);
   long long at = 0;
-  while (fill(t, CLIP_CHUNK)) {
+  while (fill(t, chunk)) {
     HIPCHK(launch_clip_partial(t, partial + at, st));
     at += t.first[t.count];
   }
-  HIPCHK(launch_clip_norm(partial, at, max_norm, norm, scale, st));
+  const bool few = chunks <= CLIP_FEW;
+  if (!few) HIPCHK(launch_clip_norm(partial, at, max_norm, norm, scale, st));
   i = 0;
-  while (fill(t, CLIP_CHUNK)) HIPCHK(launch_clip_scale(t, scale, st));
+  for (float* write = norm; fill(t, chunk); write = nullptr)
+    HIPCHK(launch_clip_scale(t, scale, partial, few ? (int)chunks : 0, max_norm, write, st));
   return VB_OK;
 }

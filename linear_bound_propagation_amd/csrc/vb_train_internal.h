@@ -95,9 +95,11 @@ hipError_t launch_cross_entropy(const vb_cross_entropy_args& p, void* ws, hipStr
 // Gradient tensors in the kernels' argument block: CLIP_TENSORS of them at a time, cut
 // into chunks of `chunk` elements.
 constexpr int CLIP_TENSORS = 112;
-constexpr int CLIP_CHUNK = 16384;          // of a workgroup of 256
-constexpr int CLIP_SMALL_CHUNK = 2048;     // of a wavefront, when one workgroup does all:
-constexpr long long CLIP_SMALL = 160 * 1024;  // up to this many elements
+constexpr int CLIP_CHUNK = 16384;        // of a workgroup of 256
+constexpr int CLIP_FEW_CHUNK = 2048;     // the same, while there are at most
+constexpr int CLIP_FEW = 1024;           // this many chunks
+constexpr int CLIP_SMALL_CHUNK = 512;    // of a wavefront, when one workgroup does all:
+constexpr long long CLIP_SMALL = 16384;  // up to this many elements
 struct ClipTable {
   const void* grad[CLIP_TENSORS];
   void* out[CLIP_TENSORS];
@@ -109,7 +111,9 @@ struct ClipTable {
 hipError_t launch_clip_partial(const ClipTable& t, double* partial, hipStream_t st);
 hipError_t launch_clip_norm(const double* partial, long long n, float max_norm, float* norm, float* scale,
                             hipStream_t st);
-hipError_t launch_clip_scale(const ClipTable& t, const float* scale, hipStream_t st);
+// n > 0: the scale from n chunks' sums (norm: written, unless NULL), else from *scale
+hipError_t launch_clip_scale(const ClipTable& t, const float* scale, const double* partial, int n, float max_norm,
+                             float* norm, hipStream_t st);
 hipError_t launch_clip_small(const ClipTable& t, float max_norm, float* norm, hipStream_t st);
 
 }  // namespace vb

@@ -242,14 +242,15 @@ def cross_entropy(logits: torch.Tensor, labels: torch.Tensor, ignore_index: int 
         ld_d = _matrix("dlogits", dlogits, rows, classes, logits)
     elif want_grad:
         dlogits = logits.new_empty((rows, classes))
-    both = torch.empty(rows + 1, dtype=torch.float32, device=logits.device)
+    both = logits.new_empty(rows + 1, dtype=torch.float32)
     base = both.data_ptr()
     if ws is None:
         ws = cross_entropy_workspace(logits)
     p = _LOSS.pack(rows, classes, dt, logits.data_ptr(), ld, labels.data_ptr(), ignore_index, label_smoothing,
                    grad_scale, base + 4 * rows, base, 0 if dlogits is None else dlogits.data_ptr(), ld_d)
     _run("vb_cross_entropy", p, ws.data_ptr(), ws.nbytes, _stream(dev))
-    return both[rows:], both[:rows], dlogits
+    row_loss, loss = both.split((rows, 1))
+    return loss, row_loss, dlogits
 
 
 def clip_grad_norm_workspace(grads: Sequence[torch.Tensor]) -> torch.Tensor:
@@ -270,22 +271,21 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
         types = array("i", [DTYPES[g.dtype] for g in grads])
     except KeyError:
         raise ValueError("gradients must be float32, bfloat16 or float16") from None
-    for i, g in enumerate(grads):
+    for g in grads:
         if g.get_device() != dev or not g.is_contiguous():
-            raise ValueError(f"gradient {i} must be contiguous, on the device of the first")
+            raise ValueError("gradients must be contiguous, on one device")
     sizes = array("q", [g.numel() for g in grads])
     src = array("Q", [g.data_ptr() for g in grads])
     dst = 0
     if out is not None:
         if len(out) != n:
             raise ValueError(f"{len(out)} outputs for {n} gradients")
-        for i, (g, o) in enumerate(zip(grads, out)):
-            if o is not g and (o.shape != g.shape or o.dtype is not g.dtype or o.get_device() != dev
-                               or not o.is_contiguous()):
-                raise ValueError(f"output {i} must be like its gradient: contiguous {g.dtype} {tuple(g.shape)}")
+        for g, o in zip(grads, out):
+            if o.shape != g.shape or o.dtype is not g.dtype or o.get_device() != dev or not o.is_contiguous():
+                raise ValueError(f"an output is not like its gradient: contiguous {g.dtype} {tuple(g.shape)}")
         outs = array("Q", [o.data_ptr() for o in out])
         dst = outs.buffer_info()[0]
-    norm = torch.empty(1, dtype=torch.float32, device=torch.device("cuda", dev))
+    norm = grads[0].new_empty(1, dtype=torch.float32) if n else torch.empty(1, device=torch.device("cuda", dev))
     if ws is None:
         ws = _workspace(_size("vb_clip_grad_norm_workspace", n, sizes.buffer_info()[0]), norm.device)
     _run("vb_clip_grad_norm", n, src.buffer_info()[0], dst or None, sizes.buffer_info()[0], types.buffer_info()[0],
