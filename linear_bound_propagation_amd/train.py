@@ -242,14 +242,12 @@ def cross_entropy(logits: torch.Tensor, labels: torch.Tensor, ignore_index: int 
         ld_d = _matrix("dlogits", dlogits, rows, classes, logits)
     elif want_grad:
         dlogits = logits.new_empty((rows, classes))
-    both = logits.new_empty(rows + 1, dtype=torch.float32)
-    base = both.data_ptr()
+    loss, row_loss = logits.new_empty(1, dtype=torch.float32), logits.new_empty(rows, dtype=torch.float32)
     if ws is None:
         ws = cross_entropy_workspace(logits)
     p = _LOSS.pack(rows, classes, dt, logits.data_ptr(), ld, labels.data_ptr(), ignore_index, label_smoothing,
-                   grad_scale, base + 4 * rows, base, 0 if dlogits is None else dlogits.data_ptr(), ld_d)
+                   grad_scale, loss.data_ptr(), row_loss.data_ptr(), 0 if dlogits is None else dlogits.data_ptr(), ld_d)
     _run("vb_cross_entropy", p, ws.data_ptr(), ws.nbytes, _stream(dev))
-    row_loss, loss = both.split((rows, 1))
     return loss, row_loss, dlogits
 
 
@@ -260,6 +258,18 @@ def clip_grad_norm_workspace(grads: Sequence[torch.Tensor]) -> torch.Tensor:
                       grads[0].device if len(grads) else "cuda")
 
 
+def _tensor_list(name: str, tensors: Sequence[torch.Tensor], dev: int):
+    """Types, sizes and pointers of contiguous tensors on device dev."""
+    for t in tensors:
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, on one device")
+    try:
+        types = array("i", [DTYPES[t.dtype] for t in tensors])
+    except KeyError:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16") from None
+    return types, array("q", [t.numel() for t in tensors]), array("Q", [t.data_ptr() for t in tensors])
+
+
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
                    ws: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, List[torch.Tensor]]:
     """Global norm of the gradients, and the gradients clipped to max_norm (vb_clip_grad_norm):
@@ -267,23 +277,14 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     Tensors are contiguous, of any mix of the three types."""
     n = len(grads)
     dev = _device(grads[0]) if n else torch.cuda.current_device()
-    try:
-        types = array("i", [DTYPES[g.dtype] for g in grads])
-    except KeyError:
-        raise ValueError("gradients must be float32, bfloat16 or float16") from None
-    for g in grads:
-        if g.get_device() != dev or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous, on one device")
-    sizes = array("q", [g.numel() for g in grads])
-    src = array("Q", [g.data_ptr() for g in grads])
+    types, sizes, src = _tensor_list("gradients", grads, dev)
     dst = 0
     if out is not None:
         if len(out) != n:
             raise ValueError(f"{len(out)} outputs for {n} gradients")
-        for g, o in zip(grads, out):
-            if o.shape != g.shape or o.dtype is not g.dtype or o.get_device() != dev or not o.is_contiguous():
-                raise ValueError(f"an output is not like its gradient: contiguous {g.dtype} {tuple(g.shape)}")
-        outs = array("Q", [o.data_ptr() for o in out])
+        out_types, out_sizes, outs = _tensor_list("outputs", out, dev)
+        if out_types != types or out_sizes != sizes:
+            raise ValueError("outputs must have their gradients' types and numbers of elements")
         dst = outs.buffer_info()[0]
     norm = grads[0].new_empty(1, dtype=torch.float32) if n else torch.empty(1, device=torch.device("cuda", dev))
     if ws is None:

@@ -138,3 +138,19 @@ def test_stream_graph_and_repeats(lbp):
         got = [o.clone() for o in out]
         want, res = lbp.clip_grad_norm(grads, 0.1, out=[torch.empty_like(g) for g in grads])
         assert torch.equal(norm, want) and all(torch.equal(a, b) for a, b in zip(got, res)), i
+
+
+def test_refusals_of_the_binding(lbp):
+    """Wrong tensors are refused before anything runs."""
+    g = make([(4, 5), (7,)], (F32,))
+    for grads, out, text in (
+            ([g[0].t(), g[1]], None, "contiguous"), ([g[0], g[1].cpu()], None, "one device"),
+            ([g[0].double()], None, "float32, bfloat16 or float16"), (g, [g[0]], "1 outputs for 2"),
+            (g, [g[0], g[1].to(BF16)], "types"), (g, [g[0], torch.zeros(8, device="cuda")], "numbers of elements"),
+            (g, [g[0], torch.zeros(7)], "one device")):
+        with pytest.raises(ValueError, match=text):
+            lbp.clip_grad_norm(grads, 1.0, out=out)
+    with pytest.raises(lbp.VBError, match="max_norm"):
+        lbp.clip_grad_norm(g, -1.0)
+    with pytest.raises(lbp.VBError, match="workspace too small"):
+        lbp.clip_grad_norm(g, 1.0, ws=torch.empty(8, dtype=torch.uint8, device="cuda"))

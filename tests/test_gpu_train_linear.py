@@ -90,21 +90,21 @@ def test_backward(lbp, size, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("pad, shift", [(8, 0), (5, 0), (16, 8), (3, 1)], ids=str)
-@pytest.mark.parametrize("size", [(1, 96, 40), (37, 120, 72), (200, 250, 136)], ids=str)
+@pytest.mark.parametrize("size", [(1, 96, 40), (12, 301, 77), (37, 120, 72), (200, 250, 136), (300, 515, 129)], ids=str)
 def test_strides_and_alignment(lbp, size, pad, shift, dtype):
     """Operands and outputs inside wider buffers, from an odd element on; nothing outside is written."""
     rows, n_in, n_out = size
     print(f"strides {size} pad {pad} shift {shift} {dtype}", flush=True)
 
-    def inside(t):
-        buf = torch.full((t.shape[0], t.shape[1] + pad), 7.0, dtype=dtype, device="cuda")
+    def inside(t, around=float("nan")):
+        buf = torch.full((t.shape[0], t.shape[1] + pad), around, dtype=dtype, device="cuda")
         view = buf[:, shift:shift + t.shape[1]]
         view.copy_(t)
         return buf, view
 
     x, w, b, r = case(*size, dtype, seed=3)
     (_, xv), (_, wv), (_, rv) = inside(x), inside(w), inside(r)
-    ybuf, yv = inside(torch.zeros_like(r))
+    ybuf, yv = inside(torch.zeros_like(r), 7.0)
     check_forward(lbp, xv, wv, b, rv, "silu", "strided", out=yv)
     outside = torch.ones(n_out + pad, dtype=torch.bool, device="cuda")
     outside[shift:shift + n_out] = False
@@ -115,7 +115,7 @@ def test_strides_and_alignment(lbp, size, pad, shift, dtype):
     check_backward(lbp, dyv, xv, wv, None, "none", "strided")
     # y over the residual
     alias = rv.clone()
-    buf, av = inside(alias)
+    buf, av = inside(alias, 7.0)
     y = lbp.linear(xv, wv, b, av, act="relu", out=av)
     assert y is av and torch.equal(y, lbp.linear(xv, wv, b, rv, act="relu"))
     assert (buf[:, outside] == 7.0).all()
@@ -280,3 +280,23 @@ def test_large_products(lbp, size, dtype):
     dy = normal(gen(71), rows, n_out, std=rows ** -0.5, dtype=dtype)
     check_backward(lbp, dy, x, w, None, "none", f"large {size}")
     check_backward(lbp, dy, x, w, r, "silu", f"large {size}")
+
+
+def test_refusals_of_the_binding(lbp):
+    x, w, b, r = case(6, 8, 5, F32)
+    for call, text in (
+            (lambda: lbp.linear(x, w.t()), "weight"), (lambda: lbp.linear(x.t(), w), "contiguous|weight"),
+            (lambda: lbp.linear(x, w.half()), "weight"), (lambda: lbp.linear(x, w.cpu()), "weight"),
+            (lambda: lbp.linear(x, w, b[:4]), "bias"), (lambda: lbp.linear(x, w, b, r[:5]), "residual"),
+            (lambda: lbp.linear(x, w, act="tanh"), "act"), (lambda: lbp.linear(x[0], w), "matrices"),
+            (lambda: lbp.linear(x, w, out=r[:, :4]), "out"), (lambda: lbp.linear(x.double(), w.double()), "float32"),
+            (lambda: lbp.linear_backward(r, x, w, act="relu"), "saved"),
+            (lambda: lbp.linear_backward(r, x, w, saved=r), "saved"),
+            (lambda: lbp.linear_backward(r[:5], x, w), "dy"),
+            (lambda: lbp.linear_backward(r, x, w, act="gelu", saved=r.half()), "saved")):
+        with pytest.raises(ValueError, match=text):
+            call()
+    with pytest.raises(lbp.VBError, match="nothing to compute"):
+        lbp.linear_backward(r, x, w, want_x=False, want_weight=False, want_bias=False)
+    with pytest.raises(lbp.VBError, match="leading dimension"):        # a broadcast residual has no rows
+        lbp.linear(x, w, b, r[:1].expand(6, 5))

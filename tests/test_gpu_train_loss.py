@@ -106,7 +106,7 @@ def test_masked_classes_and_odd_rows(lbp, classes, dtype):
 @pytest.mark.parametrize("classes", [10, 1001, 40004, 130001])
 def test_strides_and_in_place(lbp, classes, pad, shift, dtype):
     z, y = make(6, classes, dtype, seed=9)
-    buf = torch.full((6, classes + pad), 7.0, dtype=dtype, device="cuda")
+    buf = torch.full((6, classes + pad), float("nan"), dtype=dtype, device="cuda")
     view = buf[:, shift:shift + classes]
     view.copy_(z)
     print(f"strided {classes} {pad} {shift} {dtype}", flush=True)
@@ -121,7 +121,7 @@ def test_strides_and_in_place(lbp, classes, pad, shift, dtype):
     assert (out[:, outside] == 5.0).all()
     loss, row, grad = lbp.cross_entropy(view, y, label_smoothing=0.1, dlogits=view)     # over the logits
     assert grad is view and torch.equal(view, got[2]) and torch.equal(row, got[1]) and torch.equal(loss, got[0])
-    assert (buf[:, outside] == 7.0).all()
+    assert torch.isnan(buf[:, outside]).all()
     assert want[1].shape == row.shape
 
 
@@ -178,3 +178,17 @@ def test_stream_graph_and_repeats(lbp):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, lbp.cross_entropy(z, y))), i
+
+
+def test_refusals_of_the_binding(lbp):
+    z, y = make(6, 9, torch.float32, seed=1)
+    for call, text in (
+            (lambda: lbp.cross_entropy(z[0], y), "matrix"), (lambda: lbp.cross_entropy(z.t(), y), "contiguous"),
+            (lambda: lbp.cross_entropy(z, y.int()), "labels"), (lambda: lbp.cross_entropy(z, y[:5]), "labels"),
+            (lambda: lbp.cross_entropy(z, y.cpu()), "labels"), (lambda: lbp.cross_entropy(z.double(), y), "float32"),
+            (lambda: lbp.cross_entropy(z, y, dlogits=z[:, :8]), "dlogits"),
+            (lambda: lbp.cross_entropy(z, y, dlogits=z.half()), "dlogits")):
+        with pytest.raises(ValueError, match=text):
+            call()
+    with pytest.raises(lbp.VBError, match="label_smoothing"):
+        lbp.cross_entropy(z, y, label_smoothing=2.0)
