@@ -20,7 +20,8 @@ namespace vb {
 namespace {
 
 // tensor of chunk b: the last one whose first chunk is not after it
-__device__ __forceinline__ int clip_tensor(const ClipTable& t, unsigned b) {
+template <int N>
+__device__ __forceinline__ int clip_tensor(const ClipTable<N>& t, unsigned b) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -82,8 +83,8 @@ __device__ __forceinline__ void scaled(const void* p, void* q, long long beg, lo
   if (tid < n - full * EC) o[full * EC + tid] = from_f32<T>(to_f32(g[full * EC + tid]) * s);
 }
 
-template <int TH>
-__device__ __forceinline__ double chunk_squares(const ClipTable& t, unsigned b, int tid) {
+template <int TH, int N>
+__device__ __forceinline__ double chunk_squares(const ClipTable<N>& t, unsigned b, int tid) {
   const int i = clip_tensor(t, b);
   const long long beg = (long long)(b - t.first[i]) * t.chunk, end = min(t.n[i], beg + t.chunk);
   if (t.dtype[i] == VB_F32) return squares<float, TH>(t.grad[i], beg, end, tid);
@@ -91,8 +92,8 @@ __device__ __forceinline__ double chunk_squares(const ClipTable& t, unsigned b, 
   return squares<f16, TH>(t.grad[i], beg, end, tid);
 }
 
-template <int TH>
-__device__ __forceinline__ void chunk_scaled(const ClipTable& t, unsigned b, int tid, float s) {
+template <int TH, int N>
+__device__ __forceinline__ void chunk_scaled(const ClipTable<N>& t, unsigned b, int tid, float s) {
   const int i = clip_tensor(t, b);
   if (s == 1.f && t.out[i] == t.grad[i]) return;
   const long long beg = (long long)(b - t.first[i]) * t.chunk, end = min(t.n[i], beg + t.chunk);
@@ -122,7 +123,8 @@ __device__ __forceinline__ float clip_factor(double squares, float max_norm, flo
   return v > (double)max_norm && (float)v < INFINITY ? (float)((double)max_norm / v) : 1.f;
 }
 
-__global__ __launch_bounds__(256) void clip_partial_kernel(ClipTable t, double* partial) {
+template <int N>
+__global__ __launch_bounds__(256) void clip_partial_kernel(ClipTable<N> t, double* partial) {
   const double s = block_sum<256>(chunk_squares<256>(t, blockIdx.x, threadIdx.x));
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
@@ -137,7 +139,8 @@ __global__ __launch_bounds__(1024) void clip_norm_kernel(const double* partial, 
 }
 
 // n > 0: from the chunks' sums (the first launch's last workgroup writes the norm)
-__global__ __launch_bounds__(256) void clip_scale_kernel(ClipTable t, const float* scale, const double* partial, int n,
+template <int N>
+__global__ __launch_bounds__(256) void clip_scale_kernel(ClipTable<N> t, const float* scale, const double* partial, int n,
                                                          float max_norm, float* norm) {
   float f;
   if (n > 0) {
@@ -151,7 +154,8 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(ClipTable t, const floa
 }
 
 // Everything at once: a chunk per wavefront at a time.
-__global__ __launch_bounds__(1024) void clip_small_kernel(ClipTable t, float max_norm, float* norm) {
+template <int N>
+__global__ __launch_bounds__(1024) void clip_small_kernel(ClipTable<N> t, float max_norm, float* norm) {
   const unsigned chunks = t.first[t.count];
   double s = 0.0;
   for (unsigned b = threadIdx.x >> 6; b < chunks; b += 16) s += chunk_squares<64>(t, b, threadIdx.x & 63);
@@ -162,7 +166,8 @@ __global__ __launch_bounds__(1024) void clip_small_kernel(ClipTable t, float max
 
 }  // namespace
 
-hipError_t launch_clip_partial(const ClipTable& t, double* partial, hipStream_t st) {
+template <int N>
+hipError_t launch_clip_partial(const ClipTable<N>& t, double* partial, hipStream_t st) {
   clip_partial_kernel<<<t.first[t.count], 256, 0, st>>>(t, partial);
   return hipGetLastError();
 }
@@ -173,15 +178,26 @@ hipError_t launch_clip_norm(const double* partial, long long n, float max_norm, 
   return hipGetLastError();
 }
 
-hipError_t launch_clip_scale(const ClipTable& t, const float* scale, const double* partial, int n, float max_norm,
+template <int N>
+hipError_t launch_clip_scale(const ClipTable<N>& t, const float* scale, const double* partial, int n, float max_norm,
                              float* norm, hipStream_t st) {
   clip_scale_kernel<<<t.first[t.count], 256, 0, st>>>(t, scale, partial, n, max_norm, norm);
   return hipGetLastError();
 }
 
-hipError_t launch_clip_small(const ClipTable& t, float max_norm, float* norm, hipStream_t st) {
+template <int N>
+hipError_t launch_clip_small(const ClipTable<N>& t, float max_norm, float* norm, hipStream_t st) {
   clip_small_kernel<<<1, 1024, 0, st>>>(t, max_norm, norm);
   return hipGetLastError();
 }
+
+template hipError_t launch_clip_partial(const ClipTable<CLIP_TENSORS>&, double*, hipStream_t);
+template hipError_t launch_clip_partial(const ClipTable<CLIP_FEW_TENSORS>&, double*, hipStream_t);
+template hipError_t launch_clip_scale(const ClipTable<CLIP_TENSORS>&, const float*, const double*, int, float, float*,
+                                      hipStream_t);
+template hipError_t launch_clip_scale(const ClipTable<CLIP_FEW_TENSORS>&, const float*, const double*, int, float,
+                                      float*, hipStream_t);
+template hipError_t launch_clip_small(const ClipTable<CLIP_TENSORS>&, float, float*, hipStream_t);
+template hipError_t launch_clip_small(const ClipTable<CLIP_FEW_TENSORS>&, float, float*, hipStream_t);
 
 }  // namespace vb

@@ -280,6 +280,62 @@ long long clip_chunks(int32_t n, const int64_t* sizes, int& chunk) {
   return -1;
 }
 
+struct ClipCall {
+  int32_t n_tensors;
+  const void* const* grads;
+  void* const* out;
+  const int64_t* sizes;
+  const int32_t* dtypes;
+  float max_norm;
+  float* norm;
+  void* ws;
+  hipStream_t st;
+};
+
+template <int N>
+vb_status run_clip(const ClipCall& c) {
+  // the next tensors, from number i on, in chunks of `chunk`
+  int32_t i = 0;
+  auto fill = [&](ClipTable<N>& t, int chunk) {
+    t.count = 0;
+    t.chunk = chunk;
+    t.first[0] = 0;
+    for (; i < c.n_tensors && t.count < N; ++i) {
+      if (c.sizes[i] == 0) continue;
+      const int k = t.count++;
+      t.grad[k] = c.grads[i];
+      t.out[k] = c.out ? c.out[i] : (void*)c.grads[i];
+      t.n[k] = c.sizes[i];
+      t.dtype[k] = (unsigned char)c.dtypes[i];
+      t.first[k + 1] = t.first[k] + (unsigned)((c.sizes[i] + chunk - 1) / chunk);
+    }
+    return t.count > 0;
+  };
+  ClipTable<N> t;
+  long long total = 0;
+  for (int32_t k = 0; k < c.n_tensors; ++k) total += c.sizes[k];
+  if (total <= CLIP_SMALL && c.n_tensors <= N) {
+    fill(t, CLIP_SMALL_CHUNK);
+    HIPCHK(launch_clip_small(t, c.max_norm, c.norm, c.st));
+    return VB_OK;
+  }
+  int chunk = 0;
+  const long long chunks = clip_chunks(c.n_tensors, c.sizes, chunk);
+  float* scale = (float*)c.ws;
+  double* partial = (double*)((char*)c.ws + 16);
+  long long at = 0;
+  while (fill(t, chunk)) {
+    HIPCHK(launch_clip_partial(t, partial + at, c.st));
+    at += t.first[t.count];
+  }
+  const bool few = chunks <= CLIP_FEW;
+  if (!few) HIPCHK(launch_clip_norm(partial, at, c.max_norm, c.norm, scale, c.st));
+  i = 0;
+  for (float* write = c.norm; fill(t, chunk); write = nullptr)
+    HIPCHK(launch_clip_scale(t, scale, partial, few ? (int)chunks : 0, c.max_norm, write, c.st));
+  return VB_OK;
+}
+
 }  // namespace
 
 extern "C" vb_status vb_clip_grad_norm_workspace(int32_t n_tensors, const int64_t* sizes, size_t* bytes) {
@@ -310,45 +366,6 @@ extern "C" vb_status vb_clip_grad_norm(int32_t n_tensors, const void* const* gra
       return fail(VB_EINVAL, "%s: pointer of tensor %d is NULL or misaligned", fn, i);
   }
   TRY(check_ws(fn, ws, ws_bytes, need));
-  const hipStream_t st = (hipStream_t)stream;
-  // the next tensors, from number i on, in chunks of `chunk`
-  int32_t i = 0;
-  auto fill = [&](ClipTable& t, int chunk) {
-    t.count = 0;
-    t.chunk = chunk;
-    t.first[0] = 0;
-    for (; i < n_tensors && t.count < CLIP_TENSORS; ++i) {
-      if (sizes[i] == 0) continue;
-      const int c = t.count++;
-      t.grad[c] = grads[i];
-      t.out[c] = out ? out[i] : (void*)grads[i];
-      t.n[c] = sizes[i];
-      t.dtype[c] = (unsigned char)dtypes[i];
-      t.first[c + 1] = t.first[c] + (unsigned)((sizes[i] + chunk - 1) / chunk);
-    }
-    return t.count > 0;
-  };
-  ClipTable t;
-  long long total = 0;
-  for (int32_t k = 0; k < n_tensors; ++k) total += sizes[k];
-  if (total <= CLIP_SMALL && n_tensors <= CLIP_TENSORS) {
-    fill(t, CLIP_SMALL_CHUNK);
-    HIPCHK(launch_clip_small(t, max_norm, norm, st));
-    return VB_OK;
-  }
-  int chunk = 0;
-  const long long chunks = clip_chunks(n_tensors, sizes, chunk);
-  float* scale = (float*)ws;
-  double* partial = (double*)((char*)ws + 16);
-  long long at = 0;
-  while (fill(t, chunk)) {
-    HIPCHK(launch_clip_partial(t, partial + at, st));
-    at += t.first[t.count];
-  }
-  const bool few = chunks <= CLIP_FEW;
-  if (!few) HIPCHK(launch_clip_norm(partial, at, max_norm, norm, scale, st));
-  i = 0;
-  for (float* write = norm; fill(t, chunk); write = nullptr)
-    HIPCHK(launch_clip_scale(t, scale, partial, few ? (int)chunks : 0, max_norm, write, st));
-  return VB_OK;
+  const ClipCall c{n_tensors, grads, out, sizes, dtypes, max_norm, norm, ws, (hipStream_t)stream};
+  return n_tensors <= CLIP_FEW_TENSORS ? run_clip<CLIP_FEW_TENSORS>(c) : run_clip<CLIP_TENSORS>(c);
 }

@@ -92,28 +92,33 @@ hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long l
 // ws: one int64 (count of the rows that are not ignored)
 hipError_t launch_cross_entropy(const vb_cross_entropy_args& p, void* ws, hipStream_t st);
 
-// Gradient tensors in the kernels' argument block: CLIP_TENSORS of them at a time, cut
-// into chunks of `chunk` elements.
-constexpr int CLIP_TENSORS = 112;
+// Gradient tensors in the kernels' argument block, cut into chunks of `chunk` elements:
+// up to CLIP_TENSORS of them at a time, or CLIP_FEW_TENSORS in a block an eighth as long
+// (six tensors: 8.3 us a call against 8.9).
+constexpr int CLIP_TENSORS = 112, CLIP_FEW_TENSORS = 16;
 constexpr int CLIP_CHUNK = 16384;        // of a workgroup of 256
 constexpr int CLIP_FEW_CHUNK = 2048;     // the same, while there are at most
 constexpr int CLIP_FEW = 1024;           // this many chunks
 constexpr int CLIP_SMALL_CHUNK = 512;    // of a wavefront, when one workgroup does all:
 constexpr long long CLIP_SMALL = 16384;  // up to this many elements
+template <int N>
 struct ClipTable {
-  const void* grad[CLIP_TENSORS];
-  void* out[CLIP_TENSORS];
-  long long n[CLIP_TENSORS];
-  unsigned first[CLIP_TENSORS + 1];  // chunks before tensor i of this launch
-  unsigned char dtype[CLIP_TENSORS];
+  const void* grad[N];
+  void* out[N];
+  long long n[N];
+  unsigned first[N + 1];  // chunks before tensor i of this launch
+  unsigned char dtype[N];
   int count, chunk;
 };
-hipError_t launch_clip_partial(const ClipTable& t, double* partial, hipStream_t st);
+template <int N>
+hipError_t launch_clip_partial(const ClipTable<N>& t, double* partial, hipStream_t st);
 hipError_t launch_clip_norm(const double* partial, long long n, float max_norm, float* norm, float* scale,
                             hipStream_t st);
 // n > 0: the scale from n chunks' sums (norm: written, unless NULL), else from *scale
-hipError_t launch_clip_scale(const ClipTable& t, const float* scale, const double* partial, int n, float max_norm,
+template <int N>
+hipError_t launch_clip_scale(const ClipTable<N>& t, const float* scale, const double* partial, int n, float max_norm,
                              float* norm, hipStream_t st);
-hipError_t launch_clip_small(const ClipTable& t, float max_norm, float* norm, hipStream_t st);
+template <int N>
+hipError_t launch_clip_small(const ClipTable<N>& t, float max_norm, float* norm, hipStream_t st);
 
 }  // namespace vb
