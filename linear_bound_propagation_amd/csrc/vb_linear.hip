@@ -82,24 +82,24 @@ __device__ __forceinline__ float act_grad(float dy, float s, int act) {
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
-// 16 bytes of a row; mma: the products of a wavefront's 64 chunks (16 rows x 4) of each operand
+// 16 bytes of a row; mma: MFMA s of the MFMAS that multiply a wavefront's 64 chunks (16
+// rows x 4) of each operand.  The MFMAs of one block of outputs wait for each other, so
+// other blocks come between (float32, one after the other: 75 % of the rate).
 template <typename T>
 struct Chunk;
 template <>
 struct Chunk<float> {
   typedef f32x4 type;
   static constexpr int MFMAS = 4;
-  __device__ static f32x4 mma(f32x4 a, f32x4 b, f32x4 c) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], c, 0, 0, 0);
-    return c;
+  __device__ static f32x4 mma(f32x4 a, f32x4 b, f32x4 c, int s) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], c, 0, 0, 0);
   }
 };
 template <>
 struct Chunk<bf16> {
   typedef bf16x8 type;
   static constexpr int MFMAS = 1;
-  __device__ static f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  __device__ static f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c, int) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
 };
@@ -107,7 +107,7 @@ template <>
 struct Chunk<f16> {
   typedef f16x8 type;
   static constexpr int MFMAS = 1;
-  __device__ static f32x4 mma(f16x8 a, f16x8 b, f32x4 c) {
+  __device__ static f32x4 mma(f16x8 a, f16x8 b, f32x4 c, int) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
 };
@@ -125,11 +125,11 @@ __device__ const u32x4 zero_chunk = {0, 0, 0, 0};
 __device__ __forceinline__ unsigned lds_address(const void* l) {
   return __builtin_amdgcn_readfirstlane((unsigned)(unsigned long long)(__attribute__((address_space(3))) const void*)l);
 }
-__device__ __forceinline__ void load_to_lds(const void* base, unsigned off, const void* l) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_address(l)), "v"(off), "s"(base));
+__device__ __forceinline__ void load_to_lds(const void* base, unsigned off, unsigned l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(l), "v"(off), "s"(base));
 }
-__device__ __forceinline__ void load_to_lds(const void* g, const void* l) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_address(l)), "v"(g));
+__device__ __forceinline__ void load_to_lds(const void* g, unsigned l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(l), "v"(g));
 }
 
 // The activation of VEC values; one branch for all of them.
@@ -258,13 +258,13 @@ struct Operand {
     }
   }
   // a stage that the reduction fills
-  __device__ void load(int t, char* lds) const {
+  __device__ void load(int t, unsigned lds) const {
     const char* at = base + t * step;
 #pragma unroll
     for (int i = 0; i < L; ++i) load_to_lds(at, off[i], lds + (i * NW + wave) * 1024);
   }
   // any stage: zeros past the end of the reduction's K elements
-  __device__ void load_part(int t, char* lds, int K) const {
+  __device__ void load_part(int t, unsigned lds, int K) const {
     const char* at = base + t * step;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
@@ -327,8 +327,9 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Pr
   OB b;
   a.init(p.a, p.lda, m0, p.M, first, wave, lane);
   b.init(p.b, p.ldb, n0, p.N, first, wave, lane);
-  auto issue = [&](int t, int base) { a.load(t, lds + base), b.load(t, lds + base + BM * DEPTH); };
-  auto issue_part = [&](int t, int base) { a.load_part(t, lds + base, K), b.load_part(t, lds + base + BM * DEPTH, K); };
+  const unsigned lds0 = lds_address(lds);
+  auto issue = [&](int t, int base) { a.load(t, lds0 + base), b.load(t, lds0 + base + BM * DEPTH); };
+  auto issue_part = [&](int t, int base) { a.load_part(t, lds0 + base, K), b.load_part(t, lds0 + base + BM * DEPTH, K); };
   // The next stage has landed (all but the loads of the NS - 2 stages after it), this
   // wavefront has its reads of the last stage, and so have the others.
   auto join = [] {
@@ -358,9 +359,11 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Pr
   };
   auto multiply = [&](int h, int f) {
 #pragma unroll
-    for (int i = h * MH; i < h * MH + MH; ++i)
+    for (int s = 0; s < Chunk<T>::MFMAS; ++s)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = Chunk<T>::mma(fa[i], fb[f][j], acc[i][j]);
+      for (int i = h * MH; i < h * MH + MH; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = Chunk<T>::mma(fa[i], fb[f][j], acc[i][j], s);
   };
   auto after = [](int base, int n) {  // the ring position n stages on
     const int x = base + n * STAGE;
@@ -593,7 +596,9 @@ __global__ __launch_bounds__(1024) void narrow_kernel(Product p, int period) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int m = 0; m < MB; ++m) acc[m] = Chunk<T>::mma(wv[u], xv[u][m], acc[m]);
+      for (int q = 0; q < Chunk<T>::MFMAS; ++q)
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[m] = Chunk<T>::mma(wv[u], xv[u][m], acc[m], q);
   }
   // the chunks left over and those that the row fills in part (the first one comes last),
   // zeros elsewhere, a step of four per wavefront
@@ -612,7 +617,11 @@ __global__ __launch_bounds__(1024) void narrow_kernel(Product p, int period) {
   for (int i0 = wave * 4; i0 < total; i0 += 4 * NW) {
     const C wv = part(w, i0 + quarter);
 #pragma unroll
-    for (int m = 0; m < MB; ++m) acc[m] = Chunk<T>::mma(wv, part(x[m], i0 + quarter), acc[m]);
+    for (int m = 0; m < MB; ++m) {
+      const C xv = part(x[m], i0 + quarter);
+#pragma unroll
+      for (int q = 0; q < Chunk<T>::MFMAS; ++q) acc[m] = Chunk<T>::mma(wv, xv, acc[m], q);
+    }
   }
 #pragma unroll
   for (int m = 0; m < MB; ++m) *(f32x4*)&red[wave][m * 256 + lane * 4] = acc[m];
