@@ -554,51 +554,66 @@ __global__ __launch_bounds__(256) void rows_kernel(Product p) {
   }
 }
 
-// Up to 16 MB rows: 16 weight rows per workgroup along the MFMA rows, the x rows along
-// its columns; the 16 wavefronts take runs of 128 bytes of the reduction in turn (two
-// MFMA steps) and their sums meet in LDS.  Measured at 8 x 4096 -> 16384, bf16: 29.2 us;
-// with eight wavefronts 29.4 (and 63.7 against 60.7 us in float32), with longer runs
-// 30.3, with 32 weight rows per workgroup 61.
+// Up to 16 MB rows: 16 NB weight rows per workgroup along the MFMA rows, the x rows along
+// its columns; the NW wavefronts take runs of 128 bytes of the reduction in turn (two
+// MFMA steps) and their sums meet in LDS.  Many wavefronts on 16 weight rows where those
+// are needed to fill the card, else four on 64, which read x a quarter as often; a
+// workgroup's first run is its number's, as workgroups that went through the reduction
+// in step would read the same memory channels (32 weight rows: 38 against 28.5 us).
+// Measured at 16 x 4096 -> 16384 | 16 x 4096 -> 4096, bf16: 35.5 | 12.8 us and 26.4 | 22.1
+// us (float32 75 | 22.8 and 50 | 41); longer runs and other numbers lie between.
 // Weight rows are read in chunks that lie on 16-byte boundaries of memory, wherever the
 // rows start: rows `period` apart (1, 2, 4 or 8) start at one distance `lead` from a
 // boundary, a workgroup takes rows of one distance, and its x chunks start as much
 // earlier.  (7 x 5001 -> 3999 in float16: 20.6 us with weight chunks from the rows' starts,
-// which cross a line every other time.)
-template <typename T, int MB>
-__global__ __launch_bounds__(1024) void narrow_kernel(Product p, int period) {
+// which cross a line every other time, 13.5 so.)
+template <typename T, int MB, int NB, int NW>
+__global__ __launch_bounds__(64 * NW) void narrow_kernel(Product p, int period) {
   typedef typename Chunk<T>::type C;
-  constexpr int EC = 16 / sizeof(T), U = 2, NW = 16;
-  __shared__ __align__(16) float red[NW][MB * 256];
+  constexpr int EC = 16 / sizeof(T), U = 2, OUT = MB * NB * 256;
+  __shared__ __align__(16) float red[NW][OUT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, quarter = lane >> 4;
-  const int like = blockIdx.x % period, n0 = blockIdx.x / period * 16 * period + like;
+  const int like = blockIdx.x % period, n0 = blockIdx.x / period * (16 * NB) * period + like;
   if (like >= p.N) return;  // the whole workgroup
   const int last = p.N - 1 - (p.N - 1 - like) % period;
-  const T* w = (const T*)p.b + (long long)min(n0 + r16 * period, last) * p.ldb;
-  const int lead = __builtin_amdgcn_readfirstlane((int)((uintptr_t)w % 16 / sizeof(T)));
+  const T* w[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) w[b] = (const T*)p.b + (long long)min(n0 + (16 * b + r16) * period, last) * p.ldb;
+  const int lead = __builtin_amdgcn_readfirstlane((int)((uintptr_t)w[0] % 16 / sizeof(T)));
   const T* x[MB];
 #pragma unroll
   for (int m = 0; m < MB; ++m) x[m] = (const T*)p.a + min((long long)(16 * m + r16), p.M - 1) * p.lda;
-  f32x4 acc[MB];
+  f32x4 acc[NB][MB];
 #pragma unroll
-  for (int m = 0; m < MB; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int m = 0; m < MB; ++m) acc[b][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const C* wv, const C* xv) {
+#pragma unroll
+    for (int q = 0; q < Chunk<T>::MFMAS; ++q)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[b][m] = Chunk<T>::mma(wv[b], xv[m], acc[b][m], q);
+  };
   // whole chunks first .. end - 1 (chunk c holds elements c EC - lead on), of which runs
   const int K = (int)p.K, first = lead > 0, end = (lead + K) / EC;
   const int runs = max(end - first, 0) / (4 * U);
+  const int turn = runs ? (int)(blockIdx.x % (unsigned)runs) : 0;
   for (int s = wave; s < runs; s += NW) {
-    C wv[U], xv[U][MB];
-    const long long k0 = (long long)(first + s * (4 * U) + quarter) * EC - lead;
+    const int run = s + turn < runs ? s + turn : s + turn - runs;
+    C wv[U][NB], xv[U][MB];
+    const long long k0 = (long long)(first + run * (4 * U) + quarter) * EC - lead;
 #pragma unroll
-    for (int u = 0; u < U; ++u) wv[u] = *(const C*)(w + k0 + u * 4 * EC);
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int u = 0; u < U; ++u) wv[u][b] = *(const C*)(w[b] + k0 + u * 4 * EC);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int m = 0; m < MB; ++m) xv[u][m] = load_loose(x[m] + k0 + u * 4 * EC);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int q = 0; q < Chunk<T>::MFMAS; ++q)
-#pragma unroll
-        for (int m = 0; m < MB; ++m) acc[m] = Chunk<T>::mma(wv[u], xv[u][m], acc[m], q);
+    for (int u = 0; u < U; ++u) multiply(wv[u], xv[u]);
   }
   // the chunks left over and those that the row fills in part (the first one comes last),
   // zeros elsewhere, a step of four per wavefront
@@ -615,21 +630,21 @@ __global__ __launch_bounds__(1024) void narrow_kernel(Product p, int period) {
     return v;
   };
   for (int i0 = wave * 4; i0 < total; i0 += 4 * NW) {
-    const C wv = part(w, i0 + quarter);
+    C wv[NB], xv[MB];
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      const C xv = part(x[m], i0 + quarter);
+    for (int b = 0; b < NB; ++b) wv[b] = part(w[b], i0 + quarter);
 #pragma unroll
-      for (int q = 0; q < Chunk<T>::MFMAS; ++q) acc[m] = Chunk<T>::mma(wv, xv, acc[m], q);
-    }
+    for (int m = 0; m < MB; ++m) xv[m] = part(x[m], i0 + quarter);
+    multiply(wv, xv);
   }
 #pragma unroll
-  for (int m = 0; m < MB; ++m) *(f32x4*)&red[wave][m * 256 + lane * 4] = acc[m];
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int m = 0; m < MB; ++m) *(f32x4*)&red[wave][(b * MB + m) * 256 + lane * 4] = acc[b][m];
   __syncthreads();
-  const int o = threadIdx.x;
-  if (o < MB * 256) {
-    const int n = o % 16, m = o / 16;
-    const int at = (m >> 4) * 256 + ((n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+  for (int o = threadIdx.x; o < OUT; o += 64 * NW) {
+    const int n = o % (16 * NB), m = o / (16 * NB);
+    const int at = ((n >> 4) * MB + (m >> 4)) * 256 + (((n >> 2) & 3) * 16 + (m & 15)) * 4 + (n & 3);
     float v = 0.f;
 #pragma unroll
     for (int k = 0; k < NW; ++k) v += red[k][at];
@@ -659,9 +674,15 @@ hipError_t launch_narrow(const Product& p, hipStream_t st) {
   }
   int period = 1;
   while (period < 16 / (int)sizeof(T) && p.ldb * sizeof(T) * period % 16) period *= 2;
-  const unsigned blocks = (unsigned)(((long long)p.N + 16 * period - 1) / (16 * period) * period);
-  if (p.M <= 16) narrow_kernel<T, 1><<<blocks, 1024, 0, st>>>(p, period);
-  else narrow_kernel<T, 2><<<blocks, 1024, 0, st>>>(p, period);
+  auto blocks = [&](int rows) { return (unsigned)((p.N + rows * period - 1LL) / (rows * period) * period); };
+  const bool many = blocks(64) >= 200;
+  if (p.M <= 16) {
+    if (many) narrow_kernel<T, 1, 4, 4><<<blocks(64), 256, 0, st>>>(p, period);
+    else narrow_kernel<T, 1, 1, 16><<<blocks(16), 1024, 0, st>>>(p, period);
+  } else {
+    if (many) narrow_kernel<T, 2, 4, 4><<<blocks(64), 256, 0, st>>>(p, period);
+    else narrow_kernel<T, 2, 1, 16><<<blocks(16), 1024, 0, st>>>(p, period);
+  }
   return hipGetLastError();
 }
 
@@ -921,10 +942,12 @@ size_t tiling_bytes(const Tiling& t, long long M, int N) {
 }
 
 // Up to 16 rows, and up to 32 where the weights are few (24 x 1024 -> 1024 in bf16: 5.2
-// against 7.7 us; 24 x 4096 -> 4096: 14.7 against 13.2).
+// against 7.7 us; 24 x 4096 -> 4096: 14.7 against 13.2) or long and many (32 x 4096 ->
+// 16384: 34 against 37, float32 63 against 72; 32 x 1024 -> 65536: 36 against 31).
 bool product_is_narrow(const Product& p, int dtype) {
   if (p.across_a || p.across_b) return false;
-  return p.M <= 16 || (p.M <= 32 && p.N * p.K * (long long)elem_size(dtype) <= 8 << 20);
+  const long long row = p.K * (long long)elem_size(dtype);
+  return p.M <= 16 || (p.M <= 32 && (p.N * row <= 8 << 20 || (p.N >= 12800 && row >= 8192)));
 }
 
 size_t product_bytes(const Product& p, int dtype) {

@@ -263,6 +263,10 @@ def test_few_rows_at_every_alignment(lbp, rows, dtype):
                 wv = buf[shift:shift + n_out * n_in].view(n_out, n_in)
                 wv.copy_(w)
                 check_forward(lbp, x, wv, b, r, "none", f"few rows {rows} {n_in} {n_out} {shift} {dtype}")
+    # workgroups of 64 weight rows
+    for n_in, n_out in ((40, 12801), (77, 13001), (2056, 12810)):
+        x, w, b, r = case(rows, n_in, n_out, dtype, seed=n_in)
+        check_forward(lbp, x, w, b, r, "relu", f"few rows {rows} {n_in} {n_out} {dtype}")
     print(f"few rows {rows} {dtype}", flush=True)
 
 
