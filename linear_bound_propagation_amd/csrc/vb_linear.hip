@@ -52,31 +52,36 @@ __device__ __forceinline__ float act_grad(float dy, float s, int act) {
 // and x for dweight); rows start on 16-byte boundaries.
 //
 // Workgroups of WM x WN wavefronts compute BM x BN tiles.  Both operands pass through
-// a ring of NS stages in LDS, each 64 bytes of the reduction deep (32 16-bit or 16
-// float32 numbers), loaded straight from global memory.  NS - 1 stages are in flight
-// at a time: all workgroups of an XCD reach new memory together, so a stage's first
-// touch waits for HBM.
+// a ring of NS stages in LDS, each 128 or 64 bytes of the reduction deep, loaded straight
+// from global memory.  NS - 1 stages are in flight at a time: all workgroups of an XCD
+// reach new memory together, so a stage's first touch waits for HBM.
 // A wavefront's tile is MT x NT blocks of 16 x 16 outputs (v_mfma 16x16x32: at this
 // size the card is limited by power, and on the same random operands, from registers,
 // the 16-wide instructions ran at 1.63 GHz against 1.52 GHz for 32x32x16).  A stage is
-// two phases: the products of the upper half of the rows, under which the lower half
-// is read from LDS; then the barrier; then the products of the lower half, under which
-// the next stage's upper half and columns are read.  No wavefront waits on the barrier
-// or on LDS with idle matrix cores.
+// worked off in steps of 64 bytes (32 16-bit or 16 float32 numbers), a step in two phases:
+// the products of the upper half of the rows, under which the lower half is read from
+// LDS; after a stage's last step the barrier; then the products of the lower half, under
+// which the next step's upper half and columns are read.  No wavefront waits on the
+// barrier or on LDS with idle matrix cores.
+//
+// What bounds it: in 16 bits the card's power (8192 x 8192 -> 8192 in bf16 0.97 ms, 1.13
+// PFLOP/s at about 1.4 GHz; the library's product 0.84 ms), in float32 the matrix cores
+// (8192 x 8192 -> 4096 3.78 ms, 145 TFLOP/s; the library's 3.60 ms).
 //
 // The MFMA wants, per lane, chunk q = lane / 16 (16 bytes along the reduction) of row
 // lane % 16.
-//  - Reduction along the rows: a stage holds 64 bytes of each row, and a lane reads its
-//    chunk.  Chunk c of row r lies at position c ^ ((r >> 2) & 3): the 16 rows that a
-//    quarter of a wavefront reads together (256 bytes a clock) then fall on different
-//    LDS banks; measured 4.1 clocks a 1 KB read, against 16 for c ^ (r & 3).
-//  - Reduction across the rows: a stage holds 64 bytes / element size rows of BM (BN)
+//  - Reduction along the rows: a stage holds its depth of each row, and a lane reads its
+//    chunk.  Chunk c of row r lies at position c ^ ((r >> 1) & 7) (64 bytes deep: c ^ ((r >>
+//    2) & 3)): the 16 rows that a quarter of a wavefront reads together (256 bytes a clock)
+//    then fall on different LDS banks; measured 4.1 clocks a 1 KB read, against 16 for a
+//    position c ^ (r & 3).
+//  - Reduction across the rows: a stage holds depth / element size rows of BM (BN)
 //    elements.  16-bit operands are turned by the transposing LDS read (a group of 16
 //    lanes reads four rows of 16 elements, lane i receives column i); float32 ones are
 //    read element by element.  The rows of such a read lie at one bank offset, so
 //    blocks of 16 columns are permuted within a row by row_swizzle.
 // A direct load writes 64 consecutive chunks of LDS, so either permutation is done on
-// the global side, within pieces of 64 bytes (along) or whole rows (across).
+// the global side, within pieces of the depth (along) or whole rows (across).
 // Float32 uses the same bytes: MFMA step s of a chunk takes element s of it for both
 // operands, which permutes the reduction alike on both sides.
 
@@ -300,27 +305,33 @@ struct Operand {
   }
 };
 
+// Stages of 128 bytes (whole lines of an operand along: 192 us against 210 with 64 at
+// 4096 x 8192 -> 4096, bf16), three of them, or two for the largest tiles; those have four
+// of 64 bytes when both operands lie across, whose loads are whole lines anyway.
+template <int BM, int BN, bool XA, bool XB>
+struct Ring {
+  static constexpr bool LARGE = BM == 256 && BN == 256;
+  static constexpr int DEPTH = LARGE && XA && XB ? 64 : 128, NS = !LARGE ? 3 : DEPTH == 128 ? 2 : 4;
+  static constexpr int BYTES = NS * (BM + BN) * DEPTH;
+};
+
+// Workgroup number `block` of those that the tiles take, part `part` of the reduction.
 template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB>
-__global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Product p, int tm, int tn) {
+__device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned block, unsigned split, char* lds) {
   typedef typename Chunk<T>::type C;
-  // Stages of 128 bytes (whole lines of an operand along: 192 us against 210 with 64 at
-  // 4096 x 8192 -> 4096, bf16), three of them, or two for the largest tiles; those have
-  // four of 64 bytes when both operands lie across, whose loads are whole lines anyway.
-  constexpr bool LARGE = BM == 256 && BN == 256;
-  constexpr int DEPTH = LARGE && XA && XB ? 64 : 128, NS = !LARGE ? 3 : DEPTH == 128 ? 2 : 4;
+  constexpr int DEPTH = Ring<BM, BN, XA, XB>::DEPTH, NS = Ring<BM, BN, XA, XB>::NS;
   constexpr int NW = WM * WN, STAGE = (BM + BN) * DEPTH, KS = DEPTH / sizeof(T);
   constexpr int TM = BM / WM, TN = BN / WN, MT = TM / 16, NT = TN / 16, MH = MT / 2;
   typedef Operand<T, BM, NW, XA, DEPTH> OA;
   typedef Operand<T, BN, NW, XB, DEPTH> OB;
   constexpr int LA = OA::L, LB = OB::L, RA = OA::READS, RB = OB::READS;
-  __shared__ __align__(16) char lds[NS * STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int ti, tj;
-  tile_of(blockIdx.x, tm, tn, ti, tj);
+  tile_of(block, tm, tn, ti, tj);
   const long long m0 = (long long)ti * BM;
   const int n0 = tj * BN;
   // this workgroup's part of the reduction
-  const int first = blockIdx.y * (p.split_steps * 64 / DEPTH);
+  const int first = split * (p.split_steps / (DEPTH / 64));
   const int K = (int)min(p.K - (long long)first * KS, (long long)p.split_steps * (64 / (int)sizeof(T)));
   const int stages = (K + KS - 1) / KS, full = K / KS;
   OA a;
@@ -447,7 +458,7 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Pr
     const int nb = n0 + wn * TN;
     if (p.partial) {
       // float32 sums of this part, rows of N rounded up to four
-      float* part = p.partial + (blockIdx.y * p.M + mb) * (long long)p.ld_partial + nb;
+      float* part = p.partial + (split * p.M + mb) * (long long)p.ld_partial + nb;
       const int row = lane / (TN / 4), col = lane % (TN / 4) * 4;
 #pragma unroll
       for (int r = 0; r < 32; r += 256 / TN)
@@ -470,6 +481,64 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Pr
     __builtin_amdgcn_wave_barrier();
     asm volatile("" ::: "memory");
   }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB>
+__global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Product p, int tm, int tn) {
+  __shared__ __align__(16) char lds[Ring<BM, BN, XA, XB>::BYTES];
+  gemm_tile<T, BM, BN, WM, WN, XA, XB>(p, tm, tn, blockIdx.x, blockIdx.y, lds);
+}
+
+// dbias from the sums of act_grad_kernel's workgroups: 64 columns per workgroup, in 16 sums
+// of every 16th part whatever the number of wavefronts
+template <typename T, int NW>
+__device__ __forceinline__ void sum_columns(const ColumnSums& s, unsigned block, float* red) {
+  const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int col = block * 64 + c;
+  float v[16 / NW];
+#pragma unroll
+  for (int k = 0; k < 16 / NW; ++k) v[k] = 0.f;
+  if (col < s.n)
+    for (int i = w; i < s.parts; i += 16)
+#pragma unroll
+      for (int k = 0; k < 16 / NW; ++k)
+        if (i + k * NW < s.parts) v[k] += s.partial[(long long)(i + k * NW) * s.n + col];
+#pragma unroll
+  for (int k = 0; k < 16 / NW; ++k) red[(w + k * NW) * 64 + c] = v[k];
+  __syncthreads();
+  if (w == 0 && col < s.n) {
+    float sum = red[c];
+#pragma unroll
+    for (int k = 1; k < 16; ++k) sum += red[k * 64 + c];
+    ((T*)s.out)[col] = from_f32<T>(sum);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSums s) {
+  __shared__ float red[1024];
+  sum_columns<T, 16>(s, blockIdx.x, red);
+}
+
+// Both products of a backward pass, and dbias, by one launch: the sums' workgroups, then
+// the tiles of the product with the longer reduction, then the other's.
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void pair_kernel(Product dx, Product dw, ColumnSums s, int tn) {
+  __shared__ __align__(16) char lds[Ring<BM, BN, false, true>::BYTES];
+  static_assert(Ring<BM, BN, false, true>::BYTES == Ring<BM, BN, true, true>::BYTES, "one ring for both");
+  unsigned block = blockIdx.x;
+  const unsigned sums = s.out ? (s.n + 63) / 64 : 0;
+  if (block < sums) {
+    sum_columns<T, WM * WN>(s, block, (float*)lds);
+    return;
+  }
+  block -= sums;
+  const int tx = (int)((dx.M + BM - 1) / BM), tw = (int)((dw.M + BM - 1) / BM);
+  const unsigned first = (dx.K >= dw.K ? tx : tw) * tn;
+  if ((block < first) == (dx.K >= dw.K))
+    gemm_tile<T, BM, BN, WM, WN, false, true>(dx, tx, tn, block < first ? block : block - first, 0, lds);
+  else
+    gemm_tile<T, BM, BN, WM, WN, true, true>(dw, tw, tn, block < first ? block : block - first, 0, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -499,7 +568,8 @@ __device__ __forceinline__ typename Chunk<T>::type load_loose(const T* p) {
 
 // Up to four rows: R weight rows per workgroup, whose four wavefronts take the chunks
 // of the reduction in turn (1 KB of a row per load, R loads and a chunk of each x row,
-// which stay in the L1 cache, per step); float32 multiply-adds on the vector units.
+// which stay in the L1 cache, per step); float32 multiply-adds on the vector units.  1 x
+// 4096 -> 16384 in bf16: 23.3 us, 134 MB at 5.8 TB/s, what reading them takes.
 template <typename T, int MR, int R>
 __global__ __launch_bounds__(256) void rows_kernel(Product p) {
   typedef typename Chunk<T>::type C;
@@ -749,14 +819,14 @@ hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
 // ---------------------------------------------------------------------------
 // Rows that do not start on 16-byte boundaries or end in part of a chunk are copied to
 // rows that do, zeros to the end of the chunk, before a large product; both operands of
-// a call in one launch.
+// a call in one launch, a chunk per thread.
 template <typename T>
-__global__ __launch_bounds__(256) void pack_kernel(PackJob j0, PackJob j1) {
+__device__ __forceinline__ void pack_chunk(const PackJobs& jobs, unsigned block) {
   typedef typename Chunk<T>::type C;
   constexpr int EC = 16 / sizeof(T);
-  const bool second = blockIdx.x >= j0.blocks;
-  const PackJob& j = second ? j1 : j0;
-  const long long i = (long long)(blockIdx.x - (second ? j0.blocks : 0)) * 256 + threadIdx.x;
+  const bool second = block >= jobs.job[0].blocks;
+  const PackJob& j = jobs.job[second];
+  const long long i = (long long)(block - (second ? jobs.job[0].blocks : 0)) * 256 + threadIdx.x;
   const long long r = i / j.chunks;
   const int c = (int)(i % j.chunks);
   if (r >= j.rows) return;
@@ -771,11 +841,17 @@ __global__ __launch_bounds__(256) void pack_kernel(PackJob j0, PackJob j1) {
   *(C*)((T*)j.dst + i * EC) = v;
 }
 
+template <typename T>
+__global__ __launch_bounds__(256) void pack_kernel(PackJobs jobs) {
+  pack_chunk<T>(jobs, blockIdx.x);
+}
+
 // g = dy act'(saved), its copies and its column sums.  A thread has one chunk of columns
 // and every eighth of the workgroup's rows (16-byte accesses at any alignment); the
 // workgroup's 32 chunks of columns are summed over its rows in LDS, one float32 per
-// column and workgroup.  Workgroups have 64 rows, or as few as 8 while there would be
-// less than two workgroups a CU (1037 x 999 in float16: 13 us with 64 rows).
+// column and workgroup.  HBM bounds it (4096 x 8192 in bf16, GELU: 40 us, 201 MB at 5.0
+// TB/s).  Workgroups have 64 rows, or as few as 8 while there would be less than two
+// workgroups a CU (1037 x 999 in float16: 13 us with 64 rows, 5.5 so).
 int sum_rows(long long rows, int n, int chunk) {
   const long long across = (n + 32 * chunk - 1) / (32 * chunk);
   int r = 64;
@@ -784,14 +860,19 @@ int sum_rows(long long rows, int n, int chunk) {
 }
 
 template <typename T, int ACT>
-__global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p) {
+__global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p, PackJobs jobs) {
   typedef typename Chunk<T>::type C;
   typedef typename Loose<T>::type LC;
   constexpr int EC = 16 / sizeof(T);
   __shared__ float red[8][32 * EC + 1];
+  if (blockIdx.x >= p.blocks) {  // the copies that the products need, by the same launch
+    pack_chunk<T>(jobs, blockIdx.x - p.blocks);
+    return;
+  }
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int n = (blockIdx.x * 32 + c) * EC;
-  const long long m0 = (long long)blockIdx.y * p.part_rows;
+  const unsigned across = (p.n + 32 * EC - 1) / (32 * EC), bx = blockIdx.x % across, by = blockIdx.x / across;
+  const int n = (bx * 32 + c) * EC;
+  const long long m0 = (long long)by * p.part_rows;
   const T* dy = (const T*)p.dy;
   const T* saved = (const T*)p.saved;
   float sum[EC];
@@ -834,34 +915,14 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p) {
   for (int e = 0; e < EC; ++e) red[w][c * EC + e] = sum[e];
   __syncthreads();
   for (int i = threadIdx.x; i < 32 * EC; i += 256) {
-    const int col = blockIdx.x * 32 * EC + i;
+    const int col = bx * 32 * EC + i;
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) s += red[k][i];
     if (col < p.n) {
       if (!p.partial) ((T*)p.dbias)[col] = from_f32<T>(s);
-      else p.partial[(long long)blockIdx.y * p.n + col] = s;
+      else p.partial[(long long)by * p.n + col] = s;
     }
-  }
-}
-
-// dbias from the workgroups' sums: 64 columns per workgroup, whose 16 wavefronts take
-// the sums in turn
-template <typename T>
-__global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, int parts, int n, T* out) {
-  __shared__ float red[16][64];
-  const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + c;
-  float s = 0.f;
-  if (col < n)
-    for (int i = w; i < parts; i += 16) s += partial[(long long)i * n + col];
-  red[w][c] = s;
-  __syncthreads();
-  if (w == 0 && col < n) {
-    s = red[0][c];
-#pragma unroll
-    for (int k = 1; k < 16; ++k) s += red[k][c];
-    out[col] = from_f32<T>(s);
   }
 }
 
@@ -870,30 +931,47 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(unsigned short* p, long 
   if (i < rows * n) p[i / n * ld + i % n] = 0;
 }
 
-template <typename T>
-hipError_t launch_act_grad_typed(const ActGrad& p, hipStream_t st) {
-  constexpr int EC = 16 / sizeof(T);
-  const int per = sum_rows(p.rows, p.n, EC);
-  const long long parts = (p.rows + per - 1) / per;
-  // the rows go along the second grid dimension, 65535 parts at most a launch
-  for (long long at = 0; at < parts; at += 65535) {
-    const long long m = at * per;
-    ActGrad q = p;
-    q.dy = (const T*)p.dy + m * p.ld_dy;
-    if (p.saved) q.saved = (const T*)p.saved + m * p.ld_saved;
-    if (p.g) q.g = (T*)p.g + m * p.ld_g;
-    if (p.dres) q.dres = (T*)p.dres + m * p.ld_dres;
-    q.rows = p.rows - m;
-    q.part_rows = per;
-    q.partial = parts > 1 && p.dbias ? p.partial + at * p.n : nullptr;
-    const dim3 grid((p.n + 32 * EC - 1) / (32 * EC), (unsigned)std::min(parts - at, 65535LL));
-    if (p.act == VB_ACT_NONE) act_grad_kernel<T, VB_ACT_NONE><<<grid, 256, 0, st>>>(q);
-    else if (p.act == VB_ACT_RELU) act_grad_kernel<T, VB_ACT_RELU><<<grid, 256, 0, st>>>(q);
-    else if (p.act == VB_ACT_GELU) act_grad_kernel<T, VB_ACT_GELU><<<grid, 256, 0, st>>>(q);
-    else act_grad_kernel<T, VB_ACT_SILU><<<grid, 256, 0, st>>>(q);
+unsigned pack_blocks(PackJobs& jobs, int dtype) {
+  long long blocks = 0;
+  for (PackJob& j : jobs.job) {
+    if (!j.dst) j.rows = 0;
+    j.chunks = (int)(chunked_row(j.n, dtype) / 16);
+    const long long b = (j.rows * j.chunks + 255) / 256;
+    blocks += b;
+    if (blocks > 0x7fffffffLL) return ~0u;
+    j.blocks = (unsigned)b;
   }
-  if (p.dbias && parts > 1)
-    column_sum_kernel<T><<<(p.n + 63) / 64, 1024, 0, st>>>(p.partial, (int)parts, p.n, (T*)p.dbias);
+  return (unsigned)blocks;
+}
+
+template <typename T>
+hipError_t launch_act_grad_typed(ActGrad p, const PackJobs& jobs, unsigned copies, ColumnSums& sums, hipStream_t st) {
+  constexpr int EC = 16 / sizeof(T);
+  p.part_rows = sum_rows(p.rows, p.n, EC);
+  const long long parts = (p.rows + p.part_rows - 1) / p.part_rows;
+  const long long blocks = parts * ((p.n + 32 * EC - 1) / (32 * EC));
+  if (blocks + copies > 0x7fffffffLL) return hipErrorInvalidValue;
+  p.blocks = (unsigned)blocks;
+  if (parts == 1) p.partial = nullptr;
+  else if (p.dbias) sums = {p.partial, (int)parts, p.n, p.dbias};
+  const dim3 grid((unsigned)(blocks + copies));
+  if (p.act == VB_ACT_NONE) act_grad_kernel<T, VB_ACT_NONE><<<grid, 256, 0, st>>>(p, jobs);
+  else if (p.act == VB_ACT_RELU) act_grad_kernel<T, VB_ACT_RELU><<<grid, 256, 0, st>>>(p, jobs);
+  else if (p.act == VB_ACT_GELU) act_grad_kernel<T, VB_ACT_GELU><<<grid, 256, 0, st>>>(p, jobs);
+  else act_grad_kernel<T, VB_ACT_SILU><<<grid, 256, 0, st>>>(p, jobs);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_pair_typed(Product dx, Product dw, int tile, const ColumnSums& s, hipStream_t st) {
+  for (Product* p : {&dx, &dw})  // no split
+    p->split_steps = (int)((p->K * (long long)sizeof(T) + 127) / 128 * 2), p->partial = nullptr;
+  const int tn = (dx.N + tile - 1) / tile;
+  const long long tiles = ((dx.M + tile - 1) / tile + (dw.M + tile - 1) / tile) * tn;
+  const long long blocks = tiles + (s.out ? (s.n + 63) / 64 : 0);
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  if (tile == 64) pair_kernel<T, 64, 64, 2, 2><<<(unsigned)blocks, 256, 0, st>>>(dx, dw, s, tn);
+  else pair_kernel<T, 128, 128, 2, 4><<<(unsigned)blocks, 512, 0, st>>>(dx, dw, s, tn);
   return hipGetLastError();
 }
 
@@ -907,23 +985,29 @@ hipError_t launch_act_grad_typed(const ActGrad& p, hipStream_t st) {
 // 128 122, 128 140, 64 197), at 2048 x 4096 x 4096 those of 256 x 128 (61 us; 256 92, 128
 // 85, 64 111).  A split costs the writing and reading of its float32 parts at 4 TB/s and
 // another launch.
+namespace {
+
+struct Kind {
+  int bm, bn, per_cu;
+  double latency, share;
+};
+const Kind k16[] = {{256, 256, 1, 0.70, 0.83}, {256, 128, 1, 0.39, 0.46}, {128, 128, 1, 0.25, 0.27},
+                     {64, 64, 3, 0.13, 0.09}};
+const Kind k32[] = {{256, 128, 1, 1.90, 1.90}, {128, 128, 1, 1.01, 1.01}, {64, 64, 3, 0.285, 0.27}};
+
+long long steps_of(long long K, int dtype) { return (K * (long long)elem_size(dtype) + 63) / 64; }
+
+}  // namespace
+
 Tiling choose_tiling(int dtype, long long M, int N, long long K) {
-  struct Kind {
-    int bm, bn, per_cu;
-    double latency, share;
-  };
-  static const Kind k16[] = {{256, 256, 1, 0.70, 0.83}, {256, 128, 1, 0.39, 0.46}, {128, 128, 1, 0.25, 0.27},
-                             {64, 64, 3, 0.13, 0.09}};
-  static const Kind k32[] = {{256, 128, 1, 1.90, 1.90}, {128, 128, 1, 1.01, 1.01}, {64, 64, 3, 0.285, 0.27}};
   const Kind* kinds = dtype == VB_F32 ? k32 : k16;
   const int nk = dtype == VB_F32 ? 3 : 4;
-  const long long stages = (K * (long long)elem_size(dtype) + 63) / 64;
-  Tiling best{64, 64, 1};
-  double best_us = 1e30;
+  const long long stages = steps_of(K, dtype);
+  Tiling best{64, 64, 1, 1e30};
   for (int k = 0; k < nk; ++k) {
     const Kind& c = kinds[k];
     const double tiles = (double)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
-    for (int s = 1; s <= 32 && s * 4 <= stages; s *= 2) {
+    for (int s = 1; s <= 32 && (s == 1 || s * 4 <= stages); s *= 2) {
       const double blocks = tiles * s, slots = 256.0 * c.per_cu;
       const double full = std::floor(blocks / slots), rest = blocks - full * slots;
       auto stage = [&](double on_cu) { return std::fmax(c.latency, on_cu * c.share); };
@@ -931,8 +1015,58 @@ Tiling choose_tiling(int dtype, long long M, int N, long long K) {
       double us = full * (run * stage(c.per_cu) + 3.0);
       if (rest > 0) us += run * stage(std::ceil(rest / 256.0)) + 3.0;
       if (s > 1) us += 3.0 + (2.0 * s * M * N * 4.0) / 4e6;
-      if (us < best_us) best_us = us, best = Tiling{c.bm, c.bn, s};
+      if (us < best.us) best = Tiling{c.bm, c.bn, s, us};
     }
+  }
+  return best;
+}
+
+namespace {
+
+// When 256 CUs that take tiles one at a time, a of them for c us, then a2 for c2, are done.
+double list_time(double a, double c, double a2, double c2) {
+  const double q = std::floor(a / 256.0), rest = a - q * 256.0, early = q * c, late = early + c;
+  auto done = [&](double t) {
+    return (256.0 - rest) * std::floor((t - early) / c2 + 1e-6) + rest * std::fmax(std::floor((t - late) / c2 + 1e-6), 0.0);
+  };
+  double best = 1e30;
+  for (const double base : {early, late}) {
+    double t = base + std::fmax(std::floor(((a * c + a2 * c2) / 256.0 - base) / c2), 0.0) * c2;
+    while (done(t) < a2) t += c2;
+    best = std::fmin(best, t);
+  }
+  return std::fmax(best, rest > 0 ? late : early);
+}
+
+}  // namespace
+
+// Side of the tiles with which both products of a backward pass take one launch, which
+// fills the card while the first one ends, or 0 where two launches are faster by the same
+// model (the second one: 2 us).  Together | apart, with g and dbias: 1024 x 1024 -> 1024 in
+// bf16 19.4 | 23.7 us (64-wide tiles), float32 44 | 52; 1024 x 2048 -> 2048 34 | 41 (128);
+// 4096 x 2048 -> 2048 96 | 92.  A split reduction stays one, so that each gradient has the
+// same bits alone as with the other.
+int pair_tile(const Product& dx, const Product& dw, int dtype) {
+  const Tiling x = choose_tiling(dtype, dx.M, dx.N, dx.K), w = choose_tiling(dtype, dw.M, dw.N, dw.K);
+  if (x.splits > 1 || w.splits > 1) return 0;
+  const Product &first = dx.K >= dw.K ? dx : dw, &second = dx.K >= dw.K ? dw : dx;
+  const double run = (double)steps_of(first.K, dtype), run2 = (double)steps_of(second.K, dtype);
+  int best = 0;
+  double best_us = x.us + w.us + 2.0;
+  const Kind* kinds = dtype == VB_F32 ? k32 + 1 : k16 + 2;
+  for (int k = 0; k < 2; ++k) {
+    const Kind& c = kinds[k];
+    auto tiles = [&](const Product& p) { return (double)((p.M + c.bm - 1) / c.bm) * ((p.N + c.bn - 1) / c.bn); };
+    const double n = tiles(first), n2 = tiles(second);
+    double us;
+    if (c.per_cu == 1) {
+      us = list_time(n, run * c.latency + 3.0, n2, run2 * c.latency + 3.0);
+    } else {  // a CU has its share of the steps and half a tile more; its tiles' ends overlap
+      const double share = std::fmin(std::ceil(n / 256.0) * run + std::ceil(n2 / 256.0) * run2,
+                                     (n * run + n2 * run2) / 256.0 + run / 2);
+      us = std::fmax(c.latency * run, c.share * share) + 2.0 + std::ceil((n + n2) / (256.0 * c.per_cu));
+    }
+    if (us < best_us) best_us = us, best = c.bm;
   }
   return best;
 }
@@ -972,21 +1106,13 @@ bool is_chunked(const void* p, long long ld, long long n, int dtype) {
   return (uintptr_t)p % 16 == 0 && ld * es % 16 == 0 && n * es % 16 == 0 && ld * es <= MAX_CHUNKED_ROW;
 }
 
-hipError_t launch_pack(PackJob j0, PackJob j1, int dtype, hipStream_t st) {
-  long long blocks = 0;
-  for (PackJob* j : {&j0, &j1}) {
-    if (!j->dst) j->rows = 0;
-    j->chunks = (int)(chunked_row(j->n, dtype) / 16);
-    const long long b = (j->rows * j->chunks + 255) / 256;
-    blocks += b;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    j->blocks = (unsigned)b;
-  }
+hipError_t launch_pack(PackJobs jobs, int dtype, hipStream_t st) {
+  const unsigned blocks = pack_blocks(jobs, dtype);
+  if (blocks == ~0u) return hipErrorInvalidValue;
   if (!blocks) return hipSuccess;
-  const dim3 grid((unsigned)blocks);
-  if (dtype == VB_F32) pack_kernel<float><<<grid, 256, 0, st>>>(j0, j1);
-  else if (dtype == VB_BF16) pack_kernel<bf16><<<grid, 256, 0, st>>>(j0, j1);
-  else pack_kernel<f16><<<grid, 256, 0, st>>>(j0, j1);
+  if (dtype == VB_F32) pack_kernel<float><<<blocks, 256, 0, st>>>(jobs);
+  else if (dtype == VB_BF16) pack_kernel<bf16><<<blocks, 256, 0, st>>>(jobs);
+  else pack_kernel<f16><<<blocks, 256, 0, st>>>(jobs);
   return hipGetLastError();
 }
 
@@ -995,10 +1121,26 @@ size_t act_grad_bytes(long long rows, int n, int dtype) {
   return rows > per ? (size_t)((rows + per - 1) / per) * n * 4 : 0;
 }
 
-hipError_t launch_act_grad(const ActGrad& p, int dtype, hipStream_t st) {
-  if (dtype == VB_F32) return launch_act_grad_typed<float>(p, st);
-  if (dtype == VB_BF16) return launch_act_grad_typed<bf16>(p, st);
-  return launch_act_grad_typed<f16>(p, st);
+hipError_t launch_act_grad(const ActGrad& p, PackJobs jobs, int dtype, ColumnSums& sums, hipStream_t st) {
+  const unsigned copies = pack_blocks(jobs, dtype);
+  if (copies == ~0u) return hipErrorInvalidValue;
+  if (dtype == VB_F32) return launch_act_grad_typed<float>(p, jobs, copies, sums, st);
+  if (dtype == VB_BF16) return launch_act_grad_typed<bf16>(p, jobs, copies, sums, st);
+  return launch_act_grad_typed<f16>(p, jobs, copies, sums, st);
+}
+
+hipError_t launch_column_sums(const ColumnSums& s, int dtype, hipStream_t st) {
+  const unsigned blocks = (s.n + 63) / 64;
+  if (dtype == VB_F32) column_sum_kernel<float><<<blocks, 1024, 0, st>>>(s);
+  else if (dtype == VB_BF16) column_sum_kernel<bf16><<<blocks, 1024, 0, st>>>(s);
+  else column_sum_kernel<f16><<<blocks, 1024, 0, st>>>(s);
+  return hipGetLastError();
+}
+
+hipError_t launch_pair(const Product& dx, const Product& dw, int tile, const ColumnSums& s, int dtype, hipStream_t st) {
+  if (dtype == VB_F32) return launch_pair_typed<float>(dx, dw, tile, s, st);
+  if (dtype == VB_BF16) return launch_pair_typed<bf16>(dx, dw, tile, s, st);
+  return launch_pair_typed<f16>(dx, dw, tile, s, st);
 }
 
 hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long long ld_bytes, hipStream_t st) {

@@ -109,6 +109,7 @@ ForwardPlan plan_forward(const vb_linear_fwd& p) {
 struct BackwardPlan {
   Product dx{}, dw{};
   Part g, x, w, sums, partial;
+  int pair = 0;  // tiles of one launch for both products
   size_t total = 0;
 };
 
@@ -132,6 +133,8 @@ BackwardPlan plan_backward(const vb_linear_bwd& p) {
   if (p.dweight && !is_chunked(p.x, p.ld_x, p.n_in, dt)) f.x.take(f.total, p.rows * row);
   if (p.dx && !is_chunked(p.weight, p.ld_w, p.n_in, dt)) f.w.take(f.total, p.n_out * row);
   if (p.dbias) f.sums.take(f.total, act_grad_bytes(p.rows, p.n_out, dt));
+  if (p.dx && p.dweight) f.pair = pair_tile(a, b, dt);
+  if (f.pair) return f;
   size_t parts = 0;  // the products run one after the other
   if (p.dx) parts = product_bytes(a, dt);
   if (p.dweight) {
@@ -177,7 +180,7 @@ extern "C" vb_status vb_linear_forward(const vb_linear_fwd* p, void* ws, size_t 
   TRY(check_ws(fn, ws, ws_bytes, f.total));
   const hipStream_t st = (hipStream_t)stream;
   const long long ld = (long long)(chunked_row(p->n_in, p->dtype) / elem_size(p->dtype));
-  HIPCHK(launch_pack({p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws)}, {p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws)},
+  HIPCHK(launch_pack({{{p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws)}, {p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws)}}},
                      p->dtype, st));
   if (f.x.used) f.d.a = f.x.in(ws), f.d.lda = ld;
   if (f.w.used) f.d.b = f.w.in(ws), f.d.ldb = ld;
@@ -212,6 +215,8 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
   }
   BackwardPlan f = plan_backward(*p);
   TRY(check_ws(fn, ws, ws_bytes, f.total));
+  const PackJobs jobs = {{{p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws)}, {p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws)}}};
+  ColumnSums sums{};
   if (f.g.used || p->dbias || p->dresidual) {
     ActGrad g{};
     g.dy = p->dy, g.ld_dy = p->ld_dy;
@@ -220,14 +225,19 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
     g.dres = p->dresidual, g.ld_dres = p->ld_dres;
     g.dbias = p->dbias, g.partial = (float*)f.sums.in(ws);
     g.rows = p->rows, g.n = p->n_out, g.act = p->act;
-    HIPCHK(launch_act_grad(g, p->dtype, st));
+    HIPCHK(launch_act_grad(g, jobs, p->dtype, sums, st));
     if (f.g.used) f.dx.a = f.dw.a = g.g, f.dx.lda = f.dw.lda = g.ld_g;
+  } else {
+    HIPCHK(launch_pack(jobs, p->dtype, st));
   }
   const long long ld = (long long)chunked_row(p->n_in, p->dtype) / es;
-  HIPCHK(launch_pack({p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws)}, {p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws)},
-                     p->dtype, st));
   if (f.w.used) f.dx.b = f.w.in(ws), f.dx.ldb = ld;
   if (f.x.used) f.dw.b = f.x.in(ws), f.dw.ldb = ld;
+  if (f.pair) {
+    HIPCHK(launch_pair(f.dx, f.dw, f.pair, sums, p->dtype, st));
+    return VB_OK;
+  }
+  if (sums.out) HIPCHK(launch_column_sums(sums, p->dtype, st));
   f.dx.partial = f.dw.partial = (float*)f.partial.in(ws);
   if (p->dx) HIPCHK(launch_product(f.dx, p->dtype, st));
   if (p->dweight) HIPCHK(launch_product(f.dw, p->dtype, st));

@@ -43,6 +43,7 @@ struct Product {
 };
 struct Tiling {
   int bm, bn, splits;
+  double us;  // as estimated
 };
 bool product_is_narrow(const Product& p, int dtype);
 size_t product_bytes(const Product& p, int dtype);
@@ -65,7 +66,10 @@ struct PackJob {
   int chunks;
   unsigned blocks;
 };
-hipError_t launch_pack(PackJob j0, PackJob j1, int dtype, hipStream_t st);
+struct PackJobs {
+  PackJob job[2];
+};
+hipError_t launch_pack(PackJobs jobs, int dtype, hipStream_t st);
 
 // v = dy * act'(saved), in float32: g = v (rows of ld_g elements that start on 16-byte
 // boundaries, zeros to the end of the last chunk), dres = v, dbias = column sums of v;
@@ -83,10 +87,23 @@ struct ActGrad {
   long long rows;
   int n;
   int act;
-  int part_rows;  // set by launch_act_grad: rows of a workgroup
+  // set by launch_act_grad: rows of a workgroup, workgroups
+  int part_rows;
+  unsigned blocks;
+};
+// dbias from sums over parts of the rows, parts x n
+struct ColumnSums {
+  const float* partial;
+  int parts, n;
+  void* out;  // NULL: nothing to sum
 };
 size_t act_grad_bytes(long long rows, int n, int dtype);
-hipError_t launch_act_grad(const ActGrad& p, int dtype, hipStream_t st);
+// sums: set if dbias is left for launch_column_sums or launch_pair
+hipError_t launch_act_grad(const ActGrad& p, PackJobs jobs, int dtype, ColumnSums& sums, hipStream_t st);
+hipError_t launch_column_sums(const ColumnSums& s, int dtype, hipStream_t st);
+// Both products of a backward pass by one launch, with tiles of this side (0: use two)
+int pair_tile(const Product& dx, const Product& dw, int dtype);
+hipError_t launch_pair(const Product& dx, const Product& dw, int tile, const ColumnSums& s, int dtype, hipStream_t st);
 hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long long ld_bytes, hipStream_t st);
 
 // ws: one int64 (count of the rows that are not ignored)

@@ -286,6 +286,22 @@ def test_large_products(lbp, size, dtype):
     check_backward(lbp, dy, x, w, r, "silu", f"large {size}")
 
 
+@pytest.mark.parametrize("size, dtype", [((1030, 2050, 2000), F16), ((1021, 2047, 2045), F32), ((300, 701, 5000), BF16),
+                                         ((2047, 1000, 1033), F32)], ids=str)
+def test_gradients_alone_and_together(lbp, size, dtype):
+    """Both products by one launch, with wide and narrow tiles, and the column sums beside them."""
+    rows, n_in, n_out = size
+    print(f"together {size} {dtype}", flush=True)
+    x, w, b, r = case(*size, dtype, seed=80)
+    dy = normal(gen(81), rows, n_out, std=rows ** -0.5, dtype=dtype)
+    out = check_backward(lbp, dy, x, w, r, "gelu", f"together {size}")
+    for k, name in enumerate(("want_x", "want_weight", "want_bias")):
+        flags = dict(want_x=False, want_weight=False, want_bias=False)
+        flags[name] = True
+        one = lbp.linear_backward(dy, x, w, act="gelu", saved=r, **flags)
+        assert torch.equal(one[k], out[k]), name
+
+
 def test_refusals_of_the_binding(lbp):
     x, w, b, r = case(6, 8, 5, F32)
     for call, text in (
