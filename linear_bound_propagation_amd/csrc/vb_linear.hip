@@ -766,8 +766,17 @@ __global__ __launch_bounds__(256) void join_kernel(Product p, int splits) {
   const int n = (int)(i % quads) * 4;
   if (m >= p.M) return;
   const float* q = p.partial + m * p.ld_partial + n;
+  const long long step = p.M * p.ld_partial;
   f32x4 v = *(const f32x4*)q;
-  for (int s = 1; s < splits; ++s) v += *(const f32x4*)(q + s * p.M * p.ld_partial);
+  int s = 1;
+  for (; s + 5 <= splits; s += 5) {  // five loads at a time
+    f32x4 part[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) part[k] = *(const f32x4*)(q + (s + k) * step);
+#pragma unroll
+    for (int k = 0; k < 5; ++k) v += part[k];
+  }
+  for (; s < splits; ++s) v += *(const f32x4*)(q + s * step);
   const float x[4] = {v[0], v[1], v[2], v[3]};
   if (n + 4 <= p.N) {
     finish<T, 4>(p, m, n, x);
@@ -977,23 +986,24 @@ hipError_t launch_pair_typed(Product dx, Product dw, int tile, const ColumnSums&
 
 }  // namespace
 
-// Tile and split of a large product by the time they would take: rounds of workgroups
-// over 256 CUs, each a run of 64-byte steps and a fixed part.  A step takes `latency`
-// microseconds for a tile that has its CU to itself and `share` for each of several,
-// measured per tile size at 1024 x 1024 x 1024 and 4096 x 4096 x 4096: at the first the
-// 64-wide tiles win (7.2 us; 128 10.8, 256 26), at the second the 256-wide (113 us; 256 x
-// 128 122, 128 140, 64 197), at 2048 x 4096 x 4096 those of 256 x 128 (61 us; 256 92, 128
-// 85, 64 111).  A split costs the writing and reading of its float32 parts at 4 TB/s and
-// another launch.
+// Tile and split of a large product by the time they would take on the CU with the most
+// tiles: 64-byte steps of `share` microseconds (64-wide tiles, three to a CU at a time, take
+// `latency` where one has its CU to itself), the `fixed` part of each tile, mostly its
+// outputs, and a launch.  Measured, in us at 1024 x 1024 x 1024 | 2048 x 4096 x 4096 | 4096 x
+// 4096 x 4096 | 4096 x 4096 x 32: bf16 tiles of 64 6.9 | 111 | 197 | 15.6, 128 10.0 | 85 | 140
+// | 15.6, 256 x 128 14 | 61 | 122 | 12.6, 256 24 | 92 | 113 | 13.2; float32 tiles of 64 21 | 479
+// | 966 | 24, 128 62 | 475 | 948 | 25, 256 x 128 118 | 465 | 938 | 25.  A split costs the writing
+// and reading of its float32 parts, at 6 TB/s as they are in the caches, and another launch;
+// it has to gain 8 %, as it also keeps a backward pass from one launch for both products.
 namespace {
 
 struct Kind {
   int bm, bn, per_cu;
-  double latency, share;
+  double fixed, latency, share;
 };
-const Kind k16[] = {{256, 256, 1, 0.70, 0.83}, {256, 128, 1, 0.39, 0.46}, {128, 128, 1, 0.25, 0.27},
-                     {64, 64, 3, 0.13, 0.09}};
-const Kind k32[] = {{256, 128, 1, 1.90, 1.90}, {128, 128, 1, 1.01, 1.01}, {64, 64, 3, 0.285, 0.27}};
+const Kind k16[] = {{256, 256, 1, 8.0, 0.82, 0.82}, {256, 128, 1, 4.5, 0.43, 0.43}, {128, 128, 1, 3.0, 0.255, 0.255},
+                    {64, 64, 3, 0.8, 0.13, 0.115}};
+const Kind k32[] = {{256, 128, 1, 7.0, 1.80, 1.80}, {128, 128, 1, 3.5, 0.915, 0.915}, {64, 64, 3, 0.8, 0.275, 0.235}};
 
 long long steps_of(long long K, int dtype) { return (K * (long long)elem_size(dtype) + 63) / 64; }
 
@@ -1004,19 +1014,17 @@ Tiling choose_tiling(int dtype, long long M, int N, long long K) {
   const int nk = dtype == VB_F32 ? 3 : 4;
   const long long stages = steps_of(K, dtype);
   Tiling best{64, 64, 1, 1e30};
-  for (int k = 0; k < nk; ++k) {
-    const Kind& c = kinds[k];
-    const double tiles = (double)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
-    for (int s = 1; s <= 32 && (s == 1 || s * 4 <= stages); s *= 2) {
-      const double blocks = tiles * s, slots = 256.0 * c.per_cu;
-      const double full = std::floor(blocks / slots), rest = blocks - full * slots;
-      auto stage = [&](double on_cu) { return std::fmax(c.latency, on_cu * c.share); };
-      const double run = (double)((stages + s - 1) / s);
-      double us = full * (run * stage(c.per_cu) + 3.0);
-      if (rest > 0) us += run * stage(std::ceil(rest / 256.0)) + 3.0;
-      if (s > 1) us += 3.0 + (2.0 * s * M * N * 4.0) / 4e6;
-      if (us < best.us) best = Tiling{c.bm, c.bn, s, us};
+  double unsplit = 0;
+  for (int n = 1; n <= 32 && (n == 1 || n * 4 <= stages); n *= 2) {
+    for (int k = 0; k < nk; ++k) {
+      const Kind& c = kinds[k];
+      const double tiles = (double)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+      const double on_cu = std::ceil(tiles * n / 256.0), run = (double)((stages + n - 1) / n);
+      double us = std::fmax(c.latency, on_cu * c.share) * run + on_cu * c.fixed + 3.0;
+      if (n > 1) us += 2.0 + (2.0 * n * M * N * 4.0) / 6e6;
+      if (us < best.us && (n == 1 || us < 0.92 * unsplit)) best = Tiling{c.bm, c.bn, n, us};
     }
+    if (n == 1) unsplit = best.us;
   }
   return best;
 }
@@ -1060,11 +1068,11 @@ int pair_tile(const Product& dx, const Product& dw, int dtype) {
     const double n = tiles(first), n2 = tiles(second);
     double us;
     if (c.per_cu == 1) {
-      us = list_time(n, run * c.latency + 3.0, n2, run2 * c.latency + 3.0);
+      us = list_time(n, run * c.share + c.fixed, n2, run2 * c.share + c.fixed) + 3.0;
     } else {  // a CU has its share of the steps and half a tile more; its tiles' ends overlap
       const double share = std::fmin(std::ceil(n / 256.0) * run + std::ceil(n2 / 256.0) * run2,
                                      (n * run + n2 * run2) / 256.0 + run / 2);
-      us = std::fmax(c.latency * run, c.share * share) + 2.0 + std::ceil((n + n2) / (256.0 * c.per_cu));
+      us = std::fmax(c.latency * run, c.share * share) + c.fixed * std::ceil((n + n2) / 256.0) + 3.0;
     }
     if (us < best_us) best_us = us, best = c.bm;
   }
