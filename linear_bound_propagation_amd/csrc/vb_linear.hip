@@ -490,19 +490,34 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Pr
 }
 
 // dbias from the sums of act_grad_kernel's workgroups: 64 columns per workgroup, in 16 sums
-// of every 16th part whatever the number of wavefronts
+// of every 16th part whatever the number of wavefronts, eight loads at a time (650 parts:
+// 10.5 us one at a time)
 template <typename T, int NW>
 __device__ __forceinline__ void sum_columns(const ColumnSums& s, unsigned block, float* red) {
+  constexpr int U = NW / 2;
   const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int col = block * 64 + c;
   float v[16 / NW];
 #pragma unroll
   for (int k = 0; k < 16 / NW; ++k) v[k] = 0.f;
-  if (col < s.n)
-    for (int i = w; i < s.parts; i += 16)
+  if (col < s.n) {
+    int i = w;
+    for (; i + 16 * U <= s.parts; i += 16 * U) {
+      float x[U][16 / NW];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < 16 / NW; ++k) x[u][k] = s.partial[(long long)(i + 16 * u + k * NW) * s.n + col];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < 16 / NW; ++k) v[k] += x[u][k];
+    }
+    for (; i < s.parts; i += 16)
 #pragma unroll
       for (int k = 0; k < 16 / NW; ++k)
         if (i + k * NW < s.parts) v[k] += s.partial[(long long)(i + k * NW) * s.n + col];
+  }
 #pragma unroll
   for (int k = 0; k < 16 / NW; ++k) red[(w + k * NW) * 64 + c] = v[k];
   __syncthreads();
