@@ -66,10 +66,13 @@ typedef struct {
  * saved: NULL for VB_ACT_NONE; y for VB_ACT_RELU (act' = 1 where y > 0, 0
  * elsewhere: where saved is not > 0, g is 0 whatever dy holds); pre for GELU
  * and SILU.  dx, dweight, dbias and dresidual may each be NULL.  With rows = 0
- * dweight and dbias are set to zero.  For 16-bit types g enters both products
- * rounded to dtype (the matrix cores' operand type; with VB_ACT_NONE and
- * VB_ACT_RELU that changes nothing); dbias sums the unrounded g.  dresidual may
- * be dy itself (same pointer and ld); no other overlap. */
+ * dweight and dbias are set to zero.  dresidual may be dy itself (same pointer
+ * and ld); no other overlap.
+ * The matrix cores take operands of dtype.  With GELU and SILU in a 16-bit type g
+ * is no number of that type: it enters both products as the sum of two (relative
+ * error 2^-16 in bfloat16, 2^-22 in float16), which multiplies twice, or, with
+ * round_g, rounded to one, which takes half the time and adds an error as large
+ * as the rounding of the gradients themselves.  dbias sums the unrounded g. */
 typedef struct {
   int64_t rows;
   int32_t n_in, n_out;
@@ -82,6 +85,7 @@ typedef struct {
   void* dweight;        int64_t ld_dw;   /* [n_out][n_in] or NULL   */
   void* dbias;                           /* [n_out] or NULL         */
   void* dresidual;      int64_t ld_dres; /* [rows][n_out] or NULL   */
+  int32_t round_g;                       /* 0 or 1                  */
 } vb_linear_bwd;
 
 /* Workspace of a call with these arguments.  Of the pointers only x, weight and dy are

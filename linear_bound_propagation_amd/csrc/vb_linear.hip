@@ -95,7 +95,7 @@ struct Chunk;
 template <>
 struct Chunk<float> {
   typedef f32x4 type;
-  static constexpr int MFMAS = 4;
+  static constexpr int MFMAS = 4, BITS = 24;
   __device__ static f32x4 mma(f32x4 a, f32x4 b, f32x4 c, int s) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], c, 0, 0, 0);
   }
@@ -103,6 +103,7 @@ struct Chunk<float> {
 template <>
 struct Chunk<bf16> {
   typedef bf16x8 type;
+  static constexpr int BITS = 8;  // of a number's significand
   static constexpr int MFMAS = 1;
   __device__ static f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c, int) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -111,6 +112,7 @@ struct Chunk<bf16> {
 template <>
 struct Chunk<f16> {
   typedef f16x8 type;
+  static constexpr int BITS = 11;
   static constexpr int MFMAS = 1;
   __device__ static f32x4 mma(f16x8 a, f16x8 b, f32x4 c, int) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -315,8 +317,9 @@ struct Ring {
   static constexpr int BYTES = NS * (BM + BN) * DEPTH;
 };
 
-// Workgroup number `block` of those that the tiles take, part `part` of the reduction.
-template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB>
+// Workgroup number `block` of those that the tiles take, part `split` of the reduction.  TWO: A
+// in two parts (an instance of its own: its registers and branches would cost the others 4 %).
+template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB, bool TWO>
 __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned block, unsigned split, char* lds) {
   typedef typename Chunk<T>::type C;
   constexpr int DEPTH = Ring<BM, BN, XA, XB>::DEPTH, NS = Ring<BM, BN, XA, XB>::NS;
@@ -402,43 +405,74 @@ __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned bl
     __builtin_amdgcn_sched_barrier(0);
   };
   auto none = [] {};
-  for (int i = 0; i < NS - 1; ++i)
-    if (i < full) issue(i, i * STAGE);
-    else if (i < stages) issue_part(i, i * STAGE);
-  if (full >= NS - 1) join(); else join_all();
-  fetch_b(0, 0, 0);
-  fetch_a(0, 0, 0);
-  int t = 0, cur = 0;
-  if constexpr (DEPTH == 128) {
-    for (; t + NS - 1 < full; ++t) {
-      step(cur, 0, 0, [&] { issue(t + NS - 1, after(cur, NS - 1)); }, none);
-      step(cur, 1, 1, none, join);
-      cur = after(cur, 1);
+  // A in two parts: the low parts' products first, scaled down, then the high ones' on top
+  // of them (one after the other: accumulators for both would not fit the registers).  A low
+  // sum that is not finite met an infinity or NaN of B; the high parts alone have the sign.
+  const long long low = TWO ? (const char*)p.a_low - (const char*)p.a : 0;
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = f(acc[i][j][q]);
+  };
+  a.base += low;
+  for (int pass = 0;; ++pass) {
+    if constexpr (TWO) {
+      // nothing computed from these is carried round the loop (it would be 40 registers)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(pa[i]));
+#pragma unroll
+      for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(pb[j]));
+#pragma unroll
+      for (int i = 0; i < LA; ++i) asm volatile("" : "+v"(a.off[i]));
+#pragma unroll
+      for (int i = 0; i < LB; ++i) asm volatile("" : "+v"(b.off[i]));
+      asm volatile("" : "+v"(a.lane), "+v"(b.lane));
     }
-    for (; t < stages; ++t) {
-      if (t + NS - 1 < stages) issue_part(t + NS - 1, after(cur, NS - 1));
-      step(cur, 0, 0, none, none);
-      step(cur, 1, 1, none, join_all);
-      cur = after(cur, 1);
+    for (int i = 0; i < NS - 1; ++i)
+      if (i < full) issue(i, i * STAGE);
+      else if (i < stages) issue_part(i, i * STAGE);
+    if (full >= NS - 1) join(); else join_all();
+    fetch_b(0, 0, 0);
+    fetch_a(0, 0, 0);
+    int t = 0, cur = 0;
+    if constexpr (DEPTH == 128) {
+      for (; t + NS - 1 < full; ++t) {
+        step(cur, 0, 0, [&] { issue(t + NS - 1, after(cur, NS - 1)); }, none);
+        step(cur, 1, 1, none, join);
+        cur = after(cur, 1);
+      }
+      for (; t < stages; ++t) {
+        if (t + NS - 1 < stages) issue_part(t + NS - 1, after(cur, NS - 1));
+        step(cur, 0, 0, none, none);
+        step(cur, 1, 1, none, join_all);
+        cur = after(cur, 1);
+      }
+    } else {
+      for (; t + NS < full; t += 2) {
+        step(cur, 0, 0, [&] { issue(t + NS - 1, after(cur, NS - 1)); }, join);
+        cur = after(cur, 1);
+        step(cur, 0, 1, [&] { issue(t + NS, after(cur, NS - 1)); }, join);
+        cur = after(cur, 1);
+      }
+      for (; t < stages; t += 2) {
+        if (t + NS - 1 < stages) issue_part(t + NS - 1, after(cur, NS - 1));
+        step(cur, 0, 0, none, join_all);
+        cur = after(cur, 1);
+        if (t + 1 == stages) break;
+        if (t + NS < stages) issue_part(t + NS, after(cur, NS - 1));
+        step(cur, 0, 1, none, join_all);
+        cur = after(cur, 1);
+      }
     }
-  } else {
-    for (; t + NS < full; t += 2) {
-      step(cur, 0, 0, [&] { issue(t + NS - 1, after(cur, NS - 1)); }, join);
-      cur = after(cur, 1);
-      step(cur, 0, 1, [&] { issue(t + NS, after(cur, NS - 1)); }, join);
-      cur = after(cur, 1);
-    }
-    for (; t < stages; t += 2) {
-      if (t + NS - 1 < stages) issue_part(t + NS - 1, after(cur, NS - 1));
-      step(cur, 0, 0, none, join_all);
-      cur = after(cur, 1);
-      if (t + 1 == stages) break;
-      if (t + NS < stages) issue_part(t + NS, after(cur, NS - 1));
-      step(cur, 0, 1, none, join_all);
-      cur = after(cur, 1);
-    }
+    join_all();
+    if (!TWO || pass == 1) break;
+    a.base -= low;
+    each([](float v) { return fabsf(v) < INFINITY ? v * (1.f / (1 << Chunk<T>::BITS)) : 0.f; });
   }
-  join_all();
+  if (TWO) each([](float v) { return 2.f * v; });
   // Outputs leave through LDS, 32 rows of the wavefront's tile at a time in its own
   // part of it, so that a row's outputs are written as whole 128-byte pieces.
   constexpr int LDE = TN + 4, VEC = 16 / sizeof(T), LPR = TN / VEC, RPI = 64 / LPR;
@@ -483,10 +517,10 @@ __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned bl
   }
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB>
+template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB, bool TWO>
 __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Product p, int tm, int tn) {
   __shared__ __align__(16) char lds[Ring<BM, BN, XA, XB>::BYTES];
-  gemm_tile<T, BM, BN, WM, WN, XA, XB>(p, tm, tn, blockIdx.x, blockIdx.y, lds);
+  gemm_tile<T, BM, BN, WM, WN, XA, XB, TWO>(p, tm, tn, blockIdx.x, blockIdx.y, lds);
 }
 
 // dbias from the sums of act_grad_kernel's workgroups: 64 columns per workgroup, in 16 sums
@@ -537,7 +571,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSums s) {
 
 // Both products of a backward pass, and dbias, by one launch: the sums' workgroups, then
 // the tiles of the product with the longer reduction, then the other's.
-template <typename T, int BM, int BN, int WM, int WN>
+template <typename T, int BM, int BN, int WM, int WN, bool TWO>
 __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void pair_kernel(Product dx, Product dw, ColumnSums s, int tn) {
   __shared__ __align__(16) char lds[Ring<BM, BN, false, true>::BYTES];
   static_assert(Ring<BM, BN, false, true>::BYTES == Ring<BM, BN, true, true>::BYTES, "one ring for both");
@@ -551,9 +585,9 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void pair_kernel(Pr
   const int tx = (int)((dx.M + BM - 1) / BM), tw = (int)((dw.M + BM - 1) / BM);
   const unsigned first = (dx.K >= dw.K ? tx : tw) * tn;
   if ((block < first) == (dx.K >= dw.K))
-    gemm_tile<T, BM, BN, WM, WN, false, true>(dx, tx, tn, block < first ? block : block - first, 0, lds);
+    gemm_tile<T, BM, BN, WM, WN, false, true, TWO>(dx, tx, tn, block < first ? block : block - first, 0, lds);
   else
-    gemm_tile<T, BM, BN, WM, WN, true, true>(dw, tw, tn, block < first ? block : block - first, 0, lds);
+    gemm_tile<T, BM, BN, WM, WN, true, true, TWO>(dw, tw, tn, block < first ? block : block - first, 0, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -808,9 +842,17 @@ hipError_t launch_gemm(const Product& p, int splits, hipStream_t st) {
   if (tm * tn > 0x7fffffffLL) return hipErrorInvalidValue;
   const dim3 grid((unsigned)(tm * tn), splits);
   constexpr int threads = 64 * WM * WN;
-  if (p.across_a) gemm_kernel<T, BM, BN, WM, WN, true, true><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
-  else if (p.across_b) gemm_kernel<T, BM, BN, WM, WN, false, true><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
-  else gemm_kernel<T, BM, BN, WM, WN, false, false><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+  constexpr bool TWO = sizeof(T) == 2;
+  if (TWO && p.a_low) {
+    if (p.across_a) gemm_kernel<T, BM, BN, WM, WN, true, true, TWO><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+    else gemm_kernel<T, BM, BN, WM, WN, false, true, TWO><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+  } else if (p.across_a) {
+    gemm_kernel<T, BM, BN, WM, WN, true, true, false><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+  } else if (p.across_b) {
+    gemm_kernel<T, BM, BN, WM, WN, false, true, false><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+  } else {
+    gemm_kernel<T, BM, BN, WM, WN, false, false, false><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+  }
   return hipGetLastError();
 }
 
@@ -883,6 +925,17 @@ int sum_rows(long long rows, int n, int chunk) {
   return r;
 }
 
+// x = 2 h + 2^(1 - p) l with h and l of a type of p significand bits, to 2^(-2 p): h is half
+// of x, as a factor act' of up to 1.13 takes float16's largest numbers out of its range, and
+// l is scaled to about the size of h, as unscaled it would be one of float16's subnormal
+// numbers from 2^-4 on down.
+template <typename T>
+__device__ __forceinline__ void split(float x, T& h, T& l) {
+  const float half = 0.5f * x;
+  h = from_f32<T>(half);
+  l = fabsf(half) < INFINITY ? from_f32<T>((half - to_f32(h)) * (1 << Chunk<T>::BITS)) : (T)0.f;
+}
+
 template <typename T, int ACT>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p, PackJobs jobs) {
   typedef typename Chunk<T>::type C;
@@ -915,14 +968,24 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p, PackJobs jobs)
         if (ACT != VB_ACT_NONE) s[e] = e < have ? saved[m * p.ld_saved + n + e] : (T)0.f;
       }
     }
-    C v;
+    C v, high, low;
 #pragma unroll
     for (int e = 0; e < EC; ++e) {
       const float x = act_grad<T>(to_f32((T)d[e]), ACT == VB_ACT_NONE ? 0.f : to_f32((T)s[e]), ACT);
       sum[e] += x;
       v[e] = from_f32<T>(x);
+      if (ACT == VB_ACT_GELU || ACT == VB_ACT_SILU) {
+        T h, l;
+        split<T>(x, h, l);
+        high[e] = h, low[e] = l;
+      }
     }
-    if (p.g) *(C*)((T*)p.g + m * p.ld_g + n) = v;
+    if ((ACT == VB_ACT_GELU || ACT == VB_ACT_SILU) && p.g_low) {
+      *(C*)((T*)p.g + m * p.ld_g + n) = high;
+      *(C*)((T*)p.g_low + m * p.ld_g + n) = low;
+    } else if (p.g) {
+      *(C*)((T*)p.g + m * p.ld_g + n) = v;
+    }
     if (p.dres) {
       T* o = (T*)p.dres + m * p.ld_dres + n;
       if (have >= EC) {
@@ -994,8 +1057,14 @@ hipError_t launch_pair_typed(Product dx, Product dw, int tile, const ColumnSums&
   const long long tiles = ((dx.M + tile - 1) / tile + (dw.M + tile - 1) / tile) * tn;
   const long long blocks = tiles + (s.out ? (s.n + 63) / 64 : 0);
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-  if (tile == 64) pair_kernel<T, 64, 64, 2, 2><<<(unsigned)blocks, 256, 0, st>>>(dx, dw, s, tn);
-  else pair_kernel<T, 128, 128, 2, 4><<<(unsigned)blocks, 512, 0, st>>>(dx, dw, s, tn);
+  constexpr bool TWO = sizeof(T) == 2;
+  if (TWO && dx.a_low) {
+    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, TWO><<<(unsigned)blocks, 256, 0, st>>>(dx, dw, s, tn);
+    else pair_kernel<T, 128, 128, 2, 4, TWO><<<(unsigned)blocks, 512, 0, st>>>(dx, dw, s, tn);
+  } else {
+    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, false><<<(unsigned)blocks, 256, 0, st>>>(dx, dw, s, tn);
+    else pair_kernel<T, 128, 128, 2, 4, false><<<(unsigned)blocks, 512, 0, st>>>(dx, dw, s, tn);
+  }
   return hipGetLastError();
 }
 
@@ -1024,7 +1093,9 @@ long long steps_of(long long K, int dtype) { return (K * (long long)elem_size(dt
 
 }  // namespace
 
-Tiling choose_tiling(int dtype, long long M, int N, long long K) {
+Tiling choose_tiling(int dtype, const Product& p) {
+  const long long M = p.M, K = p.K;
+  const int N = p.N;
   const Kind* kinds = dtype == VB_F32 ? k32 : k16;
   const int nk = dtype == VB_F32 ? 3 : 4;
   const long long stages = steps_of(K, dtype);
@@ -1034,7 +1105,7 @@ Tiling choose_tiling(int dtype, long long M, int N, long long K) {
     for (int k = 0; k < nk; ++k) {
       const Kind& c = kinds[k];
       const double tiles = (double)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
-      const double on_cu = std::ceil(tiles * n / 256.0), run = (double)((stages + n - 1) / n);
+      const double on_cu = std::ceil(tiles * n / 256.0), run = (double)((stages + n - 1) / n) * p.passes;
       double us = std::fmax(c.latency, on_cu * c.share) * run + on_cu * c.fixed + 3.0;
       if (n > 1) us += 2.0 + (2.0 * n * M * N * 4.0) / 6e6;
       if (us < best.us && (n == 1 || us < 0.92 * unsplit)) best = Tiling{c.bm, c.bn, n, us};
@@ -1070,10 +1141,10 @@ double list_time(double a, double c, double a2, double c2) {
 // 4096 x 2048 -> 2048 96 | 92.  A split reduction stays one, so that each gradient has the
 // same bits alone as with the other.
 int pair_tile(const Product& dx, const Product& dw, int dtype) {
-  const Tiling x = choose_tiling(dtype, dx.M, dx.N, dx.K), w = choose_tiling(dtype, dw.M, dw.N, dw.K);
+  const Tiling x = choose_tiling(dtype, dx), w = choose_tiling(dtype, dw);
   if (x.splits > 1 || w.splits > 1) return 0;
   const Product &first = dx.K >= dw.K ? dx : dw, &second = dx.K >= dw.K ? dw : dx;
-  const double run = (double)steps_of(first.K, dtype), run2 = (double)steps_of(second.K, dtype);
+  const double run = (double)steps_of(first.K, dtype) * first.passes, run2 = (double)steps_of(second.K, dtype) * second.passes;
   int best = 0;
   double best_us = x.us + w.us + 2.0;
   const Kind* kinds = dtype == VB_F32 ? k32 + 1 : k16 + 2;
@@ -1109,7 +1180,7 @@ bool product_is_narrow(const Product& p, int dtype) {
 
 size_t product_bytes(const Product& p, int dtype) {
   if (product_is_narrow(p, dtype)) return 0;
-  return tiling_bytes(choose_tiling(dtype, p.M, p.N, p.K), p.M, p.N);
+  return tiling_bytes(choose_tiling(dtype, p), p.M, p.N);
 }
 
 hipError_t launch_product(const Product& p, int dtype, hipStream_t st) {
@@ -1118,7 +1189,7 @@ hipError_t launch_product(const Product& p, int dtype, hipStream_t st) {
     if (dtype == VB_BF16) return launch_narrow<bf16>(p, st);
     return launch_narrow<f16>(p, st);
   }
-  const Tiling t = choose_tiling(dtype, p.M, p.N, p.K);
+  const Tiling t = choose_tiling(dtype, p);
   if (dtype == VB_F32) return launch_tiled<float>(p, t, st);
   if (dtype == VB_BF16) return launch_tiled<bf16>(p, t, st);
   return launch_tiled<f16>(p, t, st);

@@ -93,7 +93,7 @@ ForwardPlan plan_forward(const vb_linear_fwd& p) {
   Product& d = f.d;
   d.a = p.x, d.lda = p.ld_x;
   d.b = p.weight, d.ldb = p.ld_w;
-  d.M = p.rows, d.N = p.n_out, d.K = p.n_in;
+  d.M = p.rows, d.N = p.n_out, d.K = p.n_in, d.passes = 1;
   d.bias = p.bias, d.res = p.residual, d.ld_res = p.ld_res;
   d.out = p.y, d.ld_out = p.ld_y, d.pre = p.pre, d.ld_pre = p.ld_pre, d.act = p.act;
   if (p.rows == 0 || product_is_narrow(d, p.dtype)) return f;
@@ -105,10 +105,11 @@ ForwardPlan plan_forward(const vb_linear_fwd& p) {
 }
 
 // The backward products.  g is dy itself without an activation, else (or if dy's rows
-// cannot be read by a large product) a copy.
+// cannot be read by a large product) a copy, in two parts where one number of the type
+// does not hold it.
 struct BackwardPlan {
   Product dx{}, dw{};
-  Part g, x, w, sums, partial;
+  Part g, g_low, x, w, sums, partial;
   int pair = 0;  // tiles of one launch for both products
   size_t total = 0;
 };
@@ -127,8 +128,12 @@ BackwardPlan plan_backward(const vb_linear_bwd& p) {
   b.b = p.x, b.ldb = p.ld_x, b.across_b = true;
   b.M = p.n_out, b.N = p.n_in, b.K = p.rows;
   b.out = p.dweight, b.ld_out = p.ld_dw;
-  if ((p.dx || p.dweight) && (p.act != VB_ACT_NONE || !is_chunked(p.dy, p.ld_dy, p.n_out, dt)))
+  const bool two = dt != VB_F32 && (p.act == VB_ACT_GELU || p.act == VB_ACT_SILU) && !p.round_g;
+  a.passes = b.passes = two ? 2 : 1;
+  if ((p.dx || p.dweight) && (p.act != VB_ACT_NONE || !is_chunked(p.dy, p.ld_dy, p.n_out, dt))) {
     f.g.take(f.total, p.rows * chunked_row(p.n_out, dt));
+    if (two) f.g_low.take(f.total, p.rows * chunked_row(p.n_out, dt));
+  }
   const size_t row = chunked_row(p.n_in, dt);
   if (p.dweight && !is_chunked(p.x, p.ld_x, p.n_in, dt)) f.x.take(f.total, p.rows * row);
   if (p.dx && !is_chunked(p.weight, p.ld_w, p.n_in, dt)) f.w.take(f.total, p.n_out * row);
@@ -194,6 +199,7 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
   if (!p) return fail(VB_EINVAL, "%s: NULL argument", fn);
   TRY(check_sizes(fn, p->rows, p->n_in, p->n_out, p->dtype));
   if (p->act < VB_ACT_NONE || p->act > VB_ACT_SILU) return fail(VB_EINVAL, "%s: unknown activation %d", fn, p->act);
+  if (p->round_g != 0 && p->round_g != 1) return fail(VB_EINVAL, "%s: round_g must be 0 or 1 (got %d)", fn, p->round_g);
   const bool some = p->rows > 0;
   TRY(check_matrix(fn, "dy", p->dy, p->ld_dy, p->n_out, p->dtype, some));
   TRY(check_matrix(fn, "x", p->x, p->ld_x, p->n_in, p->dtype, some && p->dweight));
@@ -221,12 +227,12 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
     ActGrad g{};
     g.dy = p->dy, g.ld_dy = p->ld_dy;
     g.saved = p->act == VB_ACT_NONE ? nullptr : p->saved, g.ld_saved = p->ld_saved;
-    g.g = f.g.in(ws), g.ld_g = (long long)chunked_row(p->n_out, p->dtype) / es;
+    g.g = f.g.in(ws), g.g_low = f.g_low.in(ws), g.ld_g = (long long)chunked_row(p->n_out, p->dtype) / es;
     g.dres = p->dresidual, g.ld_dres = p->ld_dres;
     g.dbias = p->dbias, g.partial = (float*)f.sums.in(ws);
     g.rows = p->rows, g.n = p->n_out, g.act = p->act;
     HIPCHK(launch_act_grad(g, jobs, p->dtype, sums, st));
-    if (f.g.used) f.dx.a = f.dw.a = g.g, f.dx.lda = f.dw.lda = g.ld_g;
+    if (f.g.used) f.dx.a = f.dw.a = g.g, f.dx.a_low = f.dw.a_low = g.g_low, f.dx.lda = f.dw.lda = g.ld_g;
   } else {
     HIPCHK(launch_pack(jobs, p->dtype, st));
   }

@@ -19,8 +19,12 @@ inline size_t elem_size(int dtype) { return dtype == VB_F32 ? 4 : 2; }
 // across_a (likewise b); across_a implies across_b.  Unless
 // product_is_narrow, both operands are chunked (is_chunked over their rows as
 // stored; a row along the reduction may also be one that launch_pack filled with zeros).
+// With passes = 2 (16-bit types, across_b) A is 2 a + 2^(1 - p) a_low, p the type's
+// significand bits, and a_low is stored like a.
 struct Product {
   const void* a;
+  const void* a_low;
+  int passes;
   const void* b;
   long long lda, ldb;
   bool across_a, across_b;
@@ -72,13 +76,15 @@ struct PackJobs {
 hipError_t launch_pack(PackJobs jobs, int dtype, hipStream_t st);
 
 // v = dy * act'(saved), in float32: g = v (rows of ld_g elements that start on 16-byte
-// boundaries, zeros to the end of the last chunk), dres = v, dbias = column sums of v;
-// each optional.  partial: act_grad_bytes of workspace for dbias.
+// boundaries, zeros to the end of the last chunk) or, with g_low, v = 2 g + 2^(1 - p) g_low
+// as in Product; dres = v, dbias = column sums of v; each optional.  partial:
+// act_grad_bytes of workspace for dbias.
 struct ActGrad {
   const void* dy;
   const void* saved;
   long long ld_dy, ld_saved;
   void* g;
+  void* g_low;
   long long ld_g;
   void* dres;
   long long ld_dres;

@@ -34,7 +34,7 @@ class vb_linear_bwd(ctypes.Structure):
     _fields_ = [("rows", _i64), ("n_in", _i32), ("n_out", _i32), ("dtype", _i32), ("act", _i32),
                 ("dy", _P), ("ld_dy", _i64), ("x", _P), ("ld_x", _i64), ("weight", _P), ("ld_w", _i64),
                 ("saved", _P), ("ld_saved", _i64), ("dx", _P), ("ld_dx", _i64), ("dweight", _P), ("ld_dw", _i64),
-                ("dbias", _P), ("dresidual", _P), ("ld_dres", _i64)]
+                ("dbias", _P), ("dresidual", _P), ("ld_dres", _i64), ("round_g", _i32)]
 
 
 class vb_cross_entropy_args(ctypes.Structure):
@@ -44,7 +44,7 @@ class vb_cross_entropy_args(ctypes.Structure):
 
 
 _FWD = struct.Struct("qiiiiQqQqQQqQqQq")    # vb_linear_fwd
-_BWD = struct.Struct("qiiiiQqQqQqQqQqQqQQq")  # vb_linear_bwd
+_BWD = struct.Struct("qiiiiQqQqQqQqQqQqQQqi4x")  # vb_linear_bwd
 _LOSS = struct.Struct("qiiQqQqffQQQq")      # vb_cross_entropy_args
 assert (_FWD.size, _BWD.size, _LOSS.size) == tuple(
     ctypes.sizeof(c) for c in (vb_linear_fwd, vb_linear_bwd, vb_cross_entropy_args))
@@ -136,17 +136,18 @@ def _workspace(n: int, device) -> torch.Tensor:
 
 
 def linear_workspace(x: torch.Tensor, weight: torch.Tensor, backward: bool = False) -> torch.Tensor:
-    """A workspace for `linear` calls (or `linear_backward` calls, with any activation and all
-    gradients) on tensors of these sizes and strides, to keep between calls."""
+    """A workspace for `linear` calls (or `linear_backward` calls, with any activation, all
+    gradients and either round_g) on tensors of these sizes and strides, to keep between calls."""
     _device(x)
     rows, n_in = x.shape
     n_out = weight.shape[0]
     ld_x, ld_w = _matrix("x", x, rows, n_in, x), _matrix("weight", weight, n_out, n_in, x)
     head = (rows, n_in, n_out, _dtype(x))
     if backward:
-        p = _BWD.pack(*head, ACTS["silu"], 0, n_out, x.data_ptr(), ld_x, weight.data_ptr(), ld_w, 0, n_out, 16, n_in,
-                      16, n_in, 16, 16, n_out)
-        return _workspace(_size("vb_linear_backward_workspace", p), x.device)
+        need = [_size("vb_linear_backward_workspace",
+                      _BWD.pack(*head, ACTS["silu"], 0, n_out, x.data_ptr(), ld_x, weight.data_ptr(), ld_w, 0, n_out,
+                                16, n_in, 16, n_in, 16, 16, n_out, round_g)) for round_g in (0, 1)]
+        return _workspace(max(need), x.device)
     p = _FWD.pack(*head, 0, x.data_ptr(), ld_x, weight.data_ptr(), ld_w, 0, 0, n_out, 16, n_out, 0, n_out)
     return _workspace(_size("vb_linear_forward_workspace", p), x.device)
 
@@ -185,9 +186,12 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
 
 def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act: str = "none",
                     saved: Optional[torch.Tensor] = None, want_x: bool = True, want_weight: bool = True,
-                    want_bias: bool = True, want_residual: bool = False, ws: Optional[torch.Tensor] = None):
+                    want_bias: bool = True, want_residual: bool = False, ws: Optional[torch.Tensor] = None,
+                    round_g: bool = False):
     """Gradients of `linear` (vb_linear_backward) for the gradient dy of y: (dx, dweight, dbias,
-    dresidual), None where not wanted.  saved: y for relu, pre for gelu and silu."""
+    dresidual), None where not wanted.  saved: y for relu, pre for gelu and silu.  round_g: with
+    gelu or silu in a 16-bit type, dx and dweight from the gradient of pre rounded to the type, in
+    about half the time."""
     dev = _device(x)
     dt = _dtype(x)
     if x.dim() != 2 or weight.dim() != 2:
@@ -208,7 +212,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act
     p = _BWD.pack(rows, n_in, n_out, dt, code, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, weight.data_ptr(), ld_w,
                   0 if saved is None else saved.data_ptr(), ld_s, 0 if dx is None else dx.data_ptr(), n_in,
                   0 if dw is None else dw.data_ptr(), n_in, 0 if db is None else db.data_ptr(),
-                  0 if dr is None else dr.data_ptr(), n_out)
+                  0 if dr is None else dr.data_ptr(), n_out, bool(round_g))
     if ws is None:
         ws = _workspace(_size("vb_linear_backward_workspace", p), x.device)
     _run("vb_linear_backward", p, ws.data_ptr(), ws.nbytes, _stream(dev))
