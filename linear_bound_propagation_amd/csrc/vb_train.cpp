@@ -328,9 +328,11 @@ vb_status run_clip(const ClipCall& c) {
     return t.count > 0;
   };
   ClipTable<N> t;
+  // one workgroup for few numbers, also for none at all, when the norm is written all the same
   long long total = 0;
-  for (int32_t k = 0; k < c.n_tensors; ++k) total += c.sizes[k];
-  if (total <= CLIP_SMALL && c.n_tensors <= N) {
+  int32_t filled = 0;
+  for (int32_t k = 0; k < c.n_tensors; ++k) total += c.sizes[k], filled += c.sizes[k] > 0;
+  if (total <= CLIP_SMALL && filled <= N) {
     fill(t, CLIP_SMALL_CHUNK);
     HIPCHK(launch_clip_small(t, c.max_norm, c.norm, c.st));
     return VB_OK;
