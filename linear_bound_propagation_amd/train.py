@@ -135,6 +135,13 @@ def _workspace(n: int, device) -> torch.Tensor:
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
+def _scratch(ws: torch.Tensor, dev: int) -> Tuple[int, int]:
+    """Address and bytes of a caller's workspace; the library checks its size and alignment."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on the current GPU, got strides {ws.stride()} on {ws.device}")
+    return ws.data_ptr(), ws.nbytes
+
+
 def linear_workspace(x: torch.Tensor, weight: torch.Tensor, backward: bool = False) -> torch.Tensor:
     """A workspace for `linear` calls (or `linear_backward` calls, with any activation, all
     gradients and either round_g) on tensors of these sizes and strides, to keep between calls."""
@@ -180,7 +187,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
                   y.data_ptr(), ld_y, 0 if pre is None else pre.data_ptr(), n_out)
     if ws is None:
         ws = _workspace(_size("vb_linear_forward_workspace", p), x.device)
-    _run("vb_linear_forward", p, ws.data_ptr(), ws.nbytes, _stream(dev))
+    _run("vb_linear_forward", p, *_scratch(ws, dev), _stream(dev))
     return (y, pre) if want_pre else y
 
 
@@ -215,7 +222,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act
                   0 if dr is None else dr.data_ptr(), n_out, bool(round_g))
     if ws is None:
         ws = _workspace(_size("vb_linear_backward_workspace", p), x.device)
-    _run("vb_linear_backward", p, ws.data_ptr(), ws.nbytes, _stream(dev))
+    _run("vb_linear_backward", p, *_scratch(ws, dev), _stream(dev))
     return dx, dw, db, dr
 
 
@@ -251,7 +258,7 @@ def cross_entropy(logits: torch.Tensor, labels: torch.Tensor, ignore_index: int 
         ws = cross_entropy_workspace(logits)
     p = _LOSS.pack(rows, classes, dt, logits.data_ptr(), ld, labels.data_ptr(), ignore_index, label_smoothing,
                    grad_scale, loss.data_ptr(), row_loss.data_ptr(), 0 if dlogits is None else dlogits.data_ptr(), ld_d)
-    _run("vb_cross_entropy", p, ws.data_ptr(), ws.nbytes, _stream(dev))
+    _run("vb_cross_entropy", p, *_scratch(ws, dev), _stream(dev))
     return loss, row_loss, dlogits
 
 
@@ -294,5 +301,5 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     if ws is None:
         ws = _workspace(_size("vb_clip_grad_norm_workspace", n, sizes.buffer_info()[0]), norm.device)
     _run("vb_clip_grad_norm", n, src.buffer_info()[0], dst or None, sizes.buffer_info()[0], types.buffer_info()[0],
-         max_norm, norm.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(dev))
+         max_norm, norm.data_ptr(), *_scratch(ws, dev), _stream(dev))
     return norm, list(grads if out is None else out)
