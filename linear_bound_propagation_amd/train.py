@@ -228,6 +228,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act
 
 def cross_entropy_workspace(logits: torch.Tensor) -> torch.Tensor:
     """A workspace for `cross_entropy` calls of these sizes, to keep between calls."""
+    _device(logits)
     rows, classes = logits.shape
     return _workspace(_size("vb_cross_entropy_workspace", rows, classes, _dtype(logits)), logits.device)
 
@@ -264,6 +265,8 @@ def cross_entropy(logits: torch.Tensor, labels: torch.Tensor, ignore_index: int 
 
 def clip_grad_norm_workspace(grads: Sequence[torch.Tensor]) -> torch.Tensor:
     """A workspace for `clip_grad_norm` calls on tensors of these sizes, to keep between calls."""
+    if len(grads):
+        _device(grads[0])
     sizes = array("q", [g.numel() for g in grads])
     return _workspace(_size("vb_clip_grad_norm_workspace", len(sizes), sizes.buffer_info()[0]),
                       grads[0].device if len(grads) else "cuda")

@@ -16,3 +16,11 @@ def test_host_and_strided_workspaces_are_refused():
     assert train._scratch(own, -1) == (own.data_ptr(), 4 * 4096)
     with pytest.raises(ValueError, match="ws must be contiguous"):
         train._scratch(own[::2], -1)
+
+
+def test_workspaces_are_not_made_for_host_tensors():
+    for call in (lambda: train.linear_workspace(torch.zeros(4, 3), torch.zeros(5, 3)),
+                 lambda: train.cross_entropy_workspace(torch.zeros(4, 3)),
+                 lambda: train.clip_grad_norm_workspace([torch.zeros(4)])):
+        with pytest.raises(ValueError, match="current GPU"):
+            call()
