@@ -520,7 +520,9 @@ __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned bl
 template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB, bool TWO>
 __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Product p, int tm, int tn) {
   __shared__ __align__(16) char lds[Ring<BM, BN, XA, XB>::BYTES];
-  gemm_tile<T, BM, BN, WM, WN, XA, XB, TWO>(p, tm, tn, blockIdx.x, blockIdx.y, lds);
+  const unsigned block = workgroup_number();
+  if (block >= (unsigned)tm * tn) return;  // the whole workgroup
+  gemm_tile<T, BM, BN, WM, WN, XA, XB, TWO>(p, tm, tn, block, blockIdx.y, lds);
 }
 
 // dbias from the sums of act_grad_kernel's workgroups: 64 columns per workgroup, in 16 sums
@@ -575,7 +577,7 @@ template <typename T, int BM, int BN, int WM, int WN, bool TWO>
 __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void pair_kernel(Product dx, Product dw, ColumnSums s, int tn) {
   __shared__ __align__(16) char lds[Ring<BM, BN, false, true>::BYTES];
   static_assert(Ring<BM, BN, false, true>::BYTES == Ring<BM, BN, true, true>::BYTES, "one ring for both");
-  unsigned block = blockIdx.x;
+  unsigned block = workgroup_number();
   const unsigned sums = s.out ? (s.n + 63) / 64 : 0;
   if (block < sums) {
     sum_columns<T, WM * WN>(s, block, (float*)lds);
@@ -583,6 +585,7 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void pair_kernel(Pr
   }
   block -= sums;
   const int tx = (int)((dx.M + BM - 1) / BM), tw = (int)((dw.M + BM - 1) / BM);
+  if (block >= ((unsigned)tx + tw) * tn) return;  // the whole workgroup
   const unsigned first = (dx.K >= dw.K ? tx : tw) * tn;
   if ((block < first) == (dx.K >= dw.K))
     gemm_tile<T, BM, BN, WM, WN, false, true, TWO>(dx, tx, tn, block < first ? block : block - first, 0, lds);
@@ -810,7 +813,7 @@ hipError_t launch_narrow(const Product& p, hipStream_t st) {
 template <typename T>
 __global__ __launch_bounds__(256) void join_kernel(Product p, int splits) {
   const int quads = p.ld_partial / 4;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long i = (long long)workgroup_number() * 256 + threadIdx.x;
   const long long m = i / quads;
   const int n = (int)(i % quads) * 4;
   if (m >= p.M) return;
@@ -840,7 +843,7 @@ template <typename T, int BM, int BN, int WM, int WN>
 hipError_t launch_gemm(const Product& p, int splits, hipStream_t st) {
   const long long tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
   if (tm * tn > 0x7fffffffLL) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)(tm * tn), splits);
+  const dim3 grid = grid_of(tm * tn, splits);
   constexpr int threads = 64 * WM * WN;
   constexpr bool TWO = sizeof(T) == 2;
   if (TWO && p.a_low) {
@@ -878,7 +881,7 @@ hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
   if (e != hipSuccess || splits == 1) return e;
   const long long quads = p.M * (p.ld_partial / 4), blocks = (quads + 255) / 256;
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-  join_kernel<T><<<dim3((unsigned)blocks), 256, 0, st>>>(p, splits);
+  join_kernel<T><<<grid_of(blocks), 256, 0, st>>>(p, splits);
   return hipGetLastError();
 }
 
@@ -909,7 +912,7 @@ __device__ __forceinline__ void pack_chunk(const PackJobs& jobs, unsigned block)
 
 template <typename T>
 __global__ __launch_bounds__(256) void pack_kernel(PackJobs jobs) {
-  pack_chunk<T>(jobs, blockIdx.x);
+  pack_chunk<T>(jobs, workgroup_number());
 }
 
 // g = dy act'(saved), its copies and its column sums.  A thread has one chunk of columns
@@ -942,12 +945,13 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p, PackJobs jobs)
   typedef typename Loose<T>::type LC;
   constexpr int EC = 16 / sizeof(T);
   __shared__ float red[8][32 * EC + 1];
-  if (blockIdx.x >= p.blocks) {  // the copies that the products need, by the same launch
-    pack_chunk<T>(jobs, blockIdx.x - p.blocks);
+  const unsigned block = workgroup_number();
+  if (block >= p.blocks) {  // the copies that the products need, by the same launch
+    pack_chunk<T>(jobs, block - p.blocks);
     return;
   }
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const unsigned across = (p.n + 32 * EC - 1) / (32 * EC), bx = blockIdx.x % across, by = blockIdx.x / across;
+  const unsigned across = (p.n + 32 * EC - 1) / (32 * EC), bx = block % across, by = block / across;
   const int n = (bx * 32 + c) * EC;
   const long long m0 = (long long)by * p.part_rows;
   const T* dy = (const T*)p.dy;
@@ -1014,7 +1018,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p, PackJobs jobs)
 }
 
 __global__ __launch_bounds__(256) void fill_zero_kernel(unsigned short* p, long long rows, long long n, long long ld) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long i = (long long)workgroup_number() * 256 + threadIdx.x;
   if (i < rows * n) p[i / n * ld + i % n] = 0;
 }
 
@@ -1041,7 +1045,7 @@ hipError_t launch_act_grad_typed(ActGrad p, const PackJobs& jobs, unsigned copie
   p.blocks = (unsigned)blocks;
   if (parts == 1) p.partial = nullptr;
   else if (p.dbias) sums = {p.partial, (int)parts, p.n, p.dbias};
-  const dim3 grid((unsigned)(blocks + copies));
+  const dim3 grid = grid_of(blocks + copies);
   if (p.act == VB_ACT_NONE) act_grad_kernel<T, VB_ACT_NONE><<<grid, 256, 0, st>>>(p, jobs);
   else if (p.act == VB_ACT_RELU) act_grad_kernel<T, VB_ACT_RELU><<<grid, 256, 0, st>>>(p, jobs);
   else if (p.act == VB_ACT_GELU) act_grad_kernel<T, VB_ACT_GELU><<<grid, 256, 0, st>>>(p, jobs);
@@ -1059,11 +1063,11 @@ hipError_t launch_pair_typed(Product dx, Product dw, int tile, const ColumnSums&
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   constexpr bool TWO = sizeof(T) == 2;
   if (TWO && dx.a_low) {
-    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, TWO><<<(unsigned)blocks, 256, 0, st>>>(dx, dw, s, tn);
-    else pair_kernel<T, 128, 128, 2, 4, TWO><<<(unsigned)blocks, 512, 0, st>>>(dx, dw, s, tn);
+    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, TWO><<<grid_of(blocks), 256, 0, st>>>(dx, dw, s, tn);
+    else pair_kernel<T, 128, 128, 2, 4, TWO><<<grid_of(blocks), 512, 0, st>>>(dx, dw, s, tn);
   } else {
-    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, false><<<(unsigned)blocks, 256, 0, st>>>(dx, dw, s, tn);
-    else pair_kernel<T, 128, 128, 2, 4, false><<<(unsigned)blocks, 512, 0, st>>>(dx, dw, s, tn);
+    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, false><<<grid_of(blocks), 256, 0, st>>>(dx, dw, s, tn);
+    else pair_kernel<T, 128, 128, 2, 4, false><<<grid_of(blocks), 512, 0, st>>>(dx, dw, s, tn);
   }
   return hipGetLastError();
 }
@@ -1204,9 +1208,9 @@ hipError_t launch_pack(PackJobs jobs, int dtype, hipStream_t st) {
   const unsigned blocks = pack_blocks(jobs, dtype);
   if (blocks == ~0u) return hipErrorInvalidValue;
   if (!blocks) return hipSuccess;
-  if (dtype == VB_F32) pack_kernel<float><<<blocks, 256, 0, st>>>(jobs);
-  else if (dtype == VB_BF16) pack_kernel<bf16><<<blocks, 256, 0, st>>>(jobs);
-  else pack_kernel<f16><<<blocks, 256, 0, st>>>(jobs);
+  if (dtype == VB_F32) pack_kernel<float><<<grid_of(blocks), 256, 0, st>>>(jobs);
+  else if (dtype == VB_BF16) pack_kernel<bf16><<<grid_of(blocks), 256, 0, st>>>(jobs);
+  else pack_kernel<f16><<<grid_of(blocks), 256, 0, st>>>(jobs);
   return hipGetLastError();
 }
 
@@ -1241,7 +1245,7 @@ hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long l
   const long long n = row_bytes / 2;
   const long long blocks = (rows * n + 255) / 256;
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-  fill_zero_kernel<<<dim3((unsigned)blocks), 256, 0, st>>>((unsigned short*)p, rows, n, ld_bytes / 2);
+  fill_zero_kernel<<<grid_of(blocks), 256, 0, st>>>((unsigned short*)p, rows, n, ld_bytes / 2);
   return hipGetLastError();
 }
 

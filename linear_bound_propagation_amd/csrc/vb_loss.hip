@@ -316,7 +316,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH, CH <= 8 ? 8 : 4) void loss_row
                                                                         const long long* count, float* row_loss) {
   __shared__ float red[16];
   constexpr int PER = TH < 256 ? 256 / TH : 1;
-  const long long r = (long long)blockIdx.x * PER + threadIdx.x / TH;
+  const long long r = (long long)workgroup_number() * PER + threadIdx.x / TH;
   if (r >= p.rows) return;  // whole wavefronts, and no barrier when PER > 1
   const float scale = p.grad_scale / (float)*count;
   float loss;
@@ -350,8 +350,9 @@ hipError_t launch_typed(const vb_cross_entropy_args& p, void* ws, hipStream_t st
     return hipGetLastError();
   }
   loss_count_kernel<<<1, 1024, 0, st>>>(p.labels, p.rows, p.ignore_index, count);
+  if (const hipError_t e = hipGetLastError()) return e;
   if (p.rows > 0) {
-    const unsigned rows = (unsigned)p.rows, quads = (unsigned)((p.rows + 3) / 4);
+    const dim3 rows = grid_of(p.rows), quads = grid_of((p.rows + 3) / 4);
     if (chunks <= 64) loss_rows_kernel<T, 64, 1><<<quads, 256, 0, st>>>(p, count, row_loss);
     else if (chunks <= 256) loss_rows_kernel<T, 64, 4><<<quads, 256, 0, st>>>(p, count, row_loss);
     else if (chunks <= 1024) loss_rows_kernel<T, 256, 4><<<rows, 256, 0, st>>>(p, count, row_loss);
@@ -362,6 +363,7 @@ hipError_t launch_typed(const vb_cross_entropy_args& p, void* ws, hipStream_t st
     else if (chunks <= 12288) loss_rows_kernel<T, 1024, 12><<<rows, 1024, 0, st>>>(p, count, row_loss);
     else if (chunks <= 16384) loss_rows_kernel<T, 1024, 16><<<rows, 1024, 0, st>>>(p, count, row_loss);
     else loss_rows_kernel<T, 1024, 0><<<rows, 1024, 0, st>>>(p, count, row_loss);
+    if (const hipError_t e = hipGetLastError()) return e;
   }
   if (p.loss) loss_mean_kernel<<<1, 1024, 0, st>>>(row_loss, p.rows, count, p.loss);
   return hipGetLastError();

@@ -288,7 +288,7 @@ long long clip_chunks(int32_t n, const int64_t* sizes, int& chunk) {
     for (int32_t i = 0; i < n; ++i) {
       if (sizes[i] < 0 || sizes[i] > (INT64_C(1) << 44)) return -1;
       count += (sizes[i] + c - 1) / c;
-      if (count > 0x7fffffffLL && c == CLIP_CHUNK) return -1;
+      if (count > CLIP_MAX_CHUNKS && c == CLIP_CHUNK) return -1;
     }
     chunk = c;
     if (c == CLIP_CHUNK || count <= CLIP_FEW) return count;

@@ -15,6 +15,15 @@ vb_status set_error(vb_status s, const char* msg) noexcept;
 
 inline size_t elem_size(int dtype) { return dtype == VB_F32 ? 4 : 2; }
 
+// Grid of `blocks` workgroups, at most 2^31: a dimension of a launch holds less than 2^32
+// work-items, so from GRID_X workgroups of up to 1024 threads on they go on in z (y is the
+// kernel's).  Kernels number them by workgroup_number, and those past the last have no work.
+constexpr unsigned GRID_X = 1u << 21;  // a multiple of the number of XCDs
+inline dim3 grid_of(long long blocks, unsigned y = 1) {
+  if (blocks <= GRID_X) return dim3((unsigned)blocks, y);
+  return dim3(GRID_X, y, (unsigned)((blocks + GRID_X - 1) / GRID_X));
+}
+
 // C(m, n) = sum_k A(m, k) B(n, k) with A(m, k) = a[m * lda + k], or a[k * lda + m] when
 // across_a (likewise b); across_a implies across_b.  Unless
 // product_is_narrow, both operands are chunked (is_chunked over their rows as
@@ -122,6 +131,7 @@ constexpr int CLIP_TENSORS = 112, CLIP_FEW_TENSORS = 16;
 constexpr int CLIP_CHUNK = 16384;        // of a workgroup of 256
 constexpr int CLIP_FEW_CHUNK = 2048;     // the same, while there are at most
 constexpr int CLIP_FEW = 1024;           // this many chunks
+constexpr long long CLIP_MAX_CHUNKS = (1 << 24) - 1;  // of a call: 2^38 elements
 constexpr int CLIP_SMALL_CHUNK = 512;    // of a wavefront, when one workgroup does all:
 constexpr long long CLIP_SMALL = 16384;  // up to this many elements
 template <int N>
