@@ -13,10 +13,11 @@ namespace {
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 
-// exp and the normal CDF: to float32 accuracy for float32 data; for 16-bit data the
-// hardware exponential and, on its exp(-v^2 / 2) = e, a polynomial in t = 1 / (1 + 0.35 |v|)
-// for Phi(-|v|) / e, fitted here to the smallest relative error over |v| < 14.5 (2^-20.6; e is
-// 0 beyond), so that the lower tail keeps its bits too.
+// exp and the normal CDF: to float32 accuracy for float32 data.  For 16-bit data the
+// hardware exponential, whose argument v log2(e) is rounded (relative error |v| 2^-24, of
+// results that are rounded to 2^-9 or 2^-12), and, on its exp(-v^2 / 2) = e, a polynomial in
+// t = 1 / (1 + 0.35 |v|) for Phi(-|v|) / e, fitted here to the smallest relative error over
+// |v| < 14.5 (2^-20.6; e is 0 beyond), so that the lower tail keeps its bits too.
 template <typename T>
 __device__ __forceinline__ float exp_of(float v) {
   return sizeof(T) == 4 ? expf(v) : __expf(v);

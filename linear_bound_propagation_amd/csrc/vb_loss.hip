@@ -19,8 +19,10 @@ namespace vb {
 
 namespace {
 
-// to float32 accuracy for float32 logits, else the hardware exponential (relative
-// error 2^-20 at -16, where p is far below a 16-bit gradient's last place)
+// To float32 accuracy for float32 logits, else the hardware exponential, whose argument is
+// rounded (relative error 2^-20 at -16).  In a 16-bit gradient that is nothing.  In a loss the
+// numbers far below the top count little, and the float32 sum's own rounding is as large: worst
+// relative error of 64 losses of 65536 normal logits 2^-22.8 in bfloat16, 2^-22.5 in float32.
 template <typename T>
 __device__ __forceinline__ float exp_of(float v) {
   return sizeof(T) == 4 ? expf(v) : __expf(v);
