@@ -23,6 +23,9 @@
  *    otherwise.  Any element alignment is accepted; rows that start on 16-byte
  *    boundaries are faster.
  *  - Infinities and NaN follow the formulas.
+ *  - What a call writes shares no memory with its other arguments, except where the
+ *    call names an output that may be an input itself.  Overlaps are refused; rows
+ *    of one matrix between those of another (column ranges of one buffer) are none.
  */
 #ifndef VB_TRAIN_H
 #define VB_TRAIN_H
@@ -54,8 +57,7 @@ typedef struct {
   const void* bias;                      /* [n_out] or NULL                        */
   const void* residual; int64_t ld_res;  /* [rows][n_out] or NULL                  */
   void* y;              int64_t ld_y;    /* [rows][n_out]; may be residual itself  */
-                                         /* (the same pointer and ld), no other    */
-                                         /* overlap                                */
+                                         /* (the same pointer and ld)              */
   void* pre;            int64_t ld_pre;  /* [rows][n_out] or NULL: pre, rounded to */
                                          /* dtype, for the backward pass of        */
                                          /* VB_ACT_GELU / VB_ACT_SILU              */
@@ -67,7 +69,7 @@ typedef struct {
  * elsewhere: where saved is not > 0, g is 0 whatever dy holds); pre for GELU
  * and SILU.  dx, dweight, dbias and dresidual may each be NULL.  With rows = 0
  * dweight and dbias are set to zero.  dresidual may be dy itself (same pointer
- * and ld); no other overlap.
+ * and ld).
  * The matrix cores take operands of dtype.  With GELU and SILU in a 16-bit type g
  * is no number of that type: it enters both products as the sum of two (relative
  * error 2^-16 in bfloat16, 2^-22 in float16), which multiplies twice, or, with

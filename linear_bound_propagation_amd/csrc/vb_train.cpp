@@ -1,8 +1,10 @@
 // C ABI of the training operators (include/vb_train.h): argument checks and the
 // sequence of launches.  Nothing here throws.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <new>
 
 #include "vb_train.h"
 #include "vb_train_internal.h"
@@ -57,6 +59,35 @@ vb_status check_ws(const char* fn, const void* ws, size_t ws_bytes, size_t need)
   if (!ws || ws_bytes < need)
     return fail(VB_ENOMEM, "%s: workspace too small (%zu bytes, needs %zu)", fn, ws ? ws_bytes : (size_t)0, need);
   if ((uintptr_t)ws & 15) return fail(VB_EINVAL, "%s: workspace is not 16-byte aligned", fn);
+  return VB_OK;
+}
+
+// An argument's memory, and whether the call writes it.
+struct Named {
+  const char* name;
+  Span span;
+  bool written;
+};
+
+Named matrix(const char* name, const void* p, int64_t rows, int64_t n, int64_t ld, int dtype, bool written) {
+  const int64_t es = (int64_t)elem_size(dtype);
+  return {name, {(uintptr_t)p, rows, n * es, ld * es}, written};
+}
+
+Named block(const char* name, const void* p, int64_t bytes, bool written) {
+  return {name, {(uintptr_t)p, 1, bytes, bytes}, written};
+}
+
+// What is written shares no memory with anything else.  over: an output that may be that
+// input itself (their pointers and leading dimensions are equal).
+template <int N>
+vb_status check_overlaps(const char* fn, const Named (&m)[N], int out = -1, int over = -1) {
+  for (int i = 0; i < N; ++i)
+    for (int j = 0; j < N; ++j) {
+      if (!m[i].written || i == j || (m[j].written && j < i)) continue;
+      if (i == out && j == over && m[i].span.at == m[j].span.at) continue;
+      if (overlap(m[i].span, m[j].span)) return fail(VB_EINVAL, "%s: %s overlaps %s", fn, m[i].name, m[j].name);
+    }
   return VB_OK;
 }
 
@@ -183,6 +214,14 @@ extern "C" vb_status vb_linear_forward(const vb_linear_fwd* p, void* ws, size_t 
   if (p->residual == p->y && p->ld_res != p->ld_y) return fail(VB_ESHAPE, "%s: y over residual needs the same leading dimension", fn);
   ForwardPlan f = plan_forward(*p);
   TRY(check_ws(fn, ws, ws_bytes, f.total));
+  const Named memory[] = {matrix("y", p->y, p->rows, p->n_out, p->ld_y, p->dtype, true),
+                          matrix("pre", p->pre, p->rows, p->n_out, p->ld_pre, p->dtype, true),
+                          block("the workspace", ws, (int64_t)f.total, true),
+                          matrix("residual", p->residual, p->rows, p->n_out, p->ld_res, p->dtype, false),
+                          matrix("x", p->x, p->rows, p->n_in, p->ld_x, p->dtype, false),
+                          matrix("weight", p->weight, p->n_out, p->n_in, p->ld_w, p->dtype, false),
+                          matrix("bias", p->bias, 1, p->n_out, p->n_out, p->dtype, false)};
+  TRY(check_overlaps(fn, memory, 0, 3));
   const hipStream_t st = (hipStream_t)stream;
   const long long ld = (long long)(chunked_row(p->n_in, p->dtype) / elem_size(p->dtype));
   HIPCHK(launch_pack({{{p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws)}, {p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws)}}},
@@ -214,19 +253,30 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
     return fail(VB_ESHAPE, "%s: dresidual over dy needs the same leading dimension", fn);
   const hipStream_t st = (hipStream_t)stream;
   const long long es = (long long)elem_size(p->dtype);
+  BackwardPlan f = plan_backward(*p);
+  if (some) TRY(check_ws(fn, ws, ws_bytes, f.total));
+  const void* saved = p->act == VB_ACT_NONE ? nullptr : p->saved;
+  const Named memory[] = {matrix("dresidual", p->dresidual, p->rows, p->n_out, p->ld_dres, p->dtype, true),
+                          matrix("dx", p->dx, p->rows, p->n_in, p->ld_dx, p->dtype, true),
+                          matrix("dweight", p->dweight, p->n_out, p->n_in, p->ld_dw, p->dtype, true),
+                          matrix("dbias", p->dbias, 1, p->n_out, p->n_out, p->dtype, true),
+                          block("the workspace", ws, (int64_t)f.total, true),
+                          matrix("dy", p->dy, p->rows, p->n_out, p->ld_dy, p->dtype, false),
+                          matrix("x", p->dweight ? p->x : nullptr, p->rows, p->n_in, p->ld_x, p->dtype, false),
+                          matrix("weight", p->dx ? p->weight : nullptr, p->n_out, p->n_in, p->ld_w, p->dtype, false),
+                          matrix("saved", saved, p->rows, p->n_out, p->ld_saved, p->dtype, false)};
+  TRY(check_overlaps(fn, memory, 0, 5));
   if (!some) {
     if (p->dweight) HIPCHK(launch_fill_zero(p->dweight, p->n_out, p->n_in * es, p->ld_dw * es, st));
     if (p->dbias) HIPCHK(launch_fill_zero(p->dbias, 1, p->n_out * es, p->n_out * es, st));
     return VB_OK;
   }
-  BackwardPlan f = plan_backward(*p);
-  TRY(check_ws(fn, ws, ws_bytes, f.total));
   const PackJobs jobs = {{{p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws)}, {p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws)}}};
   ColumnSums sums{};
   if (f.g.used || p->dbias || p->dresidual) {
     ActGrad g{};
     g.dy = p->dy, g.ld_dy = p->ld_dy;
-    g.saved = p->act == VB_ACT_NONE ? nullptr : p->saved, g.ld_saved = p->ld_saved;
+    g.saved = saved, g.ld_saved = p->ld_saved;
     g.g = f.g.in(ws), g.g_low = f.g_low.in(ws), g.ld_g = (long long)chunked_row(p->n_out, p->dtype) / es;
     g.dres = p->dresidual, g.ld_dres = p->ld_dres;
     g.dbias = p->dbias, g.partial = (float*)f.sums.in(ws);
@@ -275,6 +325,12 @@ extern "C" vb_status vb_cross_entropy(const vb_cross_entropy_args* p, void* ws, 
   size_t need = 0;
   TRY(vb_cross_entropy_workspace(p->rows, p->classes, p->dtype, &need));
   TRY(check_ws(fn, ws, ws_bytes, need));
+  const Named memory[] = {matrix("dlogits", p->dlogits, p->rows, p->classes, p->ld_d, p->dtype, true),
+                          block("loss", p->loss, 4, true), block("row_loss", p->row_loss, p->rows * 4, true),
+                          block("the workspace", ws, (int64_t)need, true),
+                          matrix("logits", p->logits, p->rows, p->classes, p->ld, p->dtype, false),
+                          block("labels", p->labels, p->rows * 8, false)};
+  TRY(check_overlaps(fn, memory, 0, 4));
   HIPCHK(launch_cross_entropy(*p, ws, (hipStream_t)stream));
   return VB_OK;
 }
@@ -307,6 +363,41 @@ struct ClipCall {
   void* ws;
   hipStream_t st;
 };
+
+// As check_overlaps, of any number of tensors: their spans in the order of memory.  An
+// output that is its own gradient is one span.
+vb_status check_clip_overlaps(const char* fn, const ClipCall& c, size_t ws_bytes) {
+  struct Item {
+    uintptr_t at, end;
+    bool written;
+  };
+  constexpr int FEW = 64;
+  Item few[2 * FEW + 2], *item = few;
+  if (c.n_tensors > FEW && !(item = new (std::nothrow) Item[2 * (size_t)c.n_tensors + 2]))
+    return fail(VB_ENOMEM, "%s: no host memory for %d tensors", fn, c.n_tensors);
+  size_t n = 0;
+  auto add = [&](const void* p, size_t bytes, bool written) {
+    if (bytes) item[n++] = {(uintptr_t)p, (uintptr_t)p + bytes, written};
+  };
+  add(c.norm, 4, true);
+  add(c.ws, ws_bytes, true);
+  for (int32_t i = 0; i < c.n_tensors; ++i) {
+    const size_t bytes = (size_t)c.sizes[i] * elem_size(c.dtypes[i]);
+    const bool apart = c.out && c.out[i] != c.grads[i];
+    add(c.grads[i], bytes, !apart);
+    if (apart) add(c.out[i], bytes, true);
+  }
+  std::sort(item, item + n, [](const Item& a, const Item& b) { return a.at < b.at; });
+  uintptr_t end = 0, written_end = 0;  // of what starts before
+  bool clash = false;
+  for (size_t i = 0; i < n; ++i) {
+    clash |= item[i].at < (item[i].written ? end : written_end);
+    end = std::max(end, item[i].end);
+    if (item[i].written) written_end = std::max(written_end, item[i].end);
+  }
+  if (item != few) delete[] item;
+  return clash ? fail(VB_EINVAL, "%s: a tensor that is written overlaps another one", fn) : VB_OK;
+}
 
 template <int N>
 vb_status run_clip(const ClipCall& c) {
@@ -385,5 +476,6 @@ extern "C" vb_status vb_clip_grad_norm(int32_t n_tensors, const void* const* gra
   }
   TRY(check_ws(fn, ws, ws_bytes, need));
   const ClipCall c{n_tensors, grads, out, sizes, dtypes, max_norm, norm, ws, (hipStream_t)stream};
+  TRY(check_clip_overlaps(fn, c, need));
   return n_tensors <= CLIP_FEW_TENSORS ? run_clip<CLIP_FEW_TENSORS>(c) : run_clip<CLIP_TENSORS>(c);
 }

@@ -15,6 +15,36 @@ vb_status set_error(vb_status s, const char* msg) noexcept;
 
 inline size_t elem_size(int dtype) { return dtype == VB_F32 ? 4 : 2; }
 
+// The bytes of a matrix: rows of `bytes`, `ld` bytes apart (no less than `bytes`).
+struct Span {
+  uintptr_t at;
+  int64_t rows, bytes, ld;
+};
+inline bool is_empty(const Span& s) { return !s.at || s.rows <= 0 || s.bytes <= 0; }
+
+// Do two matrices share a byte?  Rows may lie between each other's.
+inline bool overlap(Span a, Span b) {
+  if (is_empty(a) || is_empty(b)) return false;
+  const int64_t d = (int64_t)(a.at - b.at);  // a's start, seen from b's
+  if (d >= (b.rows - 1) * b.ld + b.bytes || -d >= (a.rows - 1) * a.ld + a.bytes) return false;
+  // the first row of b, counted on before and past its ends, that ends after byte s
+  auto row_after = [&](int64_t s) {
+    const int64_t q = s - b.bytes;
+    return (q >= 0 ? q / b.ld : -((-q + b.ld - 1) / b.ld)) + 1;
+  };
+  if (a.ld == b.ld) {  // row r of a lies to row r + j of b as row 0 to row j, whatever r
+    for (int64_t j = row_after(d), end = j + 2; j < end; ++j)
+      if (j * b.ld < d + a.bytes && -j < a.rows && j < b.rows) return true;
+    return false;
+  }
+  if (a.rows > b.rows) return overlap(b, a);
+  for (int64_t r = 0; r < a.rows; ++r) {
+    const int64_t s = d + r * a.ld, first = row_after(s), j = first < 0 ? 0 : first;
+    if (j < b.rows && j * b.ld < s + a.bytes) return true;
+  }
+  return false;
+}
+
 // Grid of `blocks` workgroups, at most 2^31: a dimension of a launch holds less than 2^32
 // work-items, so from GRID_X workgroups of up to 1024 threads on they go on in z (y is the
 // kernel's).  Kernels number them by workgroup_number, and those past the last have no work.
