@@ -5,6 +5,8 @@ gradient, and the clipping of gradients to a global norm (include/vb_train.h).
 Thin ctypes binding, like the rest of the package: every step runs in the
 library's HIP kernels on the current stream; results are new tensors on it.
 Matrices may have any row stride; elements of a row are contiguous.
+No autograd graph is recorded: the gradients are calls of their own, and a tensor that
+requires grad is refused unless torch.no_grad() says that its graph is not wanted.
 """
 from __future__ import annotations
 
@@ -124,6 +126,13 @@ def _vector(name: str, t: torch.Tensor, n: int, like: torch.Tensor) -> None:
         raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
 
 
+def _no_graph(*tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("a tensor requires grad, and no autograd graph is recorded here: call under "
+                             "torch.no_grad() (or with detached tensors), and linear_backward or cross_entropy for gradients")
+
+
 def _act(act: str) -> int:
     code = ACTS.get(act)
     if code is None:
@@ -172,6 +181,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
         raise ValueError("x and weight must be matrices")
     rows, n_in = x.shape
     n_out = weight.shape[0]
+    _no_graph(x, weight, bias, residual, out)
     ld_x = _matrix("x", x, rows, n_in, x)
     ld_w = _matrix("weight", weight, n_out, n_in, x)
     if bias is not None:
@@ -208,6 +218,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act
     code = _act(act)
     if (saved is None) != (code == 0):
         raise ValueError("saved is the forward pass's y (relu) or pre (gelu, silu), and None without an activation")
+    _no_graph(dy, x, weight, saved)
     ld_dy = _matrix("dy", dy, rows, n_out, x)
     ld_x = _matrix("x", x, rows, n_in, x)
     ld_w = _matrix("weight", weight, n_out, n_in, x)
@@ -244,6 +255,7 @@ def cross_entropy(logits: torch.Tensor, labels: torch.Tensor, ignore_index: int 
     dt = _dtype(logits)
     if logits.dim() != 2:
         raise ValueError("logits must be a matrix")
+    _no_graph(logits, dlogits)
     rows, classes = logits.shape
     ld = _matrix("logits", logits, rows, classes, logits)
     if labels.dtype is not torch.int64 or labels.shape != (rows,) or labels.get_device() != dev \
@@ -277,6 +289,8 @@ def _tensor_list(name: str, tensors: Sequence[torch.Tensor], dev: int):
     for t in tensors:
         if t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous, on one device")
+        if t.requires_grad:
+            _no_graph(t)
     try:
         types = array("i", [DTYPES[t.dtype] for t in tensors])
     except KeyError:
