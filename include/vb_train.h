@@ -67,8 +67,8 @@ typedef struct {
  *   dx = g W, dweight = g^T x, dbias = column sums of g, dresidual = g.
  * saved: NULL for VB_ACT_NONE; y for VB_ACT_RELU (act' = 1 where y > 0, 0
  * elsewhere: where saved is not > 0, g is 0 whatever dy holds); pre for GELU
- * and SILU.  dx, dweight, dbias and dresidual may each be NULL.  With rows = 0
- * dweight and dbias are set to zero.  dresidual may be dy itself (same pointer
+ * and SILU.  dx, dweight, dbias and dresidual may each be NULL, with rows > 0 not
+ * all of them.  With rows = 0 dweight and dbias are set to zero.  dresidual may be dy itself (same pointer
  * and ld).
  * The matrix cores take operands of dtype.  With GELU and SILU in a 16-bit type g
  * is no number of that type: it enters both products as the sum of two (relative

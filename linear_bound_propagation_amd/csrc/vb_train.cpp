@@ -248,7 +248,8 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
   TRY(check_matrix(fn, "dweight", p->dweight, p->ld_dw, p->n_in, p->dtype, false));
   TRY(check_matrix(fn, "dbias", p->dbias, p->n_out, p->n_out, p->dtype, false));
   TRY(check_matrix(fn, "dresidual", p->dresidual, p->ld_dres, p->n_out, p->dtype, false));
-  if (!p->dx && !p->dweight && !p->dbias && !p->dresidual) return fail(VB_EINVAL, "%s: nothing to compute", fn);
+  // without rows dx and dresidual are empty, and may be NULL for that
+  if (some && !p->dx && !p->dweight && !p->dbias && !p->dresidual) return fail(VB_EINVAL, "%s: nothing to compute", fn);
   if (p->dresidual == p->dy && p->dy && p->ld_dres != p->ld_dy)
     return fail(VB_ESHAPE, "%s: dresidual over dy needs the same leading dimension", fn);
   const hipStream_t st = (hipStream_t)stream;
