@@ -107,9 +107,11 @@ vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t ws_bytes, 
  * A row with t == ignore_index has row_loss 0 and gradient 0 and does not
  * count; with every row ignored (or rows = 0) loss is 0.  A label outside
  * [0, classes) that is not ignore_index makes its row's loss and gradient NaN
- * (and counts), so that it cannot pass unseen.  Logits of -inf (masked classes)
- * have p = 0 and gradient 0; a row with no finite logit gives NaN, as the
- * formula does. */
+ * (and counts), so that it cannot pass unseen.  A logit of -inf (a masked class)
+ * has p = 0: without smoothing its gradient is 0 and the row's loss does not feel
+ * it; with smoothing the formula holds as it stands, with a gradient of
+ * -e / classes * grad_scale / n and a row_loss of +inf.  A row with no finite
+ * logit gives NaN, as the formula does. */
 typedef struct {
   int64_t rows;                          /* >= 0                                   */
   int32_t classes;                       /* > 0                                    */

@@ -151,7 +151,8 @@ int pair_tile(const Product& dx, const Product& dw, int dtype);
 hipError_t launch_pair(const Product& dx, const Product& dw, int tile, const ColumnSums& s, int dtype, hipStream_t st);
 hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long long ld_bytes, hipStream_t st);
 
-// ws: one int64 (count of the rows that are not ignored)
+// ws: the count of the rows that are not ignored (int64, in 16 bytes), then the rows' losses
+// (float32) if the caller does not want them
 hipError_t launch_cross_entropy(const vb_cross_entropy_args& p, void* ws, hipStream_t st);
 
 // Gradient tensors in the kernels' argument block, cut into chunks of `chunk` elements:

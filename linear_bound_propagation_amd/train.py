@@ -153,7 +153,8 @@ def _scratch(ws: torch.Tensor, dev: int) -> Tuple[int, int]:
 
 def linear_workspace(x: torch.Tensor, weight: torch.Tensor, backward: bool = False) -> torch.Tensor:
     """A workspace for `linear` calls (or `linear_backward` calls, with any activation, all
-    gradients and either round_g) on tensors of these sizes and strides, to keep between calls."""
+    gradients and either round_g) on tensors of these sizes, strides and alignment, to keep between
+    calls (rows that start off 16-byte boundaries take more than others)."""
     _device(x)
     rows, n_in = x.shape
     n_out = weight.shape[0]

@@ -57,3 +57,29 @@ def test_row_losses(lbp, classes, dtype):
             mean = z.double().cpu().mean(1)
             assert (((expected(z, y, eps, with_mean=False)[0] - want).abs() > bound) | (mean.abs() < 1)).all()
             assert (eps * 0.01 * mean.abs() > bound)[mean.abs() > 4].all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("classes", [10, 1001, 40004, 131074])
+def test_masked_classes(lbp, classes, dtype):
+    """Logits of -inf: without smoothing as if they were not there, with it by the formula."""
+    eps, scale = 0.25, 8.0
+    z, y = make(4, classes, dtype, 1.0, seed=5)
+    z[:, ::3] = float("-inf")
+    y = torch.full_like(y, 1)
+    kept = torch.ones(classes, dtype=torch.bool, device="cuda")
+    kept[::3] = False
+    print(f"masked {classes} {dtype}", flush=True)
+    loss, row, grad = lbp.cross_entropy(z, y, grad_scale=scale)
+    assert (grad[:, ~kept] == 0).all() and torch.isfinite(row).all()
+    want, bound = expected(z[:, kept], torch.zeros_like(y), 0.0)        # class 1 comes first of those kept
+    ref.assert_within(row, want, bound, "row_loss without the masked classes")
+    loss, row, grad = lbp.cross_entropy(z, y, label_smoothing=eps, grad_scale=scale)
+    assert (row == float("inf")).all() and loss == float("inf")
+    p = torch.softmax(z.double(), 1)
+    d = p - eps / classes
+    d[:, 1] -= 1 - eps
+    d *= scale / 4
+    e = scale / 4 * (2 * (ref.ACT[dtype] + (max(128, classes // 1024 + 1) + 26) * ref.U32) * p + 4 * ref.U32 * (p + 1 / classes)) \
+        + 4 * ref.U32 * d.abs()
+    ref.assert_within(grad, d, e + ref.UNIT[dtype] * (d.abs() + e) + ref.TINY[dtype], "smoothed gradient")
