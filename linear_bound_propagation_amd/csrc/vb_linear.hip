@@ -932,8 +932,9 @@ __global__ __launch_bounds__(256) void pack_kernel(PackJobs jobs) {
 // g = dy act'(saved), its copies and its column sums.  A thread has one chunk of columns
 // and every eighth of the workgroup's rows (16-byte accesses at any alignment); the
 // workgroup's 32 chunks of columns are summed over its rows in LDS, one float32 per
-// column and workgroup.  HBM bounds it (4096 x 8192 in bf16, GELU: 40 us, 201 MB at 5.0
-// TB/s).  Workgroups have 64 rows, or as few as 8 while there would be less than two
+// column and workgroup.  HBM bounds it (4096 x 8192 in bf16, GELU: 51 us with both parts of
+// g, 268 MB at 5.3 TB/s, 37 us with one, 201 MB at 5.5; its vector instructions alone are
+// about 34 and 26 us).  Workgroups have 64 rows, or as few as 8 while there would be less than two
 // workgroups a CU (1037 x 999 in float16: 13 us with 64 rows, 5.5 so).
 int sum_rows(long long rows, int n, int chunk) {
   const long long across = (n + 32 * chunk - 1) / (32 * chunk);
@@ -1089,14 +1090,15 @@ hipError_t launch_pair_typed(Product dx, Product dw, int tile, const ColumnSums&
 }  // namespace
 
 // Tile and split of a large product by the time they would take on the CU with the most
-// tiles: 64-byte steps of `share` microseconds (64-wide tiles, three to a CU at a time, take
-// `latency` where one has its CU to itself), the `fixed` part of each tile, mostly its
-// outputs, and a launch.  Measured, in us at 1024 x 1024 x 1024 | 2048 x 4096 x 4096 | 4096 x
-// 4096 x 4096 | 4096 x 4096 x 32: bf16 tiles of 64 6.9 | 111 | 197 | 15.6, 128 10.0 | 85 | 140
-// | 15.6, 256 x 128 14 | 61 | 122 | 12.6, 256 24 | 92 | 113 | 13.2; float32 tiles of 64 21 | 479
-// | 966 | 24, 128 62 | 475 | 948 | 25, 256 x 128 118 | 465 | 938 | 25.  A split costs the writing
-// and reading of its float32 parts, at 6 TB/s as they are in the caches, and another launch;
-// it has to gain 8 %, as it also keeps a backward pass from one launch for both products.
+// tiles: 64-byte steps, those of both passes, of `share` microseconds (64-wide tiles,
+// three to a CU at a time, take `latency` where one has its CU to itself), the `fixed`
+// part of each tile, mostly its outputs, and a launch.  Measured, in us at 1024 x 1024 x
+// 1024 | 2048 x 4096 x 4096 | 4096 x 4096 x 4096 | 4096 x 4096 x 32: bf16 tiles of 64 6.9
+// | 111 | 197 | 15.6, 128 10.0 | 85 | 140 | 15.6, 256 x 128 14 | 61 | 122 | 12.6, 256 24
+// | 92 | 113 | 13.2; float32 tiles of 64 21 | 479 | 966 | 24, 128 62 | 475 | 948 | 25,
+// 256 x 128 118 | 465 | 938 | 25.  A split costs the writing and reading of its float32
+// parts, at 6 TB/s as they are in the caches, and another launch; it has to gain 8 %, as
+// it also keeps a backward pass from one launch for both products.
 namespace {
 
 struct Kind {
