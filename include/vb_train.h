@@ -1,8 +1,9 @@
 /* vb_train.h -- C ABI of the training and evaluation operators in libvbprop.so.
  *
  * The networks whose bounds vb.h computes are evaluated and trained with these
- * calls: the fused linear layer and its backward pass, the softmax cross
- * entropy with its gradient, and the clipping of gradients to a global norm.
+ * calls: the fused linear layer and its backward pass, the gated linear layer,
+ * layer norm and dropout with theirs, the softmax cross entropy with its gradient,
+ * and the clipping of gradients to a global norm.
  *
  * Conventions (those of vb.h, where they apply):
  *  - Tensor pointers are DEVICE pointers owned by the caller; nothing is kept
@@ -98,6 +99,117 @@ vb_status vb_linear_forward_workspace(const vb_linear_fwd* p, size_t* bytes);
 vb_status vb_linear_backward_workspace(const vb_linear_bwd* p, size_t* bytes);
 vb_status vb_linear_forward(const vb_linear_fwd* p, void* ws, size_t ws_bytes, void* stream);
 vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t ws_bytes, void* stream);
+
+/* The gated linear layer: (gate | up) = x W^T + bias, y = act(gate) * up, both projections,
+ * the activation and the product in one pass.  weight holds the gate's rows, then up's. */
+typedef struct {
+  int64_t rows;                          /* >= 0 (0: nothing is enqueued)          */
+  int32_t n_in, n_out;                   /* in [1, 2^20], n_out in [1, 2^19]       */
+  int32_t dtype, act;                    /* VB_ACT_NONE: the plain product         */
+  const void* x;        int64_t ld_x;    /* [rows][n_in]                           */
+  const void* weight;   int64_t ld_w;    /* [2 n_out][n_in]                        */
+  const void* bias;                      /* [2 n_out] or NULL                      */
+  void* y;              int64_t ld_y;    /* [rows][n_out]                          */
+  void* pre;            int64_t ld_pre;  /* [rows][2 n_out] or NULL: gate and up,  */
+                                         /* rounded to dtype, for the backward pass*/
+} vb_gated_linear_fwd;
+
+/* Its backward pass for the gradient dy of y, with g = (dy * up * act'(gate) | dy * act(gate)):
+ *   dx = g W, dweight = g^T x, dbias = column sums of g,
+ * each optional (with rows > 0 not all of them NULL; with rows = 0 dweight and dbias are set to
+ * zero).  Where the gate of a ReLU is not > 0, its part of g is 0 whatever dy and up hold.  In
+ * 16-bit types g is no number of the type, whatever the activation: it enters the products in
+ * two parts or, with round_g, rounded to one, as in vb_linear_bwd (in float16 a g beyond 131008,
+ * or 65504 with round_g, is infinite there).  dbias sums the unrounded g. */
+typedef struct {
+  int64_t rows;
+  int32_t n_in, n_out;
+  int32_t dtype, act;
+  const void* dy;       int64_t ld_dy;   /* [rows][n_out]           */
+  const void* x;        int64_t ld_x;    /* [rows][n_in]            */
+  const void* weight;   int64_t ld_w;    /* [2 n_out][n_in]         */
+  const void* pre;      int64_t ld_pre;  /* [rows][2 n_out]         */
+  void* dx;             int64_t ld_dx;   /* [rows][n_in] or NULL    */
+  void* dweight;        int64_t ld_dw;   /* [2 n_out][n_in] or NULL */
+  void* dbias;                           /* [2 n_out] or NULL       */
+  int32_t round_g;                       /* 0 or 1                  */
+} vb_gated_linear_bwd;
+
+/* As the workspaces of the linear layer. */
+vb_status vb_gated_linear_forward_workspace(const vb_gated_linear_fwd* p, size_t* bytes);
+vb_status vb_gated_linear_backward_workspace(const vb_gated_linear_bwd* p, size_t* bytes);
+vb_status vb_gated_linear_forward(const vb_gated_linear_fwd* p, void* ws, size_t ws_bytes, void* stream);
+vb_status vb_gated_linear_backward(const vb_gated_linear_bwd* p, void* ws, size_t ws_bytes, void* stream);
+
+/* Layer norm of each row: mean = sum x / n, rstd = 1 / sqrt(sum (x - mean)^2 / n + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ * The variance comes from differences, so that rows far off zero keep it.  (Rows that spread over
+ * more than 1e19 overflow the float32 squares.)  A row with an infinity or NaN is NaN, as is a
+ * row of equal numbers with eps = 0. */
+typedef struct {
+  int64_t rows;                          /* >= 0 (0: nothing is enqueued)          */
+  int32_t n;                             /* in [1, 2^20]                           */
+  int32_t dtype;
+  const void* x;        int64_t ld_x;    /* [rows][n]                              */
+  const void* weight;                    /* [n] or NULL: ones                      */
+  const void* bias;                      /* [n] or NULL: zeros                     */
+  float eps;                             /* >= 0, finite                           */
+  void* y;              int64_t ld_y;    /* [rows][n]; may be x itself (the same   */
+                                         /* pointer and ld)                        */
+  float* mean;                           /* [rows] or NULL                         */
+  float* rstd;                           /* [rows] or NULL                         */
+} vb_layer_norm_fwd;
+
+/* Its backward pass for the gradient dy of y, with xh = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - sum g / n - xh * sum(g xh) / n) + dresidual,
+ *   dweight = column sums of dy * xh, dbias = column sums of dy,
+ * each optional (with rows > 0 not all of them NULL; with rows = 0 dweight and dbias are set to
+ * zero).  dresidual is the gradient that reaches x past the norm, of a skip connection. */
+typedef struct {
+  int64_t rows;
+  int32_t n;
+  int32_t dtype;
+  const void* dy;       int64_t ld_dy;   /* [rows][n]               */
+  const void* x;        int64_t ld_x;    /* [rows][n]               */
+  const float* mean;                     /* [rows]                  */
+  const float* rstd;                     /* [rows]                  */
+  const void* weight;                    /* [n] or NULL: ones       */
+  const void* dresidual; int64_t ld_dres;/* [rows][n] or NULL       */
+  void* dx;             int64_t ld_dx;   /* [rows][n] or NULL; may be dy or dresidual itself */
+                                         /* (the same pointer and ld)                        */
+  void* dweight;                         /* [n] or NULL             */
+  void* dbias;                           /* [n] or NULL             */
+} vb_layer_norm_bwd;
+
+/* Workspace of the backward pass; the forward pass needs none. */
+vb_status vb_layer_norm_backward_workspace(int64_t rows, int32_t n, int32_t dtype, size_t* bytes);
+vb_status vb_layer_norm_forward(const vb_layer_norm_fwd* p, void* stream);
+vb_status vb_layer_norm_backward(const vb_layer_norm_bwd* p, void* ws, size_t ws_bytes, void* stream);
+
+/* Dropout, with a mask that a counter-based generator gives and that is never stored:
+ *   y = (kept ? x / (1 - p) : 0) + residual.
+ * Element (r, c) has word c % 4 of Philox4x32 with 7 rounds (Salmon, Moraes, Dror and Shaw, 2011:
+ * the fewest that pass their statistical tests), whose key is seed and whose counter is
+ * r * ceil(n / 4) + c / 4 in its lower 64 bits, offset in its upper ones; it is kept if the word
+ * is at least round(p 2^32), and 1 - p is what that leaves.  The mask depends on nothing else, not
+ * on type or strides: the backward pass is the same call on the gradient, without the residual.
+ * Another offset is another mask.  step, a number on the device, is added to offset (modulo 2^64),
+ * so that replays of a captured call can differ: the caller counts it up.
+ * A dropped element is 0, whatever x holds there; p = 1 drops all, p = 0 none. */
+typedef struct {
+  int64_t rows;                          /* >= 0 (0: nothing is enqueued)          */
+  int32_t n;                             /* in [1, 2^30]                           */
+  int32_t dtype;
+  const void* x;        int64_t ld_x;    /* [rows][n]                              */
+  const void* residual; int64_t ld_res;  /* [rows][n] or NULL                      */
+  double p;                              /* in [0, 1]                              */
+  uint64_t seed, offset;
+  const uint64_t* step;                  /* [1] or NULL                            */
+  void* y;              int64_t ld_y;    /* [rows][n]; may be x or residual itself */
+                                         /* (the same pointer and ld)              */
+} vb_dropout_args;
+
+vb_status vb_dropout(const vb_dropout_args* p, void* stream);
 
 /* Softmax cross entropy of integer labels, and its gradient in the same call.
  * Row r with label t = labels[r] (p = softmax of the row, e = label_smoothing):

@@ -21,7 +21,8 @@ import torch
 
 from . import train as _train
 from .train import (clip_grad_norm, clip_grad_norm_workspace, cross_entropy, cross_entropy_workspace,  # noqa: F401
-                    linear, linear_backward, linear_workspace)
+                    dropout, gated_linear, gated_linear_backward, gated_linear_workspace, layer_norm,
+                    layer_norm_backward, layer_norm_workspace, linear, linear_backward, linear_workspace)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvbprop.so")

@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libvbprop.so")
 PROBE_LIB = os.path.join(HERE, "libvbprobe.so")
 
 SOURCES = ["vb_gemm.hip", "vb_ibp_narrow.hip", "vb_kernels.hip", "vb_scratch.hip", "vb_linear.hip", "vb_loss.hip",
-           "vb_clip.hip", "vb_api.cpp", "vb_train.cpp"]
+           "vb_clip.hip", "vb_norm.hip", "vb_dropout.hip", "vb_api.cpp", "vb_train.cpp", "vb_block.cpp"]
 PROBE_SOURCES = ["vb_probe.hip"]
 
 HIPCC_FLAGS = [

@@ -1,7 +1,8 @@
-// The fused linear layer y = act(x W^T + bias + residual) and the products of
-// its backward pass.
+// The fused linear layer y = act(x W^T + bias + residual), the gated one y = act(gate) * up
+// with (gate | up) = x W^T + bias, and the products of their backward passes.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "vb_train_device.h"
 #include "vb_train_internal.h"
@@ -198,6 +199,33 @@ __device__ __forceinline__ void finish(const Product& p, long long m, int n, con
   put((T*)p.out + m * p.ld_out + n);
 }
 
+// The same for the gated layer: VEC outputs of row m from n on, from their gates and ups.
+template <typename T, int VEC>
+__device__ __forceinline__ void finish_gated(const Product& p, long long m, int n, const float* gate, const float* up) {
+  typedef T TV __attribute__((ext_vector_type(VEC)));
+  typedef TV LV __attribute__((aligned(sizeof(T))));
+  float g[VEC], u[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) g[i] = gate[i], u[i] = up[i];
+  auto add = [&](const T* q, float* x) {
+    const TV t = *(const LV*)q;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] += to_f32((T)t[i]);
+  };
+  auto put = [&](T* q, const float* x) {
+    TV t;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) t[i] = from_f32<T>(x[i]);
+    *(LV*)q = t;
+  };
+  if (p.bias) add((const T*)p.bias + n, g), add((const T*)p.bias + p.N + n, u);
+  if (p.pre) put((T*)p.pre + m * p.ld_pre + n, g), put((T*)p.pre + m * p.ld_pre + p.N + n, u);
+  activate<T, VEC>(g, p.act);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) g[i] *= u[i];
+  put((T*)p.out + m * p.ld_out + n, g);
+}
+
 // Tile of a workgroup: workgroups go round the eight XCDs in turn, so each XCD takes
 // a contiguous run of tiles, walked in bands of eight tile rows; the 32 tiles that an
 // XCD has at a time then share 8 row and 4 column panels through its L2.
@@ -333,20 +361,24 @@ struct Ring {
 
 // Workgroup number `block` of those that the tiles take, part `split` of the reduction.  TWO: A
 // in two parts (an instance of its own: its registers and branches would cost the others 4 %).
-template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB, bool TWO>
+// GATED: B's stage holds BN / 2 of the gate's rows, then the same ones of up, and a wavefront's
+// column blocks are gate and up in turn, so that its tile has both of TN / 2 outputs.
+template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB, bool TWO, bool GATED = false>
 __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned block, unsigned split, char* lds) {
   typedef typename Chunk<T>::type C;
   constexpr int DEPTH = Ring<BM, BN, XA, XB>::DEPTH, NS = Ring<BM, BN, XA, XB>::NS;
   constexpr int NW = WM * WN, STAGE = (BM + BN) * DEPTH, KS = DEPTH / sizeof(T);
   constexpr int TM = BM / WM, TN = BN / WN, MT = TM / 16, NT = TN / 16, MH = MT / 2;
   typedef Operand<T, BM, NW, XA, DEPTH> OA;
-  typedef Operand<T, BN, NW, XB, DEPTH> OB;
-  constexpr int LA = OA::L, LB = OB::L, RA = OA::READS, RB = OB::READS;
+  constexpr int BO = GATED ? BN / 2 : BN, TO = GATED ? TN / 2 : TN;  // outputs of a tile's, a wavefront's row
+  static_assert(!GATED || (!XA && !XB && !TWO && NT % 2 == 0), "gated: the forward product");
+  typedef Operand<T, BO, NW, XB, DEPTH> OB;
+  constexpr int LA = OA::L, LB = OB::L * (GATED ? 2 : 1), RA = OA::READS, RB = OB::READS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int ti, tj;
   tile_of(block, tm, tn, ti, tj);
   const long long m0 = (long long)ti * BM;
-  const int n0 = tj * BN;
+  const int n0 = tj * BO;
   // this workgroup's part of the reduction
   const int first = split * (p.split_steps / (DEPTH / 64));
   const int K = (int)min(p.K - (long long)first * KS, (long long)p.split_steps * (64 / (int)sizeof(T)));
@@ -355,9 +387,18 @@ __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned bl
   OB b;
   a.init(p.a, p.lda, m0, p.M, first, wave, lane);
   b.init(p.b, p.ldb, n0, p.N, first, wave, lane);
+  // up's rows lie as the gate's do
+  OB up = b;
+  if constexpr (GATED) up.base += p.N * p.ldb * (long long)sizeof(T);
   const unsigned lds0 = lds_address(lds);
-  auto issue = [&](int t, int base) { a.load(t, lds0 + base), b.load(t, lds0 + base + BM * DEPTH); };
-  auto issue_part = [&](int t, int base) { a.load_part(t, lds0 + base, K), b.load_part(t, lds0 + base + BM * DEPTH, K); };
+  auto issue = [&](int t, int base) {
+    a.load(t, lds0 + base), b.load(t, lds0 + base + BM * DEPTH);
+    if constexpr (GATED) up.load(t, lds0 + base + (BM + BO) * DEPTH);
+  };
+  auto issue_part = [&](int t, int base) {
+    a.load_part(t, lds0 + base, K), b.load_part(t, lds0 + base + BM * DEPTH, K);
+    if constexpr (GATED) up.load_part(t, lds0 + base + (BM + BO) * DEPTH, K);
+  };
   // The next stage has landed (all but the loads of the NS - 2 stages after it), this
   // wavefront has its reads of the last stage, and so have the others.
   auto join = [] {
@@ -370,7 +411,8 @@ __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned bl
 #pragma unroll
   for (int i = 0; i < MT; ++i) pa[i] = a.place(wm * MT + i);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) pb[j] = BM * DEPTH + b.place(wn * NT + j);
+  for (int j = 0; j < NT; ++j)
+    pb[j] = GATED ? (BM + j % 2 * BO) * DEPTH + b.place((wn * NT + j) / 2) : BM * DEPTH + b.place(wn * NT + j);
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -489,7 +531,8 @@ __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned bl
   if (TWO) each([](float v) { return 2.f * v; });
   // Outputs leave through LDS, 32 rows of the wavefront's tile at a time in its own
   // part of it, so that a row's outputs are written as whole 128-byte pieces.
-  constexpr int LDE = TN + 4, VEC = 16 / sizeof(T), LPR = TN / VEC, RPI = 64 / LPR;
+  // GATED: the gates in the first half of a row, then the ups.
+  constexpr int LDE = TN + 4, VEC = 16 / sizeof(T), LPR = TO / VEC, RPI = 64 / LPR;
   static_assert(NW * 32 * LDE * 4 <= NS * STAGE, "the output staging fits the operand stages");
   float* e = (float*)lds + wave * 32 * LDE;
 #pragma unroll
@@ -499,26 +542,32 @@ __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned bl
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) e[(16 * h + 4 * quarter + q) * LDE + j * 16 + r16] = acc[i + h][j][q];
+        for (int q = 0; q < 4; ++q) e[(16 * h + 4 * quarter + q) * LDE + (GATED ? j % 2 * TO + j / 2 * 16 : j * 16) + r16] = acc[i + h][j][q];
     __builtin_amdgcn_wave_barrier();
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const long long mb = m0 + wm * TM + i * 16;
-    const int nb = n0 + wn * TN;
+    const int nb = n0 + wn * TO;
     if (p.partial) {
-      // float32 sums of this part, rows of N rounded up to four
+      // float32 sums of this part, rows of N rounded up to four (GATED: the gates', then the ups')
       float* part = p.partial + (split * p.M + mb) * (long long)p.ld_partial + nb;
-      const int row = lane / (TN / 4), col = lane % (TN / 4) * 4;
+      const int row = lane / (TN / 4), col = lane % (TN / 4) * 4, of = col % TO, to = col == of ? of : of + p.ld_partial / 2;
 #pragma unroll
       for (int r = 0; r < 32; r += 256 / TN)
-        if (mb + r + row < p.M && nb + col < p.N)
-          *(f32x4*)(part + (r + row) * (long long)p.ld_partial + col) = *(const f32x4*)(e + (r + row) * LDE + col);
+        if (mb + r + row < p.M && nb + of < p.N)
+          *(f32x4*)(part + (r + row) * (long long)p.ld_partial + to) = *(const f32x4*)(e + (r + row) * LDE + col);
     } else {
       const int row = lane / LPR, col = (lane % LPR) * VEC;
 #pragma unroll
       for (int r = 0; r < 32; r += RPI) {
         const float* v = e + (r + row) * LDE + col;
         if (mb + r + row < p.M && nb + col < p.N) {
-          if (nb + col + VEC <= p.N) {
+          if constexpr (GATED) {
+            if (nb + col + VEC <= p.N) {
+              finish_gated<T, VEC>(p, mb + r + row, nb + col, v, v + TO);
+            } else {
+              for (int k = 0; nb + col + k < p.N; ++k) finish_gated<T, 1>(p, mb + r + row, nb + col + k, v + k, v + TO + k);
+            }
+          } else if (nb + col + VEC <= p.N) {
             finish<T, VEC>(p, mb + r + row, nb + col, v);
           } else {
             for (int k = 0; nb + col + k < p.N; ++k) finish<T, 1>(p, mb + r + row, nb + col + k, v + k);
@@ -531,12 +580,12 @@ __device__ __forceinline__ void gemm_tile(Product p, int tm, int tn, unsigned bl
   }
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB, bool TWO>
+template <typename T, int BM, int BN, int WM, int WN, bool XA, bool XB, bool TWO, bool GATED = false>
 __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void gemm_kernel(Product p, int tm, int tn) {
   __shared__ __align__(16) char lds[Ring<BM, BN, XA, XB>::BYTES];
   const unsigned block = workgroup_number();
   if (block >= (unsigned)tm * tn) return;  // the whole workgroup
-  gemm_tile<T, BM, BN, WM, WN, XA, XB, TWO>(p, tm, tn, block, blockIdx.y, lds);
+  gemm_tile<T, BM, BN, WM, WN, XA, XB, TWO, GATED>(p, tm, tn, block, blockIdx.y, lds);
 }
 
 // dbias from the sums of act_grad_kernel's workgroups: 64 columns per workgroup, in 16 sums
@@ -636,17 +685,19 @@ __device__ __forceinline__ typename Chunk<T>::type load_loose(const T* p) {
 // of the reduction in turn (1 KB of a row per load, R loads and a chunk of each x row,
 // which stay in the L1 cache, per step); float32 multiply-adds on the vector units.  1 x
 // 4096 -> 16384 in bf16: 23.3 us, 134 MB at 5.8 TB/s, what reading them takes.
-template <typename T, int MR, int R>
+// GATED: half of the weight rows are the gate's, half the same ones of up.
+template <typename T, int MR, int R, bool GATED>
 __global__ __launch_bounds__(256) void rows_kernel(Product p) {
   typedef typename Chunk<T>::type C;
   constexpr int EC = 16 / sizeof(T);
   __shared__ float red[4][R * MR];
+  constexpr int RO = GATED ? R / 2 : R;  // outputs
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * R, chunks = (int)(p.K / EC), tail = (int)(p.K % EC);
+  const int n0 = blockIdx.x * RO, chunks = (int)(p.K / EC), tail = (int)(p.K % EC);
   const T* w[R];
   const T* x[MR];
 #pragma unroll
-  for (int r = 0; r < R; ++r) w[r] = (const T*)p.b + (long long)min(n0 + r, p.N - 1) * p.ldb;
+  for (int r = 0; r < R; ++r) w[r] = (const T*)p.b + (long long)(min(n0 + r % RO, p.N - 1) + r / RO * p.N) * p.ldb;
 #pragma unroll
   for (int m = 0; m < MR; ++m) x[m] = (const T*)p.a + min((long long)m, p.M - 1) * p.lda;
   float acc[R][MR];
@@ -683,10 +734,16 @@ __global__ __launch_bounds__(256) void rows_kernel(Product p) {
       if (lane == 0) red[wave][m * R + r] = s;
     }
   __syncthreads();
-  const int t = threadIdx.x, m = t / R, n = n0 + t % R;
-  if (t < R * MR && m < p.M && n < p.N) {
-    const float v = (red[0][t] + red[1][t]) + (red[2][t] + red[3][t]);
-    finish<T, 1>(p, m, n, &v);
+  const int t = threadIdx.x, m = t / RO, n = n0 + t % RO;
+  if (t < RO * MR && m < p.M && n < p.N) {
+    auto sum = [&](int i) { return (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]); };
+    if constexpr (GATED) {
+      const float gate = sum(m * R + t % RO), up = sum(m * R + RO + t % RO);
+      finish_gated<T, 1>(p, m, n, &gate, &up);
+    } else {
+      const float v = sum(t);
+      finish<T, 1>(p, m, n, &v);
+    }
   }
 }
 
@@ -703,18 +760,24 @@ __global__ __launch_bounds__(256) void rows_kernel(Product p) {
 // boundary, a workgroup takes rows of one distance, and its x chunks start as much
 // earlier.  (7 x 5001 -> 3999 in float16: 20.6 us with weight chunks from the rows' starts,
 // which cross a line every other time, 13.5 so.)
-template <typename T, int MB, int NB, int NW>
+// GATED: half of the weight rows are the gate's, half the same ones of up, whose chunks start
+// where the gate's do, on boundaries or not.
+template <typename T, int MB, int NB, int NW, bool GATED>
 __global__ __launch_bounds__(64 * NW) void narrow_kernel(Product p, int period) {
   typedef typename Chunk<T>::type C;
   constexpr int EC = 16 / sizeof(T), U = 2, OUT = MB * NB * 256;
   __shared__ __align__(16) float red[NW][OUT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, quarter = lane >> 4;
-  const int like = blockIdx.x % period, n0 = blockIdx.x / period * (16 * NB) * period + like;
+  constexpr int RO = GATED ? 8 * NB : 16 * NB;  // outputs
+  const int like = blockIdx.x % period, n0 = blockIdx.x / period * RO * period + like;
   if (like >= p.N) return;  // the whole workgroup
   const int last = p.N - 1 - (p.N - 1 - like) % period;
   const T* w[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) w[b] = (const T*)p.b + (long long)min(n0 + (16 * b + r16) * period, last) * p.ldb;
+  for (int b = 0; b < NB; ++b) {
+    const int row = 16 * b + r16;
+    w[b] = (const T*)p.b + (long long)(min(n0 + row % RO * period, last) + row / RO * p.N) * p.ldb;
+  }
   const int lead = __builtin_amdgcn_readfirstlane((int)((uintptr_t)w[0] % 16 / sizeof(T)));
   const T* x[MB];
 #pragma unroll
@@ -743,7 +806,8 @@ __global__ __launch_bounds__(64 * NW) void narrow_kernel(Product p, int period) 
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int u = 0; u < U; ++u) wv[u][b] = *(const C*)(w[b] + k0 + u * 4 * EC);
+      for (int u = 0; u < U; ++u)
+        wv[u][b] = GATED ? load_loose(w[b] + k0 + u * 4 * EC) : *(const C*)(w[b] + k0 + u * 4 * EC);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -778,89 +842,119 @@ __global__ __launch_bounds__(64 * NW) void narrow_kernel(Product p, int period) 
 #pragma unroll
     for (int m = 0; m < MB; ++m) *(f32x4*)&red[wave][(b * MB + m) * 256 + lane * 4] = acc[b][m];
   __syncthreads();
-  for (int o = threadIdx.x; o < OUT; o += 64 * NW) {
-    const int n = o % (16 * NB), m = o / (16 * NB);
-    const int at = ((n >> 4) * MB + (m >> 4)) * 256 + (((n >> 2) & 3) * 16 + (m & 15)) * 4 + (n & 3);
-    float v = 0.f;
+  for (int o = threadIdx.x; o < 16 * MB * RO; o += 64 * NW) {
+    const int n = o % RO, m = o / RO;
+    auto sum = [&](int row) {  // of the workgroup's weight rows
+      const int at = ((row >> 4) * MB + (m >> 4)) * 256 + (((row >> 2) & 3) * 16 + (m & 15)) * 4 + (row & 3);
+      float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < NW; ++k) v += red[k][at];
-    if (m < p.M && n0 + n * period < p.N) finish<T, 1>(p, m, n0 + n * period, &v);
+      for (int k = 0; k < NW; ++k) v += red[k][at];
+      return v;
+    };
+    const float v = sum(n), up = GATED ? sum(RO + n) : 0.f;
+    if (m >= p.M || n0 + n * period >= p.N) continue;
+    if constexpr (GATED) finish_gated<T, 1>(p, m, n0 + n * period, &v, &up);
+    else finish<T, 1>(p, m, n0 + n * period, &v);
   }
 }
 
-template <typename T, int MR>
+int weight_rows_of(const Product& p) { return p.gated ? 2 * p.N : p.N; }
+
+template <typename T, int MR, bool GATED>
 hipError_t launch_rows(const Product& p, hipStream_t st) {
   // four workgroups a CU before a workgroup takes more weight rows
-  if (p.N >= 4096) rows_kernel<T, MR, 4><<<(p.N + 3) / 4, 256, 0, st>>>(p);
-  else if (p.N >= 2048) rows_kernel<T, MR, 2><<<(p.N + 1) / 2, 256, 0, st>>>(p);
-  else rows_kernel<T, MR, 1><<<p.N, 256, 0, st>>>(p);
+  if constexpr (GATED) {
+    if (p.N >= 2048) rows_kernel<T, MR, 4, true><<<(p.N + 1) / 2, 256, 0, st>>>(p);
+    else rows_kernel<T, MR, 2, true><<<p.N, 256, 0, st>>>(p);
+  } else {
+    if (p.N >= 4096) rows_kernel<T, MR, 4, false><<<(p.N + 3) / 4, 256, 0, st>>>(p);
+    else if (p.N >= 2048) rows_kernel<T, MR, 2, false><<<(p.N + 1) / 2, 256, 0, st>>>(p);
+    else rows_kernel<T, MR, 1, false><<<p.N, 256, 0, st>>>(p);
+  }
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool GATED>
 hipError_t launch_narrow(const Product& p, hipStream_t st) {
+  const int weight_rows = weight_rows_of(p);
   // One or two rows on the vector units where a row occupies the workgroup (two rows of
   // 1024 16-bit numbers -> 8192: 8.2 us against 6.1), up to four where there are few
   // workgroups of the other kind (4 x 8192 -> 1000 in bf16: 8.0 against 14.4 us, 4 x 4096 ->
   // 4096: 12.9 against 10.2).
-  if (p.M <= 4 && (p.N <= 2048 || (p.M <= 2 && p.K * (long long)sizeof(T) >= 4096))) {
-    if (p.M == 1) return launch_rows<T, 1>(p, st);
-    if (p.M == 2) return launch_rows<T, 2>(p, st);
-    return launch_rows<T, 4>(p, st);
+  if (p.M <= 4 && (weight_rows <= 2048 || (p.M <= 2 && p.K * (long long)sizeof(T) >= 4096))) {
+    if (p.M == 1) return launch_rows<T, 1, GATED>(p, st);
+    if (p.M == 2) return launch_rows<T, 2, GATED>(p, st);
+    return launch_rows<T, 4, GATED>(p, st);
   }
   int period = 1;
   while (period < 16 / (int)sizeof(T) && p.ldb * sizeof(T) * period % 16) period *= 2;
-  auto blocks = [&](int rows) { return (unsigned)((p.N + rows * period - 1LL) / (rows * period) * period); };
+  auto blocks = [&](int rows) {
+    if (GATED) rows /= 2;
+    return (unsigned)((p.N + rows * period - 1LL) / (rows * period) * period);
+  };
   const bool many = blocks(64) >= 200;
   if (p.M <= 16) {
-    if (many) narrow_kernel<T, 1, 4, 4><<<blocks(64), 256, 0, st>>>(p, period);
-    else narrow_kernel<T, 1, 1, 16><<<blocks(16), 1024, 0, st>>>(p, period);
+    if (many) narrow_kernel<T, 1, 4, 4, GATED><<<blocks(64), 256, 0, st>>>(p, period);
+    else narrow_kernel<T, 1, 1, 16, GATED><<<blocks(16), 1024, 0, st>>>(p, period);
   } else {
-    if (many) narrow_kernel<T, 2, 4, 4><<<blocks(64), 256, 0, st>>>(p, period);
-    else narrow_kernel<T, 2, 1, 16><<<blocks(16), 1024, 0, st>>>(p, period);
+    if (many) narrow_kernel<T, 2, 4, 4, GATED><<<blocks(64), 256, 0, st>>>(p, period);
+    else narrow_kernel<T, 2, 1, 16, GATED><<<blocks(16), 1024, 0, st>>>(p, period);
   }
   return hipGetLastError();
 }
 
 // Adds the parts of a split reduction, in order, and finishes the outputs: four of a row
 // per thread.
-template <typename T>
+template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void join_kernel(Product p, int splits) {
-  const int quads = p.ld_partial / 4;
+  const int quads = p.ld_partial / (GATED ? 8 : 4);
   const long long i = (long long)workgroup_number() * 256 + threadIdx.x;
   const long long m = i / quads;
   const int n = (int)(i % quads) * 4;
   if (m >= p.M) return;
-  const float* q = p.partial + m * p.ld_partial + n;
   const long long step = p.M * p.ld_partial;
-  f32x4 v = *(const f32x4*)q;
-  int s = 1;
-  for (; s + 5 <= splits; s += 5) {  // five loads at a time
-    f32x4 part[5];
+  auto join = [&](const float* q, float* x) {
+    f32x4 v = *(const f32x4*)q;
+    int s = 1;
+    for (; s + 5 <= splits; s += 5) {  // five loads at a time
+      f32x4 part[5];
 #pragma unroll
-    for (int k = 0; k < 5; ++k) part[k] = *(const f32x4*)(q + (s + k) * step);
+      for (int k = 0; k < 5; ++k) part[k] = *(const f32x4*)(q + (s + k) * step);
 #pragma unroll
-    for (int k = 0; k < 5; ++k) v += part[k];
-  }
-  for (; s < splits; ++s) v += *(const f32x4*)(q + s * step);
-  const float x[4] = {v[0], v[1], v[2], v[3]};
+      for (int k = 0; k < 5; ++k) v += part[k];
+    }
+    for (; s < splits; ++s) v += *(const f32x4*)(q + s * step);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = v[k];
+  };
+  const float* q = p.partial + m * p.ld_partial + n;
+  float x[4], up[4];
+  join(q, x);
+  if constexpr (GATED) join(q + p.ld_partial / 2, up);
+  auto put = [&](auto vec, int k) {
+    if constexpr (GATED) finish_gated<T, vec.value>(p, m, n + k, x + k, up + k);
+    else finish<T, vec.value>(p, m, n + k, x + k);
+  };
   if (n + 4 <= p.N) {
-    finish<T, 4>(p, m, n, x);
+    put(std::integral_constant<int, 4>(), 0);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (n + k < p.N) finish<T, 1>(p, m, n + k, x + k);
+      if (n + k < p.N) put(std::integral_constant<int, 1>(), k);
   }
 }
 
 template <typename T, int BM, int BN, int WM, int WN>
 hipError_t launch_gemm(const Product& p, int splits, hipStream_t st) {
-  const long long tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
+  const int outputs = p.gated ? BN / 2 : BN;  // of a tile's row
+  const long long tm = (p.M + BM - 1) / BM, tn = (p.N + outputs - 1) / outputs;
   if (tm * tn > 0x7fffffffLL) return hipErrorInvalidValue;
   const dim3 grid = grid_of(tm * tn, splits);
   constexpr int threads = 64 * WM * WN;
   constexpr bool TWO = sizeof(T) == 2;
-  if (TWO && p.a_low) {
+  if (p.gated) {
+    gemm_kernel<T, BM, BN, WM, WN, false, false, false, true><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
+  } else if (TWO && p.a_low) {
     if (p.across_a) gemm_kernel<T, BM, BN, WM, WN, true, true, TWO><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
     else gemm_kernel<T, BM, BN, WM, WN, false, true, TWO><<<grid, threads, 0, st>>>(p, (int)tm, (int)tn);
   } else if (p.across_a) {
@@ -873,6 +967,9 @@ hipError_t launch_gemm(const Product& p, int splits, hipStream_t st) {
   return hipGetLastError();
 }
 
+// float32 numbers of a row of parts
+int partial_row(const Product& p) { return (p.N + 3) / 4 * (p.gated ? 8 : 4); }
+
 template <typename T>
 hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
   // in steps of 64 bytes, an even number of them to a part
@@ -880,7 +977,7 @@ hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
   p.split_steps = ((steps + t.splits - 1) / t.splits + 1) / 2 * 2;
   const int splits = (steps + p.split_steps - 1) / p.split_steps;
   if (splits == 1) p.partial = nullptr;
-  p.ld_partial = (p.N + 3) / 4 * 4;
+  p.ld_partial = partial_row(p);
   hipError_t e;
   if constexpr (sizeof(T) == 2) {
     if (t.bm == 256 && t.bn == 256) e = launch_gemm<T, 256, 256, 2, 4>(p, splits, st);
@@ -893,9 +990,10 @@ hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
     else e = launch_gemm<T, 64, 64, 2, 2>(p, splits, st);
   }
   if (e != hipSuccess || splits == 1) return e;
-  const long long quads = p.M * (p.ld_partial / 4), blocks = (quads + 255) / 256;
+  const long long quads = p.M * (p.ld_partial / (p.gated ? 8 : 4)), blocks = (quads + 255) / 256;
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-  join_kernel<T><<<grid_of(blocks), 256, 0, st>>>(p, splits);
+  if (p.gated) join_kernel<T, true><<<grid_of(blocks), 256, 0, st>>>(p, splits);
+  else join_kernel<T, false><<<grid_of(blocks), 256, 0, st>>>(p, splits);
   return hipGetLastError();
 }
 
@@ -1032,6 +1130,92 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p, PackJobs jobs)
   }
 }
 
+// g of the gated layer, its copies and its column sums: as act_grad_kernel, each chunk of dy
+// giving one of dgate and one of dup.
+template <typename T, int ACT>
+__global__ __launch_bounds__(256) void gate_grad_kernel(GateGrad p, PackJobs jobs) {
+  typedef typename Chunk<T>::type C;
+  typedef typename Loose<T>::type LC;
+  constexpr int EC = 16 / sizeof(T);
+  __shared__ float red[2][8][32 * EC + 1];
+  const unsigned block = workgroup_number();
+  if (block >= p.blocks) {  // the copies that the products need, by the same launch
+    pack_chunk<T>(jobs, block - p.blocks);
+    return;
+  }
+  const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const unsigned across = (p.n + 32 * EC - 1) / (32 * EC), bx = block % across, by = block / across;
+  const int n = (bx * 32 + c) * EC;
+  const long long m0 = (long long)by * p.part_rows;
+  float sum[2][EC];
+#pragma unroll
+  for (int e = 0; e < EC; ++e) sum[0][e] = sum[1][e] = 0.f;
+  const int have = p.n - n;  // columns from this chunk on
+  const int pad = (int)(p.ld_g - 2LL * p.n);
+  for (long long m = m0 + w; m < min(m0 + p.part_rows, p.rows) && have > 0; m += 8) {
+    const T* dy = (const T*)p.dy + m * p.ld_dy + n;
+    const T* pre = (const T*)p.pre + m * p.ld_pre + n;
+    C d, gate, up;
+    if (have >= EC) {
+      d = load_loose(dy), gate = load_loose(pre), up = load_loose(pre + p.n);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EC; ++e) {
+        d[e] = e < have ? dy[e] : (T)0.f;
+        gate[e] = e < have ? pre[e] : (T)0.f;
+        up[e] = e < have ? pre[p.n + e] : (T)0.f;
+      }
+    }
+    C high[2], low[2];
+#pragma unroll
+    for (int e = 0; e < EC; ++e) {
+      const float dv = to_f32((T)d[e]), gv = to_f32((T)gate[e]), uv = to_f32((T)up[e]);
+      const float x[2] = {act_grad<T>(dv * uv, gv, ACT), dv * act_value<T>(gv, ACT)};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        sum[k][e] += x[k];
+        T h = from_f32<T>(x[k]), l = (T)0.f;
+        if (sizeof(T) == 2 && p.g_low) split<T>(x[k], h, l);
+        high[k][e] = h, low[k][e] = l;
+      }
+    }
+    auto put = [&](void* g, const C* v) {
+      T* o = (T*)g + m * p.ld_g + n;
+      if (have >= EC) {
+        *(C*)o = v[0];
+        *(LC*)(o + p.n) = v[1];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < EC; ++e)
+            if (e < have) o[k * p.n + e] = v[k][e];
+      }
+      if (have <= EC)
+        for (int e = 0; e < pad; ++e) o[p.n + have + e] = (T)0.f;
+    };
+    if (p.g) put(p.g, high);
+    if (sizeof(T) == 2 && p.g_low) put(p.g_low, low);
+  }
+  if (!p.dbias) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < EC; ++e) red[k][w][c * EC + e] = sum[k][e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * EC; i += 256) {
+    const int k = i / (32 * EC), j = i % (32 * EC), col = bx * 32 * EC + j;
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s += red[k][q][j];
+    if (col < p.n) {
+      const long long at = (long long)k * p.n + col;
+      if (!p.partial) ((T*)p.dbias)[at] = from_f32<T>(s);
+      else p.partial[(long long)by * 2 * p.n + at] = s;
+    }
+  }
+}
+
 __global__ __launch_bounds__(256) void fill_zero_kernel(unsigned short* p, long long rows, long long n, long long ld) {
   const long long i = (long long)workgroup_number() * 256 + threadIdx.x;
   if (i < rows * n) p[i / n * ld + i % n] = 0;
@@ -1065,6 +1249,24 @@ hipError_t launch_act_grad_typed(ActGrad p, const PackJobs& jobs, unsigned copie
   else if (p.act == VB_ACT_RELU) act_grad_kernel<T, VB_ACT_RELU><<<grid, 256, 0, st>>>(p, jobs);
   else if (p.act == VB_ACT_GELU) act_grad_kernel<T, VB_ACT_GELU><<<grid, 256, 0, st>>>(p, jobs);
   else act_grad_kernel<T, VB_ACT_SILU><<<grid, 256, 0, st>>>(p, jobs);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_gate_grad_typed(GateGrad p, const PackJobs& jobs, unsigned copies, ColumnSums& sums, hipStream_t st) {
+  constexpr int EC = 16 / sizeof(T);
+  p.part_rows = sum_rows(p.rows, p.n, EC);
+  const long long parts = (p.rows + p.part_rows - 1) / p.part_rows;
+  const long long blocks = parts * ((p.n + 32 * EC - 1) / (32 * EC));
+  if (blocks + copies > 0x7fffffffLL) return hipErrorInvalidValue;
+  p.blocks = (unsigned)blocks;
+  if (parts == 1) p.partial = nullptr;
+  else if (p.dbias) sums = {p.partial, (int)parts, 2 * p.n, p.dbias};
+  const dim3 grid = grid_of(blocks + copies);
+  if (p.act == VB_ACT_NONE) gate_grad_kernel<T, VB_ACT_NONE><<<grid, 256, 0, st>>>(p, jobs);
+  else if (p.act == VB_ACT_RELU) gate_grad_kernel<T, VB_ACT_RELU><<<grid, 256, 0, st>>>(p, jobs);
+  else if (p.act == VB_ACT_GELU) gate_grad_kernel<T, VB_ACT_GELU><<<grid, 256, 0, st>>>(p, jobs);
+  else gate_grad_kernel<T, VB_ACT_SILU><<<grid, 256, 0, st>>>(p, jobs);
   return hipGetLastError();
 }
 
@@ -1115,7 +1317,7 @@ long long steps_of(long long K, int dtype) { return (K * (long long)elem_size(dt
 
 Tiling choose_tiling(int dtype, const Product& p) {
   const long long M = p.M, K = p.K;
-  const int N = p.N;
+  const int N = weight_rows_of(p);
   const Kind* kinds = dtype == VB_F32 ? k32 : k16;
   const int nk = dtype == VB_F32 ? 3 : 4;
   const long long stages = steps_of(K, dtype);
@@ -1185,8 +1387,8 @@ int pair_tile(const Product& dx, const Product& dw, int dtype) {
   return best;
 }
 
-size_t tiling_bytes(const Tiling& t, long long M, int N) {
-  return t.splits > 1 ? (size_t)t.splits * M * ((N + 3) / 4 * 4) * 4 : 0;
+size_t tiling_bytes(const Tiling& t, const Product& p) {
+  return t.splits > 1 ? (size_t)t.splits * p.M * partial_row(p) * 4 : 0;
 }
 
 // Up to 16 rows, and up to 32 where the weights are few (24 x 1024 -> 1024 in bf16: 5.2
@@ -1195,19 +1397,20 @@ size_t tiling_bytes(const Tiling& t, long long M, int N) {
 bool product_is_narrow(const Product& p, int dtype) {
   if (p.across_a || p.across_b) return false;
   const long long row = p.K * (long long)elem_size(dtype);
-  return p.M <= 16 || (p.M <= 32 && (p.N * row <= 8 << 20 || (p.N >= 12800 && row >= 8192)));
+  const int n = weight_rows_of(p);
+  return p.M <= 16 || (p.M <= 32 && (n * row <= 8 << 20 || (n >= 12800 && row >= 8192)));
 }
 
 size_t product_bytes(const Product& p, int dtype) {
   if (product_is_narrow(p, dtype)) return 0;
-  return tiling_bytes(choose_tiling(dtype, p), p.M, p.N);
+  return tiling_bytes(choose_tiling(dtype, p), p);
 }
 
 hipError_t launch_product(const Product& p, int dtype, hipStream_t st) {
   if (product_is_narrow(p, dtype)) {
-    if (dtype == VB_F32) return launch_narrow<float>(p, st);
-    if (dtype == VB_BF16) return launch_narrow<bf16>(p, st);
-    return launch_narrow<f16>(p, st);
+    if (dtype == VB_F32) return p.gated ? launch_narrow<float, true>(p, st) : launch_narrow<float, false>(p, st);
+    if (dtype == VB_BF16) return p.gated ? launch_narrow<bf16, true>(p, st) : launch_narrow<bf16, false>(p, st);
+    return p.gated ? launch_narrow<f16, true>(p, st) : launch_narrow<f16, false>(p, st);
   }
   const Tiling t = choose_tiling(dtype, p);
   if (dtype == VB_F32) return launch_tiled<float>(p, t, st);
@@ -1241,6 +1444,16 @@ hipError_t launch_act_grad(const ActGrad& p, PackJobs jobs, int dtype, ColumnSum
   if (dtype == VB_F32) return launch_act_grad_typed<float>(p, jobs, copies, sums, st);
   if (dtype == VB_BF16) return launch_act_grad_typed<bf16>(p, jobs, copies, sums, st);
   return launch_act_grad_typed<f16>(p, jobs, copies, sums, st);
+}
+
+size_t gate_grad_bytes(long long rows, int n, int dtype) { return 2 * act_grad_bytes(rows, n, dtype); }
+
+hipError_t launch_gate_grad(const GateGrad& p, PackJobs jobs, int dtype, ColumnSums& sums, hipStream_t st) {
+  const unsigned copies = pack_blocks(jobs, dtype);
+  if (copies == ~0u) return hipErrorInvalidValue;
+  if (dtype == VB_F32) return launch_gate_grad_typed<float>(p, jobs, copies, sums, st);
+  if (dtype == VB_BF16) return launch_gate_grad_typed<bf16>(p, jobs, copies, sums, st);
+  return launch_gate_grad_typed<f16>(p, jobs, copies, sums, st);
 }
 
 hipError_t launch_column_sums(const ColumnSums& s, int dtype, hipStream_t st) {

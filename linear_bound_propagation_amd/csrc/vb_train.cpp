@@ -2,115 +2,14 @@
 // sequence of launches.  Nothing here throws.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <new>
 
 #include "vb_train.h"
-#include "vb_train_internal.h"
+#include "vb_train_host.h"
 
 using namespace vb;
 
 namespace {
-
-vb_status fail(vb_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  return set_error(s, buf);
-}
-
-#define HIPCHK(expr)                                                                        \
-  do {                                                                                      \
-    hipError_t e_ = (expr);                                                                 \
-    if (e_ != hipSuccess) return fail(VB_EDEVICE, "%s: %s", #expr, hipGetErrorString(e_)); \
-  } while (0)
-
-size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
-
-// Bounds that keep byte offsets within a matrix below 2^62, row counts within a grid
-// dimension and, for the layers, a row within MAX_CHUNKED_ROW bytes.
-constexpr int64_t MAX_ROWS = 0x7fffffff, MAX_LD = INT64_C(1) << 30;
-constexpr int32_t MAX_WIDTH = 1 << 20, MAX_CLASSES = 1 << 30;
-static_assert(MAX_WIDTH * 4LL <= MAX_CHUNKED_ROW, "packed rows fit the product's offsets");
-
-vb_status check_sizes(const char* fn, int64_t rows, int32_t n_in, int32_t n_out, int32_t dtype,
-                      int32_t most = MAX_WIDTH) {
-  if (rows < 0 || rows > MAX_ROWS) return fail(VB_EINVAL, "%s: rows must be in [0, 2^31) (got %lld)", fn, (long long)rows);
-  if (n_in <= 0 || n_out <= 0) return fail(VB_EINVAL, "%s: sizes must be positive (got %d, %d)", fn, n_in, n_out);
-  if (n_in > most || n_out > most)
-    return fail(VB_EUNSUPPORTED, "%s: sizes above %d are not supported (got %d, %d)", fn, most, n_in, n_out);
-  if (dtype < VB_F32 || dtype > VB_F16) return fail(VB_EINVAL, "%s: unknown dtype %d", fn, dtype);
-  return VB_OK;
-}
-
-vb_status check_matrix(const char* fn, const char* name, const void* p, int64_t ld, int64_t n, int dtype, bool required) {
-  if (!p) return required ? fail(VB_EINVAL, "%s: %s is NULL", fn, name) : VB_OK;
-  if ((uintptr_t)p % elem_size(dtype)) return fail(VB_EINVAL, "%s: %s is not aligned to its elements", fn, name);
-  if (ld < n || ld > MAX_LD)
-    return fail(VB_ESHAPE, "%s: leading dimension of %s must be in [%lld, 2^30] (got %lld)", fn, name, (long long)n, (long long)ld);
-  return VB_OK;
-}
-
-vb_status check_ws(const char* fn, const void* ws, size_t ws_bytes, size_t need) {
-  if (!need) return VB_OK;
-  if (!ws || ws_bytes < need)
-    return fail(VB_ENOMEM, "%s: workspace too small (%zu bytes, needs %zu)", fn, ws ? ws_bytes : (size_t)0, need);
-  if ((uintptr_t)ws & 15) return fail(VB_EINVAL, "%s: workspace is not 16-byte aligned", fn);
-  return VB_OK;
-}
-
-// An argument's memory, and whether the call writes it.
-struct Named {
-  const char* name;
-  Span span;
-  bool written;
-};
-
-Named matrix(const char* name, const void* p, int64_t rows, int64_t n, int64_t ld, int dtype, bool written) {
-  const int64_t es = (int64_t)elem_size(dtype);
-  return {name, {(uintptr_t)p, rows, n * es, ld * es}, written};
-}
-
-Named block(const char* name, const void* p, int64_t bytes, bool written) {
-  return {name, {(uintptr_t)p, 1, bytes, bytes}, written};
-}
-
-// What is written shares no memory with anything else.  over: an output that may be that
-// input itself (their pointers and leading dimensions are equal).
-template <int N>
-vb_status check_overlaps(const char* fn, const Named (&m)[N], int out = -1, int over = -1) {
-  for (int i = 0; i < N; ++i)
-    for (int j = 0; j < N; ++j) {
-      if (!m[i].written || i == j || (m[j].written && j < i)) continue;
-      if (i == out && j == over && m[i].span.at == m[j].span.at) continue;
-      if (overlap(m[i].span, m[j].span)) return fail(VB_EINVAL, "%s: %s overlaps %s", fn, m[i].name, m[j].name);
-    }
-  return VB_OK;
-}
-
-#define TRY(expr)                   \
-  do {                              \
-    if (vb_status s_ = (expr)) return s_; \
-  } while (0)
-
-}  // namespace
-
-namespace {
-
-// A part of the workspace: its offset, or none.
-struct Part {
-  size_t at = 0;
-  bool used = false;
-  void take(size_t& total, size_t bytes) {
-    if (!bytes) return;
-    at = total, used = true;
-    total += align_up(bytes);
-  }
-  void* in(void* ws) const { return used ? (char*)ws + at : nullptr; }
-};
 
 // The forward product, and copies of operands whose rows a large product cannot read.
 struct ForwardPlan {
@@ -135,40 +34,46 @@ ForwardPlan plan_forward(const vb_linear_fwd& p) {
   return f;
 }
 
-// The backward products.  g is dy itself without an activation, else (or if dy's rows
-// cannot be read by a large product) a copy, in two parts where one number of the type
-// does not hold it.
-struct BackwardPlan {
-  Product dx{}, dw{};
-  Part g, g_low, x, w, sums, partial;
-  int pair = 0;  // tiles of one launch for both products
-  size_t total = 0;
-};
+// g is dy itself without an activation, else (or if dy's rows cannot be read by a large
+// product) a copy, in two parts where one number of the type does not hold it.
+BackwardCall backward_call(const vb_linear_bwd& p) {
+  BackwardCall c{};
+  c.rows = p.rows, c.n_in = p.n_in, c.n_g = p.n_out, c.dtype = p.dtype;
+  c.make_g = p.act != VB_ACT_NONE || !is_chunked(p.dy, p.ld_dy, p.n_out, p.dtype);
+  c.given = p.dy, c.ld_given = p.ld_dy;
+  c.two = p.dtype != VB_F32 && (p.act == VB_ACT_GELU || p.act == VB_ACT_SILU) && !p.round_g;
+  c.x = p.x, c.ld_x = p.ld_x, c.weight = p.weight, c.ld_w = p.ld_w;
+  c.dx = p.dx, c.ld_dx = p.ld_dx, c.dweight = p.dweight, c.ld_dw = p.ld_dw;
+  if (p.dbias && p.rows > 0) c.sums_bytes = act_grad_bytes(p.rows, p.n_out, p.dtype);
+  return c;
+}
 
-BackwardPlan plan_backward(const vb_linear_bwd& p) {
+}  // namespace
+
+BackwardPlan vb::plan_backward(const BackwardCall& p) {
   BackwardPlan f;
   if (p.rows == 0) return f;
   const int dt = p.dtype;
+  const long long ld_g = (long long)(chunked_row(p.n_g, dt) / elem_size(dt));
   Product& a = f.dx;
-  a.lda = p.ld_dy, a.a = p.dy;
+  a.a = p.given, a.lda = p.make_g ? ld_g : p.ld_given;
   a.b = p.weight, a.ldb = p.ld_w, a.across_b = true;
-  a.M = p.rows, a.N = p.n_in, a.K = p.n_out;
+  a.M = p.rows, a.N = p.n_in, a.K = p.n_g;
   a.out = p.dx, a.ld_out = p.ld_dx;
   Product& b = f.dw;
-  b.a = p.dy, b.lda = p.ld_dy, b.across_a = true;
+  b.a = a.a, b.lda = a.lda, b.across_a = true;
   b.b = p.x, b.ldb = p.ld_x, b.across_b = true;
-  b.M = p.n_out, b.N = p.n_in, b.K = p.rows;
+  b.M = p.n_g, b.N = p.n_in, b.K = p.rows;
   b.out = p.dweight, b.ld_out = p.ld_dw;
-  const bool two = dt != VB_F32 && (p.act == VB_ACT_GELU || p.act == VB_ACT_SILU) && !p.round_g;
-  a.passes = b.passes = two ? 2 : 1;
-  if ((p.dx || p.dweight) && (p.act != VB_ACT_NONE || !is_chunked(p.dy, p.ld_dy, p.n_out, dt))) {
-    f.g.take(f.total, p.rows * chunked_row(p.n_out, dt));
-    if (two) f.g_low.take(f.total, p.rows * chunked_row(p.n_out, dt));
+  a.passes = b.passes = p.two ? 2 : 1;
+  if ((p.dx || p.dweight) && p.make_g) {
+    f.g.take(f.total, p.rows * chunked_row(p.n_g, dt));
+    if (p.two) f.g_low.take(f.total, p.rows * chunked_row(p.n_g, dt));
   }
   const size_t row = chunked_row(p.n_in, dt);
   if (p.dweight && !is_chunked(p.x, p.ld_x, p.n_in, dt)) f.x.take(f.total, p.rows * row);
-  if (p.dx && !is_chunked(p.weight, p.ld_w, p.n_in, dt)) f.w.take(f.total, p.n_out * row);
-  if (p.dbias) f.sums.take(f.total, act_grad_bytes(p.rows, p.n_out, dt));
+  if (p.dx && !is_chunked(p.weight, p.ld_w, p.n_in, dt)) f.w.take(f.total, p.n_g * row);
+  f.sums.take(f.total, p.sums_bytes);
   if (p.dx && p.dweight) f.pair = pair_tile(a, b, dt);
   if (f.pair) return f;
   size_t parts = 0;  // the products run one after the other
@@ -181,7 +86,25 @@ BackwardPlan plan_backward(const vb_linear_bwd& p) {
   return f;
 }
 
-}  // namespace
+PackJobs vb::backward_copies(const BackwardCall& p, const BackwardPlan& f, void* ws) {
+  return {{{p.x, p.ld_x, p.rows, p.n_in, f.x.in(ws)}, {p.weight, p.ld_w, p.n_g, p.n_in, f.w.in(ws)}}};
+}
+
+vb_status vb::run_backward(const BackwardCall& p, BackwardPlan& f, const ColumnSums& sums, void* ws, hipStream_t st) {
+  if (f.g.used) f.dx.a = f.dw.a = f.g.in(ws), f.dx.a_low = f.dw.a_low = f.g_low.in(ws);
+  const long long ld = (long long)(chunked_row(p.n_in, p.dtype) / elem_size(p.dtype));
+  if (f.w.used) f.dx.b = f.w.in(ws), f.dx.ldb = ld;
+  if (f.x.used) f.dw.b = f.x.in(ws), f.dw.ldb = ld;
+  if (f.pair) {
+    HIPCHK(launch_pair(f.dx, f.dw, f.pair, sums, p.dtype, st));
+    return VB_OK;
+  }
+  if (sums.out) HIPCHK(launch_column_sums(sums, p.dtype, st));
+  f.dx.partial = f.dw.partial = (float*)f.partial.in(ws);
+  if (p.dx) HIPCHK(launch_product(f.dx, p.dtype, st));
+  if (p.dweight) HIPCHK(launch_product(f.dw, p.dtype, st));
+  return VB_OK;
+}
 
 extern "C" vb_status vb_linear_forward_workspace(const vb_linear_fwd* p, size_t* bytes) {
   const char* fn = "vb_linear_forward_workspace";
@@ -195,7 +118,7 @@ extern "C" vb_status vb_linear_backward_workspace(const vb_linear_bwd* p, size_t
   const char* fn = "vb_linear_backward_workspace";
   if (!p || !bytes) return fail(VB_EINVAL, "%s: NULL argument", fn);
   TRY(check_sizes(fn, p->rows, p->n_in, p->n_out, p->dtype));
-  *bytes = plan_backward(*p).total;
+  *bytes = plan_backward(backward_call(*p)).total;
   return VB_OK;
 }
 
@@ -254,7 +177,8 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
     return fail(VB_ESHAPE, "%s: dresidual over dy needs the same leading dimension", fn);
   const hipStream_t st = (hipStream_t)stream;
   const long long es = (long long)elem_size(p->dtype);
-  BackwardPlan f = plan_backward(*p);
+  const BackwardCall call = backward_call(*p);
+  BackwardPlan f = plan_backward(call);
   if (some) TRY(check_ws(fn, ws, ws_bytes, f.total));
   const void* saved = p->act == VB_ACT_NONE ? nullptr : p->saved;
   const Named memory[] = {matrix("dresidual", p->dresidual, p->rows, p->n_out, p->ld_dres, p->dtype, true),
@@ -272,7 +196,7 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
     if (p->dbias) HIPCHK(launch_fill_zero(p->dbias, 1, p->n_out * es, p->n_out * es, st));
     return VB_OK;
   }
-  const PackJobs jobs = {{{p->x, p->ld_x, p->rows, p->n_in, f.x.in(ws)}, {p->weight, p->ld_w, p->n_out, p->n_in, f.w.in(ws)}}};
+  const PackJobs jobs = backward_copies(call, f, ws);
   ColumnSums sums{};
   if (f.g.used || p->dbias || p->dresidual) {
     ActGrad g{};
@@ -283,22 +207,10 @@ extern "C" vb_status vb_linear_backward(const vb_linear_bwd* p, void* ws, size_t
     g.dbias = p->dbias, g.partial = (float*)f.sums.in(ws);
     g.rows = p->rows, g.n = p->n_out, g.act = p->act;
     HIPCHK(launch_act_grad(g, jobs, p->dtype, sums, st));
-    if (f.g.used) f.dx.a = f.dw.a = g.g, f.dx.a_low = f.dw.a_low = g.g_low, f.dx.lda = f.dw.lda = g.ld_g;
   } else {
     HIPCHK(launch_pack(jobs, p->dtype, st));
   }
-  const long long ld = (long long)chunked_row(p->n_in, p->dtype) / es;
-  if (f.w.used) f.dx.b = f.w.in(ws), f.dx.ldb = ld;
-  if (f.x.used) f.dw.b = f.x.in(ws), f.dw.ldb = ld;
-  if (f.pair) {
-    HIPCHK(launch_pair(f.dx, f.dw, f.pair, sums, p->dtype, st));
-    return VB_OK;
-  }
-  if (sums.out) HIPCHK(launch_column_sums(sums, p->dtype, st));
-  f.dx.partial = f.dw.partial = (float*)f.partial.in(ws);
-  if (p->dx) HIPCHK(launch_product(f.dx, p->dtype, st));
-  if (p->dweight) HIPCHK(launch_product(f.dw, p->dtype, st));
-  return VB_OK;
+  return run_backward(call, f, sums, ws, st);
 }
 
 extern "C" vb_status vb_cross_entropy_workspace(int64_t rows, int32_t classes, int32_t dtype, size_t* bytes) {

@@ -1,5 +1,6 @@
 // Internal interface between the host side (vb_train.cpp) and the kernels
-// (vb_linear.hip, vb_loss.hip, vb_clip.hip) of the training operators.
+// (vb_linear.hip, vb_loss.hip, vb_clip.hip; vb_block.cpp: vb_linear.hip, vb_norm.hip,
+// vb_dropout.hip) of the training operators.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -70,6 +71,9 @@ struct Product {
   long long M;
   int N;
   long long K;
+  // gated (neither operand across, one pass, no res): B has 2 N rows, bias 2 N numbers, pre 2 N
+  // columns; out(m, n) = act(v(m, n)) v(m, N + n)
+  bool gated;
   // epilogue: v = sum + bias[n] + res[m][n]; pre = v; out = act(v)
   const void* bias;
   const void* res;
@@ -136,6 +140,24 @@ struct ActGrad {
   int part_rows;
   unsigned blocks;
 };
+// g = (dy * up * act'(gate) | dy * act(gate)) of the gated layer, from pre = (gate | up): rows of
+// ld_g elements, 2 n of them and zeros to the end of the last chunk; else as ActGrad.
+struct GateGrad {
+  const void* dy;
+  const void* pre;
+  long long ld_dy, ld_pre;
+  void* g;
+  void* g_low;
+  long long ld_g;
+  void* dbias;
+  float* partial;
+  long long rows;
+  int n;
+  int act;
+  // set by launch_gate_grad
+  int part_rows;
+  unsigned blocks;
+};
 // dbias from sums over parts of the rows, parts x n
 struct ColumnSums {
   const float* partial;
@@ -145,11 +167,20 @@ struct ColumnSums {
 size_t act_grad_bytes(long long rows, int n, int dtype);
 // sums: set if dbias is left for launch_column_sums or launch_pair
 hipError_t launch_act_grad(const ActGrad& p, PackJobs jobs, int dtype, ColumnSums& sums, hipStream_t st);
+size_t gate_grad_bytes(long long rows, int n, int dtype);
+hipError_t launch_gate_grad(const GateGrad& p, PackJobs jobs, int dtype, ColumnSums& sums, hipStream_t st);
 hipError_t launch_column_sums(const ColumnSums& s, int dtype, hipStream_t st);
 // Both products of a backward pass by one launch, with tiles of this side (0: use two)
 int pair_tile(const Product& dx, const Product& dw, int dtype);
 hipError_t launch_pair(const Product& dx, const Product& dw, int tile, const ColumnSums& s, int dtype, hipStream_t st);
 hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long long ld_bytes, hipStream_t st);
+
+hipError_t launch_layer_norm(const vb_layer_norm_fwd& p, hipStream_t st);
+// ws: norm_grad_bytes, for the parts of dweight and dbias
+size_t norm_grad_bytes(long long rows, int n, int dtype);
+hipError_t launch_layer_norm_grad(const vb_layer_norm_bwd& p, float* ws, hipStream_t st);
+
+hipError_t launch_dropout(const vb_dropout_args& p, hipStream_t st);
 
 // ws: the count of the rows that are not ignored (int64, in 16 bytes), then the rows' losses
 // (float32) if the caller does not want them

@@ -1,6 +1,7 @@
 """Training and evaluation of the networks whose bounds the package computes:
-the fused linear layer and its backward pass, the softmax cross entropy with its
-gradient, and the clipping of gradients to a global norm (include/vb_train.h).
+the fused linear layer, the gated linear layer, layer norm and dropout, each with its
+backward pass, the softmax cross entropy with its gradient, and the clipping of gradients
+to a global norm (include/vb_train.h).
 
 Thin ctypes binding, like the rest of the package: every step runs in the
 library's HIP kernels on the current stream; results are new tensors on it.
@@ -21,9 +22,13 @@ DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
 EXPORTS = ["vb_linear_forward_workspace", "vb_linear_backward_workspace", "vb_linear_forward",
-           "vb_linear_backward", "vb_cross_entropy_workspace", "vb_cross_entropy", "vb_clip_grad_norm_workspace", "vb_clip_grad_norm"]
+           "vb_linear_backward", "vb_cross_entropy_workspace", "vb_cross_entropy", "vb_clip_grad_norm_workspace", "vb_clip_grad_norm",
+           "vb_gated_linear_forward_workspace", "vb_gated_linear_backward_workspace", "vb_gated_linear_forward",
+           "vb_gated_linear_backward", "vb_layer_norm_backward_workspace", "vb_layer_norm_forward",
+           "vb_layer_norm_backward", "vb_dropout"]
 
 _P, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_u64, _f64 = ctypes.c_uint64, ctypes.c_double
 
 
 class vb_linear_fwd(ctypes.Structure):
@@ -45,11 +50,46 @@ class vb_cross_entropy_args(ctypes.Structure):
                 ("row_loss", _P), ("dlogits", _P), ("ld_d", _i64)]
 
 
+class vb_gated_linear_fwd(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("n_in", _i32), ("n_out", _i32), ("dtype", _i32), ("act", _i32),
+                ("x", _P), ("ld_x", _i64), ("weight", _P), ("ld_w", _i64), ("bias", _P),
+                ("y", _P), ("ld_y", _i64), ("pre", _P), ("ld_pre", _i64)]
+
+
+class vb_gated_linear_bwd(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("n_in", _i32), ("n_out", _i32), ("dtype", _i32), ("act", _i32),
+                ("dy", _P), ("ld_dy", _i64), ("x", _P), ("ld_x", _i64), ("weight", _P), ("ld_w", _i64),
+                ("pre", _P), ("ld_pre", _i64), ("dx", _P), ("ld_dx", _i64), ("dweight", _P), ("ld_dw", _i64),
+                ("dbias", _P), ("round_g", _i32)]
+
+
+class vb_layer_norm_fwd(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("n", _i32), ("dtype", _i32), ("x", _P), ("ld_x", _i64), ("weight", _P), ("bias", _P),
+                ("eps", _f32), ("y", _P), ("ld_y", _i64), ("mean", _P), ("rstd", _P)]
+
+
+class vb_layer_norm_bwd(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("n", _i32), ("dtype", _i32), ("dy", _P), ("ld_dy", _i64), ("x", _P), ("ld_x", _i64),
+                ("mean", _P), ("rstd", _P), ("weight", _P), ("dresidual", _P), ("ld_dres", _i64), ("dx", _P),
+                ("ld_dx", _i64), ("dweight", _P), ("dbias", _P)]
+
+
+class vb_dropout_args(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("n", _i32), ("dtype", _i32), ("x", _P), ("ld_x", _i64), ("residual", _P),
+                ("ld_res", _i64), ("p", _f64), ("seed", _u64), ("offset", _u64), ("step", _P), ("y", _P), ("ld_y", _i64)]
+
+
 _FWD = struct.Struct("qiiiiQqQqQQqQqQq")    # vb_linear_fwd
 _BWD = struct.Struct("qiiiiQqQqQqQqQqQqQQqi4x")  # vb_linear_bwd
 _LOSS = struct.Struct("qiiQqQqffQQQq")      # vb_cross_entropy_args
-assert (_FWD.size, _BWD.size, _LOSS.size) == tuple(
-    ctypes.sizeof(c) for c in (vb_linear_fwd, vb_linear_bwd, vb_cross_entropy_args))
+_GATED = struct.Struct("qiiiiQqQqQQqQq")    # vb_gated_linear_fwd
+_GATED_BWD = struct.Struct("qiiiiQqQqQqQqQqQqQi4x")   # vb_gated_linear_bwd
+_NORM = struct.Struct("qiiQqQQf4xQqQQ")     # vb_layer_norm_fwd
+_NORM_BWD = struct.Struct("qiiQqQqQQQQqQqQQ")         # vb_layer_norm_bwd
+_DROP = struct.Struct("qiiQqQqdQQQQq")      # vb_dropout_args
+assert tuple(s.size for s in (_FWD, _BWD, _LOSS, _GATED, _GATED_BWD, _NORM, _NORM_BWD, _DROP)) == tuple(
+    ctypes.sizeof(c) for c in (vb_linear_fwd, vb_linear_bwd, vb_cross_entropy_args, vb_gated_linear_fwd,
+                               vb_gated_linear_bwd, vb_layer_norm_fwd, vb_layer_norm_bwd, vb_dropout_args))
 
 _call = None    # the declared functions, by name
 
@@ -64,7 +104,15 @@ def declare(lib: ctypes.CDLL) -> None:
                        ("vb_cross_entropy_workspace", [_i64, _i32, _i32, psz]),
                        ("vb_cross_entropy", [_P, _P, _sz, _P]),
                        ("vb_clip_grad_norm_workspace", [_i32, _P, psz]),
-                       ("vb_clip_grad_norm", [_i32, _P, _P, _P, _P, _f32, _P, _P, _sz, _P])):
+                       ("vb_clip_grad_norm", [_i32, _P, _P, _P, _P, _f32, _P, _P, _sz, _P]),
+                       ("vb_gated_linear_forward_workspace", [_P, psz]),
+                       ("vb_gated_linear_backward_workspace", [_P, psz]),
+                       ("vb_gated_linear_forward", [_P, _P, _sz, _P]),
+                       ("vb_gated_linear_backward", [_P, _P, _sz, _P]),
+                       ("vb_layer_norm_backward_workspace", [_i64, _i32, _i32, psz]),
+                       ("vb_layer_norm_forward", [_P, _P]),
+                       ("vb_layer_norm_backward", [_P, _P, _sz, _P]),
+                       ("vb_dropout", [_P, _P])):
         fn = getattr(lib, name)
         fn.restype = _i32
         fn.argtypes = args
@@ -130,7 +178,7 @@ def _no_graph(*tensors: Optional[torch.Tensor]) -> None:
     for t in tensors:
         if t is not None and t.requires_grad and torch.is_grad_enabled():
             raise ValueError("a tensor requires grad, and no autograd graph is recorded here: call under "
-                             "torch.no_grad() (or with detached tensors), and linear_backward or cross_entropy for gradients")
+                             "torch.no_grad() (or with detached tensors), and the *_backward calls or cross_entropy for gradients")
 
 
 def _act(act: str) -> int:
@@ -321,3 +369,190 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     _run("vb_clip_grad_norm", n, src.buffer_info()[0], dst or None, sizes.buffer_info()[0], types.buffer_info()[0],
          max_norm, norm.data_ptr(), *_scratch(ws, dev), _stream(dev))
     return norm, list(grads if out is None else out)
+
+
+def _halves(weight: torch.Tensor) -> int:
+    if weight.dim() != 2 or weight.shape[0] % 2:
+        raise ValueError(f"weight must be a matrix of the gate's rows and as many of up's, got {tuple(weight.shape)}")
+    return weight.shape[0] // 2
+
+
+def gated_linear_workspace(x: torch.Tensor, weight: torch.Tensor, backward: bool = False) -> torch.Tensor:
+    """A workspace for `gated_linear` calls (or `gated_linear_backward` calls, with all gradients and
+    either round_g) on tensors of these sizes, strides and alignment, to keep between calls."""
+    _device(x)
+    n_out = _halves(weight)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    rows, n_in = x.shape
+    head = (rows, n_in, n_out, _dtype(x), ACTS["silu"])
+    ld_x, ld_w = _matrix("x", x, rows, n_in, x), _matrix("weight", weight, 2 * n_out, n_in, x)
+    if backward:
+        need = [_size("vb_gated_linear_backward_workspace",
+                      _GATED_BWD.pack(*head, 0, n_out, x.data_ptr(), ld_x, weight.data_ptr(), ld_w, 0, 2 * n_out,
+                                      16, n_in, 16, n_in, 16, round_g)) for round_g in (0, 1)]
+        return _workspace(max(need), x.device)
+    p = _GATED.pack(*head, x.data_ptr(), ld_x, weight.data_ptr(), ld_w, 0, 16, n_out, 0, 2 * n_out)
+    return _workspace(_size("vb_gated_linear_forward_workspace", p), x.device)
+
+
+def gated_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "silu",
+                 want_pre: bool = False, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """y = act(gate) * up with (gate | up) = x W^T + bias (vb_gated_linear_forward): x [rows][n_in],
+    weight [2 n_out][n_in], the gate's rows first, bias [2 n_out]; act one of none, relu, gelu, silu.
+    With want_pre also (gate | up) [rows][2 n_out], which gated_linear_backward needs: (y, pre)."""
+    dev = _device(x)
+    dt = _dtype(x)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    rows, n_in = x.shape
+    n_out = _halves(weight)
+    _no_graph(x, weight, bias, out)
+    ld_x = _matrix("x", x, rows, n_in, x)
+    ld_w = _matrix("weight", weight, 2 * n_out, n_in, x)
+    if bias is not None:
+        _vector("bias", bias, 2 * n_out, x)
+    if out is None:
+        y, ld_y = x.new_empty((rows, n_out)), n_out
+    else:
+        y, ld_y = out, _matrix("out", out, rows, n_out, x)
+    pre = x.new_empty((rows, 2 * n_out)) if want_pre else None
+    p = _GATED.pack(rows, n_in, n_out, dt, _act(act), x.data_ptr(), ld_x, weight.data_ptr(), ld_w,
+                    0 if bias is None else bias.data_ptr(), y.data_ptr(), ld_y, 0 if pre is None else pre.data_ptr(),
+                    2 * n_out)
+    if ws is None:
+        ws = _workspace(_size("vb_gated_linear_forward_workspace", p), x.device)
+    _run("vb_gated_linear_forward", p, *_scratch(ws, dev), _stream(dev))
+    return (y, pre) if want_pre else y
+
+
+def gated_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, pre: torch.Tensor,
+                          act: str = "silu", want_x: bool = True, want_weight: bool = True, want_bias: bool = True,
+                          ws: Optional[torch.Tensor] = None, round_g: bool = False):
+    """Gradients of `gated_linear` (vb_gated_linear_backward) for the gradient dy of y and the forward
+    pass's pre: (dx, dweight, dbias), None where not wanted.  round_g: in a 16-bit type, dx and dweight
+    from the gradient of pre rounded to the type, in about half the time."""
+    dev = _device(x)
+    dt = _dtype(x)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    rows, n_in = x.shape
+    n_out = _halves(weight)
+    _no_graph(dy, x, weight, pre)
+    ld_dy = _matrix("dy", dy, rows, n_out, x)
+    ld_x = _matrix("x", x, rows, n_in, x)
+    ld_w = _matrix("weight", weight, 2 * n_out, n_in, x)
+    ld_p = _matrix("pre", pre, rows, 2 * n_out, x)
+    dx = x.new_empty((rows, n_in)) if want_x else None
+    dw = x.new_empty((2 * n_out, n_in)) if want_weight else None
+    db = x.new_empty((2 * n_out,)) if want_bias else None
+    p = _GATED_BWD.pack(rows, n_in, n_out, dt, _act(act), dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, weight.data_ptr(),
+                        ld_w, pre.data_ptr(), ld_p, 0 if dx is None else dx.data_ptr(), n_in,
+                        0 if dw is None else dw.data_ptr(), n_in, 0 if db is None else db.data_ptr(), bool(round_g))
+    if ws is None:
+        ws = _workspace(_size("vb_gated_linear_backward_workspace", p), x.device)
+    _run("vb_gated_linear_backward", p, *_scratch(ws, dev), _stream(dev))
+    return dx, dw, db
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, want_stats: bool = False, out: Optional[torch.Tensor] = None):
+    """y = (x - mean) rstd weight + bias of each row of x [rows][n] (vb_layer_norm_forward), rstd =
+    1 / sqrt(variance + eps); weight and bias [n].  With want_stats also the rows' statistics in
+    float32, which layer_norm_backward needs: (y, mean, rstd).  `out` may be x itself."""
+    dev = _device(x)
+    dt = _dtype(x)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    rows, n = x.shape
+    _no_graph(x, weight, bias, out)
+    ld_x = _matrix("x", x, rows, n, x)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _vector(name, t, n, x)
+    if out is None:
+        y, ld_y = x.new_empty((rows, n)), n
+    else:
+        y, ld_y = out, _matrix("out", out, rows, n, x)
+    mean = x.new_empty(rows, dtype=torch.float32) if want_stats else None
+    rstd = x.new_empty(rows, dtype=torch.float32) if want_stats else None
+    p = _NORM.pack(rows, n, dt, x.data_ptr(), ld_x, 0 if weight is None else weight.data_ptr(),
+                   0 if bias is None else bias.data_ptr(), eps, y.data_ptr(), ld_y,
+                   0 if mean is None else mean.data_ptr(), 0 if rstd is None else rstd.data_ptr())
+    _run("vb_layer_norm_forward", p, _stream(dev))
+    return (y, mean, rstd) if want_stats else y
+
+
+def layer_norm_workspace(x: torch.Tensor) -> torch.Tensor:
+    """A workspace for `layer_norm_backward` calls of these sizes, to keep between calls."""
+    _device(x)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    return _workspace(_size("vb_layer_norm_backward_workspace", *x.shape, _dtype(x)), x.device)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: Optional[torch.Tensor] = None, dresidual: Optional[torch.Tensor] = None,
+                        want_x: bool = True, want_weight: bool = True, want_bias: bool = True,
+                        dx: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Gradients of `layer_norm` (vb_layer_norm_backward) for the gradient dy of y and the forward pass's
+    statistics: (dx, dweight, dbias), None where not wanted.  dresidual: the gradient that reaches x
+    past the norm, added to dx.  `dx` may be dy or dresidual itself."""
+    dev = _device(x)
+    dt = _dtype(x)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    rows, n = x.shape
+    _no_graph(dy, x, mean, rstd, weight, dresidual, dx)
+    ld_x = _matrix("x", x, rows, n, x)
+    ld_dy = _matrix("dy", dy, rows, n, x)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype is not torch.float32 or t.shape != (rows,) or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous float32 [{rows}] on {x.device}")
+    if weight is not None:
+        _vector("weight", weight, n, x)
+    ld_r = n if dresidual is None else _matrix("dresidual", dresidual, rows, n, x)
+    ld_dx = n
+    if dx is not None:
+        ld_dx = _matrix("dx", dx, rows, n, x)
+    elif want_x:
+        dx = x.new_empty((rows, n))
+    dw = x.new_empty((n,)) if want_weight else None
+    db = x.new_empty((n,)) if want_bias else None
+    if ws is None:
+        ws = layer_norm_workspace(x)
+    p = _NORM_BWD.pack(rows, n, dt, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, mean.data_ptr(), rstd.data_ptr(),
+                       0 if weight is None else weight.data_ptr(), 0 if dresidual is None else dresidual.data_ptr(),
+                       ld_r, 0 if dx is None else dx.data_ptr(), ld_dx, 0 if dw is None else dw.data_ptr(),
+                       0 if db is None else db.data_ptr())
+    _run("vb_layer_norm_backward", p, *_scratch(ws, dev), _stream(dev))
+    return dx, dw, db
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Optional[torch.Tensor] = None,
+            step: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Dropout of x [rows][n] with the mask that (seed, offset) give (vb_dropout): kept elements / (1 - p),
+    zeros elsewhere, + residual.  The backward pass is the same call on the gradient, without the
+    residual.  seed and offset: 64-bit numbers, another offset for each use.  step: an int64 [1] on the
+    GPU that is added to offset, for calls that are captured and replayed.  `out` may be x or the
+    residual itself."""
+    dev = _device(x)
+    dt = _dtype(x)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    if not 0 <= seed < 2 ** 64 or not 0 <= offset < 2 ** 64:
+        raise ValueError(f"seed and offset must be in [0, 2^64), got {seed} and {offset}")
+    rows, n = x.shape
+    _no_graph(x, residual, out)
+    ld_x = _matrix("x", x, rows, n, x)
+    ld_r = n if residual is None else _matrix("residual", residual, rows, n, x)
+    if step is not None and (step.dtype is not torch.int64 or step.shape != (1,) or step.get_device() != dev):
+        raise ValueError(f"step must be int64 [1] on {x.device}")
+    if out is None:
+        y, ld_y = x.new_empty((rows, n)), n
+    else:
+        y, ld_y = out, _matrix("out", out, rows, n, x)
+    a = _DROP.pack(rows, n, dt, x.data_ptr(), ld_x, 0 if residual is None else residual.data_ptr(), ld_r, p, seed, offset,
+                   0 if step is None else step.data_ptr(), y.data_ptr(), ld_y)
+    _run("vb_dropout", a, _stream(dev))
+    return y
