@@ -192,9 +192,9 @@ extern "C" vb_status vb_layer_norm_backward(const vb_layer_norm_bwd* p, void* ws
   TRY(check_sizes(fn, p->rows, p->n, p->n, p->dtype));
   const bool some = p->rows > 0;
   TRY(check_matrix(fn, "dy", p->dy, p->ld_dy, p->n, p->dtype, some));
-  TRY(check_matrix(fn, "x", p->x, p->ld_x, p->n, p->dtype, some && (p->dx || p->dweight)));
-  TRY(check_matrix(fn, "mean", p->mean, p->rows, p->rows, VB_F32, some && (p->dx || p->dweight), MAX_ROWS));
-  TRY(check_matrix(fn, "rstd", p->rstd, p->rows, p->rows, VB_F32, some && (p->dx || p->dweight), MAX_ROWS));
+  TRY(check_matrix(fn, "x", p->x, p->ld_x, p->n, p->dtype, some));
+  TRY(check_matrix(fn, "mean", p->mean, p->rows, p->rows, VB_F32, some, MAX_ROWS));
+  TRY(check_matrix(fn, "rstd", p->rstd, p->rows, p->rows, VB_F32, some, MAX_ROWS));
   TRY(check_matrix(fn, "weight", p->weight, p->n, p->n, p->dtype, false));
   TRY(check_matrix(fn, "dresidual", p->dresidual, p->ld_dres, p->n, p->dtype, false));
   TRY(check_matrix(fn, "dx", p->dx, p->ld_dx, p->n, p->dtype, false));
@@ -209,16 +209,15 @@ extern "C" vb_status vb_layer_norm_backward(const vb_layer_norm_bwd* p, void* ws
   size_t need = 0;
   if (p->dweight || p->dbias) TRY(vb_layer_norm_backward_workspace(p->rows, p->n, p->dtype, &need));
   TRY(check_ws(fn, ws, ws_bytes, need));
-  const bool reads = p->dx || p->dweight;
   const Named memory[] = {matrix("dx", p->dx, p->rows, p->n, p->ld_dx, p->dtype, true),
                           matrix("dweight", p->dweight, 1, p->n, p->n, p->dtype, true),
                           matrix("dbias", p->dbias, 1, p->n, p->n, p->dtype, true),
                           block("the workspace", ws, (int64_t)need, true),
                           matrix("dy", p->dy, p->rows, p->n, p->ld_dy, p->dtype, false),
                           matrix("dresidual", p->dx ? p->dresidual : nullptr, p->rows, p->n, p->ld_dres, p->dtype, false),
-                          matrix("x", reads ? p->x : nullptr, p->rows, p->n, p->ld_x, p->dtype, false),
-                          block("mean", reads ? p->mean : nullptr, p->rows * 4, false),
-                          block("rstd", reads ? p->rstd : nullptr, p->rows * 4, false),
+                          matrix("x", p->x, p->rows, p->n, p->ld_x, p->dtype, false),
+                          block("mean", p->mean, p->rows * 4, false),
+                          block("rstd", p->rstd, p->rows * 4, false),
                           matrix("weight", p->dx ? p->weight : nullptr, 1, p->n, p->n, p->dtype, false)};
   TRY(check_overlaps(fn, memory, 0, 4, 5));
   const hipStream_t st = (hipStream_t)stream;

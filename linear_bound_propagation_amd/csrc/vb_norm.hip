@@ -1,11 +1,14 @@
 // Layer norm and its backward pass.
 //
 // A row is read once and stays in registers: TH threads have a row, CH chunks of 16 bytes
-// each (a wavefront per row up to 4 KB, a workgroup up to 128 KB).  Longer rows are read
-// again for each step (CH = 0).  Rows may start anywhere: 16-byte accesses at element
-// alignment are ordinary ones here, which cost extra only where a line is crossed; the last
-// chunk is taken element by element where the row ends inside it.
+// each (16 lanes per row up to 256 bytes, a wavefront up to 4 KB, a workgroup up to 128 KB).
+// Longer rows are read again for each step (CH = 0).  Rows may start anywhere: 16-byte accesses
+// at element alignment are ordinary ones here, which cost extra only where a line is crossed.
+//
+// What bounds it: HBM.  8192 x 8192 in bf16, 268 MB: 50 us, 5.4 TB/s (a large copy: 5.0);
+// backward at 8192 x 4096 with dresidual, dweight and dbias, 268 MB and 17 of parts: 56 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "vb_train_device.h"
 #include "vb_train_internal.h"
@@ -23,7 +26,7 @@ struct Vec {
 
 // Elements i0 .. of a row of n, zeros past its end.
 template <typename T>
-__device__ __forceinline__ typename Vec<T>::type load_chunk(const T* row, int i0, int n) {
+__device__ __forceinline__ typename Vec<T>::type load_part(const T* row, int i0, int n) {
   constexpr int EC = Vec<T>::EC;
   typename Vec<T>::type v;
   if (i0 + EC <= n) {
@@ -34,33 +37,66 @@ __device__ __forceinline__ typename Vec<T>::type load_chunk(const T* row, int i0
   }
   return v;
 }
+
 template <typename T>
-__device__ __forceinline__ void store_chunk(T* row, int i0, int n, const float* x) {
-  constexpr int EC = Vec<T>::EC;
+__device__ __forceinline__ typename Vec<T>::type all_of(float f) {
   typename Vec<T>::type v;
 #pragma unroll
-  for (int e = 0; e < EC; ++e) v[e] = from_f32<T>(x[e]);
-  if (i0 + EC <= n) {
-    *(typename Vec<T>::loose*)(row + i0) = v;
-  } else {
+  for (int e = 0; e < Vec<T>::EC; ++e) v[e] = (T)f;
+  return v;
+}
+
+// A thread's chunks of a row of at least one: number k is TH chunks after number k - 1.  The row's
+// last chunk ends with the row, so that some of its elements (skip of them) are the chunk's
+// before it too: they count nothing in sums and are stored twice, alike.  Chunks past the end are
+// that one again, and count nothing at all.  All threads then load as many whole chunks: no
+// branch stands between a load and those of the rows after it.
+// With CH = 0 a thread goes through as many chunks as the row has, each loaded where it is used.
+template <typename T, int TH, int CH>
+struct Chunks {
+  static constexpr int EC = Vec<T>::EC;
+  typedef typename Vec<T>::type V;
+  typedef typename Vec<T>::loose L;
+  int tid, n;
+  __device__ int count() const { return CH ? CH : ((n + EC - 1) / EC - tid + TH - 1) / TH; }
+  __device__ int begin(int k) const { return CH ? min((tid + k * TH) * EC, n - EC) : (tid + k * TH) * EC; }
+  // elements before `skip` or from `end` on are not this chunk's
+  __device__ int skip(int k) const { return CH ? min((tid + k * TH) * EC - begin(k), EC) : 0; }
+  __device__ int end(int k) const { return CH ? EC : min(n - begin(k), EC); }
+  __device__ V load(const T* row, int k) const {
+    if constexpr (CH > 0) return *(const L*)(row + begin(k));
+    else return load_part(row, begin(k), n);
+  }
+  __device__ void store(T* row, int k, const float* x) const {
+    V v;
+#pragma unroll
+    for (int e = 0; e < EC; ++e) v[e] = from_f32<T>(x[e]);
+    if (CH == 0 && end(k) < EC) {
+#pragma unroll
+      for (int e = 0; e < EC; ++e)
+        if (e < end(k)) row[begin(k) + e] = v[e];
+    } else if (skip(k) < EC) {
+      *(L*)(row + begin(k)) = v;
+    }
+  }
+  // zeros where x is not this chunk's
+  __device__ void mask(int k, float* x) const {
+    if (skip(k) == 0 && end(k) == EC) return;
 #pragma unroll
     for (int e = 0; e < EC; ++e)
-      if (i0 + e < n) row[i0 + e] = v[e];
+      if (e < skip(k) || e >= end(k)) x[e] = 0.f;
   }
-}
-// weight or bias in float32; `none` where there is none
-template <typename T>
-__device__ __forceinline__ void load_factors(const T* p, int i0, int n, float none, float* f) {
-  constexpr int EC = Vec<T>::EC;
-  if (p) {
-    const typename Vec<T>::type v = load_chunk(p, i0, n);
+  // f(k) for each chunk
+  template <typename F>
+  __device__ void each(F&& f) const {
+    if constexpr (CH > 0) {
 #pragma unroll
-    for (int e = 0; e < EC; ++e) f[e] = to_f32((T)v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < EC; ++e) f[e] = none;
+      for (int k = 0; k < CH; ++k) f(k);
+    } else {
+      for (int k = 0; k < count(); ++k) f(k);
+    }
   }
-}
+};
 
 // Keeps the compiler from carrying a row's converted values from one use to the next beside
 // the row itself (three times the registers).
@@ -75,237 +111,319 @@ __device__ __forceinline__ void forget(V (&v)[CH]) {
   }
 }
 
-// Sums of a and b over the TH threads of a row, given to all of them; red: two words per
-// wavefront, free again after the next barrier but one.
-template <int TH>
-__device__ __forceinline__ void sum_row(float& a, float& b, float (*red)[2]) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    a += __shfl_xor(a, o, 64);
-    b += __shfl_xor(b, o, 64);
-  }
-  if (TH == 64) return;
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][0] = a, red[threadIdx.x >> 6][1] = b;
-  __syncthreads();
-  a = red[0][0], b = red[0][1];
-#pragma unroll
-  for (int i = 1; i < TH / 64; ++i) a += red[i][0], b += red[i][1];
-  __syncthreads();
+// Sum over 16 lanes, or a wavefront, given to all of them: four steps within 16 lanes on the
+// vector units (quad permutes, half mirror, mirror), then the four rows' sums as scalars.  (Six
+// shuffles through LDS are six of its latencies on a row's critical path.)
+template <int LANES>
+__device__ __forceinline__ float sum_lanes(float v) {
+  auto step = [](float x, auto ctrl) {
+    return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v = step(v, std::integral_constant<int, 0xB1>());   // lane ^ 1
+  v = step(v, std::integral_constant<int, 0x4E>());   // lane ^ 2
+  v = step(v, std::integral_constant<int, 0x141>());  // 7 - lane, of 8
+  v = step(v, std::integral_constant<int, 0x140>());  // 15 - lane, of 16
+  if (LANES == 16) return v;
+  auto row = [&](int lane) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
 }
 
-// rows of a workgroup at a time
-constexpr int rows_at_once(int th) { return th < 256 ? 256 / th : 1; }
+// Sums of a and b over the TH threads of a row, given to all of them; red: two words per
+// wavefront, of two sets in turn, so that one barrier does (all of the workgroup's threads).
+template <int TH>
+__device__ __forceinline__ void sum_row(float& a, float& b, float (*red)[2]) {
+  a = sum_lanes<TH == 16 ? 16 : 64>(a), b = sum_lanes<TH == 16 ? 16 : 64>(b);
+  if (TH <= 64) return;
+  const int wave = threadIdx.x >> 6, first = wave / (TH / 64) * (TH / 64);
+  if ((threadIdx.x & 63) == 0) red[wave][0] = a, red[wave][1] = b;
+  __syncthreads();
+  a = red[first][0], b = red[first][1];
+#pragma unroll
+  for (int i = 1; i < TH / 64; ++i) a += red[first + i][0], b += red[first + i][1];
+}
 
 // Differences are taken from the row's first element, whose distance from the others is as small
 // as the row's own spread (equal numbers: 0, exactly), then from their mean, and as that is
 // rounded, the mean of what is left comes beside the squares and is taken off as well.
-template <typename T, int TH, int CH>
-__global__ __launch_bounds__(TH < 256 ? 256 : TH) void norm_kernel(vb_layer_norm_fwd p) {
-  constexpr int EC = Vec<T>::EC, PER = rows_at_once(TH);
-  __shared__ float red[TH / 64][2];
+// Workgroups of WG threads have WG / TH rows at a time.
+template <typename T, int WG, int TH, int CH>
+__global__ __launch_bounds__(WG) void norm_kernel(vb_layer_norm_fwd p) {
+  typedef typename Vec<T>::type V;
+  constexpr int EC = Vec<T>::EC, PER = WG / TH;
+  static_assert(PER == 1 || TH <= 64, "rows that end before others pass no barrier");
+  __shared__ float red[2][WG / 64][2];
   const long long r = (long long)workgroup_number() * PER + threadIdx.x / TH;
-  if (r >= p.rows) return;  // whole wavefronts, and no barrier when PER > 1
-  const int tid = threadIdx.x % TH, n = p.n, chunks = (n + EC - 1) / EC;
+  if (r >= p.rows) return;
+  const Chunks<T, TH, CH> c{(int)threadIdx.x % TH, p.n};
   const T* x = (const T*)p.x + r * p.ld_x;
   T* y = (T*)p.y + r * p.ld_y;
-  typename Vec<T>::type v[CH ? CH : 1];
-  // f(chunk, its first element) for each chunk of this thread
-  auto each = [&](auto&& f) {
-    if constexpr (CH > 0) {
+  V v[CH ? CH : 1];
+  if constexpr (CH > 0) c.each([&](int k) { v[k] = c.load(x, k); });
+  auto differences = [&](int k, float from, float* d) {
+    V u;
+    if constexpr (CH > 0) u = v[k];
+    else u = c.load(x, k);
 #pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const int i0 = (tid + k * TH) * EC;
-        if (i0 < n) f(v[k], i0);
-      }
-    } else {
-      for (int c = tid; c < chunks; c += TH) f(load_chunk(x, c * EC, n), c * EC);
-    }
+    for (int e = 0; e < EC; ++e) d[e] = to_f32((T)u[e]) - from;
   };
-  if constexpr (CH > 0) {
-#pragma unroll
-    for (int k = 0; k < CH; ++k) v[k] = load_chunk(x, (tid + k * TH) * EC, n);
-  }
-  const float inv = 1.f / (float)n, x0 = to_f32(x[0]);
+  const float inv = 1.f / (float)p.n, x0 = to_f32(x[0]);
   float first = 0.f, unused = 0.f;
-  each([&](auto c, int i0) {
+  c.each([&](int k) {
+    float d[EC];
+    differences(k, x0, d);
+    c.mask(k, d);
 #pragma unroll
-    for (int e = 0; e < EC; ++e) first += i0 + e < n ? to_f32((T)c[e]) - x0 : 0.f;
+    for (int e = 0; e < EC; ++e) first += d[e];
   });
-  sum_row<TH>(first, unused, red);
+  sum_row<TH>(first, unused, red[0]);
   if constexpr (CH > 0) forget(v);
   first *= inv;
   float rest = 0.f, squares = 0.f;
-  each([&](auto c, int i0) {
+  c.each([&](int k) {
+    float d[EC];
+    differences(k, x0, d);
 #pragma unroll
-    for (int e = 0; e < EC; ++e) {
-      const float d = i0 + e < n ? to_f32((T)c[e]) - x0 - first : 0.f;
-      rest += d;
-      squares = fmaf(d, d, squares);
-    }
+    for (int e = 0; e < EC; ++e) d[e] -= first;
+    c.mask(k, d);
+#pragma unroll
+    for (int e = 0; e < EC; ++e) rest += d[e], squares = fmaf(d[e], d[e], squares);
   });
-  sum_row<TH>(rest, squares, red);
+  sum_row<TH>(rest, squares, red[1]);
   if constexpr (CH > 0) forget(v);
   rest *= inv;
   float var = squares * inv - rest * rest;
   if (var < 0.f) var = 0.f;  // NaN stays
   const float rstd = 1.f / sqrtf(var + p.eps);
-  each([&](auto c, int i0) {
-    float w[EC], b[EC], o[EC];
-    load_factors((const T*)p.weight, i0, n, 1.f, w);
-    load_factors((const T*)p.bias, i0, n, 0.f, b);
+  c.each([&](int k) {
+    float d[EC];
+    differences(k, x0, d);
+    const V w = p.weight ? c.load((const T*)p.weight, k) : all_of<T>(1.f);
+    const V b = p.bias ? c.load((const T*)p.bias, k) : all_of<T>(0.f);
 #pragma unroll
-    for (int e = 0; e < EC; ++e) o[e] = fmaf((to_f32((T)c[e]) - x0 - first - rest) * rstd, w[e], b[e]);
-    store_chunk(y, i0, n, o);
+    for (int e = 0; e < EC; ++e) d[e] = fmaf((d[e] - first - rest) * rstd, to_f32((T)w[e]), to_f32((T)b[e]));
+    c.store(y, k, d);
   });
-  if (tid == 0) {
+  if (c.tid == 0) {
     if (p.mean) p.mean[r] = x0 + (first + rest);
     if (p.rstd) p.rstd[r] = rstd;
   }
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  With dweight or dbias (SUMS) a workgroup goes through rows `gridDim.x` rows (of
-// rows_at_once) apart and keeps their sums over its rows in registers, two float32 per column:
-// x and dy are then read once.  Its sums are one of the parts that norm_sum_kernel adds.
-template <typename T, int TH, int CH, bool SUMS>
-__global__ __launch_bounds__(TH < 256 ? 256 : TH) void norm_grad_kernel(vb_layer_norm_bwd p, float* partial) {
+// Backward.
+
+// A row of the backward pass in registers.
+template <typename T, int CH>
+struct GradRow {
+  typename Vec<T>::type x[CH ? CH : 1], dy[CH ? CH : 1], res[CH ? CH : 1];
+  float mean, rstd;
+};
+
+template <typename T, int TH, int CH, bool RES>
+struct Grad {
+  static constexpr int EC = Vec<T>::EC;
   typedef typename Vec<T>::type V;
-  constexpr int EC = Vec<T>::EC, PER = rows_at_once(TH), C1 = CH ? CH : 1;
-  __shared__ float red[TH / 64][2];
-  const int tid = threadIdx.x % TH, n = p.n, chunks = (n + EC - 1) / EC;
-  const float inv = 1.f / (float)n;
-  float sum_w[C1][EC], sum_b[C1][EC];
+  const vb_layer_norm_bwd& p;
+  Chunks<T, TH, CH> c;
+  V w[CH ? CH : 1];
+
+  __device__ V weight(int k) const { return p.weight ? c.load((const T*)p.weight, k) : all_of<T>(1.f); }
+  __device__ void load_weight() {
+    if constexpr (CH > 0) c.each([&](int k) { w[k] = weight(k); });
+  }
+  __device__ void load(long long r, GradRow<T, CH>& row) const {
+    row.mean = p.mean[r], row.rstd = p.rstd[r];
+    if constexpr (CH > 0)
+      c.each([&](int k) {
+        row.x[k] = c.load((const T*)p.x + r * p.ld_x, k);
+        row.dy[k] = c.load((const T*)p.dy + r * p.ld_dy, k);
+        if (RES) row.res[k] = c.load((const T*)p.dresidual + r * p.ld_dres, k);
+      });
+  }
+  // chunk k's xh, dy and weight
+  __device__ void values(long long r, const GradRow<T, CH>& row, int k, float* xh, float* d, float* wf) const {
+    V xv, dv, wv;
+    if constexpr (CH > 0) xv = row.x[k], dv = row.dy[k], wv = w[k];
+    else xv = c.load((const T*)p.x + r * p.ld_x, k), dv = c.load((const T*)p.dy + r * p.ld_dy, k), wv = weight(k);
 #pragma unroll
-  for (int k = 0; k < C1; ++k)
-#pragma unroll
-    for (int e = 0; e < EC; ++e) sum_w[k][e] = sum_b[k][e] = 0.f;
-  const unsigned groups = SUMS ? gridDim.x : 0;
-  const bool with_x = p.dx || p.dweight;
-  for (long long r = (long long)workgroup_number() * PER + threadIdx.x / TH; r < p.rows; r += (long long)groups * PER) {
-    const T* x = (const T*)p.x + r * p.ld_x;
-    const T* dy = (const T*)p.dy + r * p.ld_dy;
-    const float mean = with_x ? p.mean[r] : 0.f, rstd = with_x ? p.rstd[r] : 0.f;
-    V xv[C1], dv[C1];
-    if constexpr (CH > 0) {
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const int i0 = (tid + k * TH) * EC;
-        xv[k] = with_x ? load_chunk(x, i0, n) : V{};
-        dv[k] = load_chunk(dy, i0, n);
-      }
+    for (int e = 0; e < EC; ++e) {
+      xh[e] = (to_f32((T)xv[e]) - row.mean) * row.rstd;
+      d[e] = to_f32((T)dv[e]);
+      wf[e] = to_f32((T)wv[e]);
     }
-    // f(number of the chunk, its first element, xh, dy) for each chunk of this thread
-    auto each = [&](auto&& f) {
-      auto one = [&](int k, int i0, V xc, V dc) {
-        float xh[EC], d[EC];
-#pragma unroll
-        for (int e = 0; e < EC; ++e) {
-          xh[e] = i0 + e < n ? (to_f32((T)xc[e]) - mean) * rstd : 0.f;
-          d[e] = to_f32((T)dc[e]);
-        }
-        f(k, i0, xh, d);
-      };
-      if constexpr (CH > 0) {
-#pragma unroll
-        for (int k = 0; k < CH; ++k)
-          if ((tid + k * TH) * EC < n) one(k, (tid + k * TH) * EC, xv[k], dv[k]);
-      } else {
-        for (int c = tid; c < chunks; c += TH) one(0, c * EC, load_chunk(x, c * EC, n), load_chunk(dy, c * EC, n));
-      }
-    };
-    float along = 0.f, level = 0.f;
-    each([&](int k, int i0, const float* xh, const float* d) {
-      float w[EC];
-      load_factors((const T*)p.weight, i0, n, 1.f, w);
+  }
+  // f(k, xh, dy) of each chunk beside the row's two sums
+  template <typename F>
+  __device__ void sums(long long r, const GradRow<T, CH>& row, float& along, float& level, F&& f) const {
+    along = level = 0.f;
+    c.each([&](int k) {
+      float xh[EC], d[EC], wf[EC];
+      values(r, row, k, xh, d, wf);
+      c.mask(k, xh), c.mask(k, d);
 #pragma unroll
       for (int e = 0; e < EC; ++e) {
-        const float g = d[e] * w[e];
+        const float g = d[e] * wf[e];
         level += g;
         along = fmaf(g, xh[e], along);
-        if (SUMS) {
+      }
+      f(k, xh, d);
+    });
+  }
+  // dx from the sums over n
+  __device__ void store(long long r, const GradRow<T, CH>& row, float along, float level) const {
+    c.each([&](int k) {
+      float xh[EC], d[EC], wf[EC], o[EC];
+      values(r, row, k, xh, d, wf);
+      V q{};
+      if constexpr (RES && CH > 0) q = row.res[k];
+      else if constexpr (RES) q = c.load((const T*)p.dresidual + r * p.ld_dres, k);
+#pragma unroll
+      for (int e = 0; e < EC; ++e) o[e] = fmaf(row.rstd, fmaf(-along, xh[e], fmaf(d[e], wf[e], -level)), to_f32((T)q[e]));
+      c.store((T*)p.dx + r * p.ld_dx, k, o);
+    });
+  }
+};
+
+template <typename T, int WG, int TH, int CH, bool RES>
+__global__ __launch_bounds__(WG) void norm_dx_kernel(vb_layer_norm_bwd p) {
+  constexpr int PER = WG / TH;
+  static_assert(PER == 1 || TH <= 64, "rows that end before others pass no barrier");
+  __shared__ float red[WG / 64][2];
+  const long long r = (long long)workgroup_number() * PER + threadIdx.x / TH;
+  if (r >= p.rows) return;
+  Grad<T, TH, CH, RES> g{p, {(int)threadIdx.x % TH, p.n}};
+  GradRow<T, CH> row;
+  g.load(r, row);
+  g.load_weight();
+  float along, level;
+  g.sums(r, row, along, level, [](int, const float*, const float*) {});
+  sum_row<TH>(along, level, red);
+  if constexpr (CH > 0) forget(row.x), forget(row.dy), forget(g.w);
+  const float inv = 1.f / (float)p.n;
+  g.store(r, row, along * inv, level * inv);
+}
+
+// Floats of a part's row: its columns' sums start on 16-byte boundaries.
+__host__ __device__ inline int part_row(int n) { return (n + 3) / 4 * 4; }
+
+// dx (DX) and the sums of dweight and dbias in one pass: a workgroup goes through the rows, WG / TH
+// at a time, and keeps its rows' sums in registers, two float32 per column.  A row is on its way
+// while another is worked on, by loads without conditions, as the compiler waits for all
+// loads behind one (16384 x 2000 in float16 62 us with, 42 without): past the end they are of the
+// last row.  Not where two chunks of 1024 threads would spill for it (4096 x 16384 in bf16: 209
+// us, without 114).  The sums of rows side by side meet in LDS, and a workgroup's are one of the
+// parts that norm_sum_kernel adds.
+template <typename T, int WG, int TH, int CH, bool DX, bool RES>
+__global__ __launch_bounds__(WG) void norm_sums_kernel(vb_layer_norm_bwd p, float* partial) {
+  constexpr int EC = Vec<T>::EC, PER = WG / TH, AHEAD = CH == 1 || WG < 1024;
+  __shared__ float red[2][WG / 64][2];
+  Grad<T, TH, CH, RES> g{p, {(int)threadIdx.x % TH, p.n}};
+  const int n = p.n, side = threadIdx.x / TH;
+  const float inv = 1.f / (float)n;
+  float sum_w[CH][EC], sum_b[CH][EC];
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+#pragma unroll
+    for (int e = 0; e < EC; ++e) sum_w[k][e] = sum_b[k][e] = 0.f;
+  const long long first = (long long)workgroup_number() * PER, step = (long long)gridDim.x * PER;
+  GradRow<T, CH> row[AHEAD + 1];
+  g.load_weight();
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) g.load(min(first + side + i * step, p.rows - 1), row[i]);
+  int set = 0;
+  for (long long r0 = first; r0 < p.rows; r0 += step) {
+    const long long r = r0 + side;
+    g.load(min(r + AHEAD * step, p.rows - 1), row[AHEAD]);
+    float along, level;
+    g.sums(r, row[0], along, level, [&](int k, const float* xh, const float* d) {
+#pragma unroll
+      for (int e = 0; e < EC; ++e) {
+        if (PER == 1 || r < p.rows) {
           sum_w[k][e] = fmaf(d[e], xh[e], sum_w[k][e]);
           sum_b[k][e] += d[e];
         }
       }
     });
-    if (!p.dx) continue;
-    sum_row<TH>(along, level, red);
-    if constexpr (CH > 0) forget(xv), forget(dv);
-    along *= inv, level *= inv;
-    T* dx = (T*)p.dx + r * p.ld_dx;
-    const T* res = p.dresidual ? (const T*)p.dresidual + r * p.ld_dres : nullptr;
-    each([&](int, int i0, const float* xh, const float* d) {
-      float w[EC], q[EC], o[EC];
-      load_factors((const T*)p.weight, i0, n, 1.f, w);
-      load_factors(res, i0, n, 0.f, q);
+    if (DX) {
+      sum_row<TH>(along, level, red[set]);
+      set ^= 1;
+      forget(row[0].x), forget(row[0].dy), forget(g.w);
+      if (r < p.rows) g.store(r, row[0], along * inv, level * inv);
+    }
+    forget(g.w);
 #pragma unroll
-      for (int e = 0; e < EC; ++e) o[e] = fmaf(rstd, fmaf(-along, xh[e], fmaf(d[e], w[e], -level)), q[e]);
-      store_chunk(dx, i0, n, o);
-    });
-    if (!SUMS) return;
+    for (int i = 0; i < AHEAD; ++i) row[i] = row[i + 1];
   }
-  if constexpr (SUMS) {
-    // rows side by side in a workgroup: their sums meet in LDS, a chunk of each thread at a time
-    __shared__ float both[PER > 1 ? PER : 1][PER > 1 ? 64 * EC * 2 : 1];
-    float* out = partial + (long long)workgroup_number() * 2 * n;
+  __shared__ __align__(16) float both[PER > 1 ? PER : 1][2][PER > 1 ? TH * EC : 4];
+  float* out = partial + (long long)workgroup_number() * 2 * part_row(n);
+  g.c.each([&](int k) {
+    const int at = PER > 1 ? g.c.begin(k) - k * TH * EC : g.c.begin(k), skip = g.c.skip(k);
+    float *to_w = PER > 1 ? both[side][0] : out, *to_b = PER > 1 ? both[side][1] : out + part_row(n);
+    if (PER > 1) __syncthreads();
+    if (skip == 0) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int i0 = (tid + k * TH) * EC;
-      if constexpr (PER > 1) {
-        __syncthreads();
-        float* mine = both[threadIdx.x / TH];
-#pragma unroll
-        for (int e = 0; e < EC; ++e) mine[e * 64 + tid] = sum_w[k][e], mine[(EC + e) * 64 + tid] = sum_b[k][e];
-        __syncthreads();
-        if (threadIdx.x < TH) {
-#pragma unroll
-          for (int e = 0; e < EC; ++e)
-#pragma unroll
-            for (int j = 1; j < PER; ++j) {
-              sum_w[k][e] += both[j][e * 64 + tid];
-              sum_b[k][e] += both[j][(EC + e) * 64 + tid];
-            }
-        }
+      for (int e = 0; e < EC; e += 4) {
+        *(f32x4*)(to_w + at + e) = f32x4{sum_w[k][e], sum_w[k][e + 1], sum_w[k][e + 2], sum_w[k][e + 3]};
+        *(f32x4*)(to_b + at + e) = f32x4{sum_b[k][e], sum_b[k][e + 1], sum_b[k][e + 2], sum_b[k][e + 3]};
       }
-      if (threadIdx.x < TH) {
+    } else {
 #pragma unroll
-        for (int e = 0; e < EC; ++e)
-          if (i0 + e < n) out[i0 + e] = sum_w[k][e], out[n + i0 + e] = sum_b[k][e];
+      for (int e = 0; e < EC; ++e)
+        if (e >= skip) to_w[at + e] = sum_w[k][e], to_b[at + e] = sum_b[k][e];
+    }
+    if constexpr (PER > 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < 2 * TH * EC; i += WG) {
+        const int of = i / (TH * EC), j = i % (TH * EC), col = k * TH * EC + j;
+        float sum = both[0][of][j];
+#pragma unroll
+        for (int q = 1; q < PER; ++q) sum += both[q][of][j];
+        if (col < n) out[of * part_row(n) + col] = sum;
       }
     }
-  }
+  });
 }
 
-// dweight and dbias of rows too long for their sums to stay in registers: a thread has a
-// chunk of columns and every eighth of the workgroup's rows, 32 chunks a workgroup.
-constexpr int LONG_ROWS = 64;
+// dweight and dbias of few rows, or of rows too long for their sums to stay in registers: a
+// thread has a chunk of columns and every eighth of the workgroup's rows, 32 chunks a workgroup.
+constexpr int COLUMN_ROWS = 64;
 template <typename T>
 __global__ __launch_bounds__(256) void norm_columns_kernel(vb_layer_norm_bwd p, float* partial) {
-  constexpr int EC = Vec<T>::EC;
+  typedef typename Vec<T>::type V;
+  constexpr int EC = Vec<T>::EC, U = 4;
   __shared__ float red[2][8][32 * EC + 1];
   const unsigned across = (p.n + 32 * EC - 1) / (32 * EC), block = workgroup_number();
   const unsigned bx = block % across;
-  const long long by = block / across, m0 = by * LONG_ROWS;
+  const long long by = block / across, m0 = by * COLUMN_ROWS, end = min(m0 + COLUMN_ROWS, (long long)p.rows);
   if (m0 >= p.rows) return;  // the whole workgroup
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5, i0 = (bx * 32 + c) * EC;
   float sw[EC], sb[EC];
 #pragma unroll
   for (int e = 0; e < EC; ++e) sw[e] = sb[e] = 0.f;
   if (i0 < p.n)
-    for (long long m = m0 + w; m < min(m0 + LONG_ROWS, (long long)p.rows); m += 8) {
-      const typename Vec<T>::type d = load_chunk((const T*)p.dy + m * p.ld_dy, i0, p.n);
-      typename Vec<T>::type x{};
-      float mean = 0.f, rstd = 0.f;
-      if (p.dweight) {
-        x = load_chunk((const T*)p.x + m * p.ld_x, i0, p.n);
-        mean = p.mean[m], rstd = p.rstd[m];
+    for (long long m = m0 + w; m < end; m += 8 * U) {
+      V d[U], x[U];
+      float mean[U], rstd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long long r = m + 8 * u;
+        d[u] = x[u] = V{};
+        mean[u] = rstd[u] = 0.f;
+        if (r >= end) continue;
+        d[u] = load_part((const T*)p.dy + r * p.ld_dy, i0, p.n);
+        if (p.dweight) {
+          x[u] = load_part((const T*)p.x + r * p.ld_x, i0, p.n);
+          mean[u] = p.mean[r], rstd[u] = p.rstd[r];
+        }
       }
 #pragma unroll
-      for (int e = 0; e < EC; ++e) {
-        const float g = to_f32((T)d[e]);
-        sw[e] = fmaf(g, (to_f32((T)x[e]) - mean) * rstd, sw[e]);
-        sb[e] += g;
-      }
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < EC; ++e) {
+          const float g = to_f32((T)d[u][e]);
+          sw[e] = fmaf(g, (to_f32((T)x[u][e]) - mean[u]) * rstd[u], sw[e]);
+          sb[e] += g;
+        }
     }
 #pragma unroll
   for (int e = 0; e < EC; ++e) red[0][w][c * EC + e] = sw[e], red[1][w][c * EC + e] = sb[e];
@@ -315,7 +433,13 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(vb_layer_norm_bwd p, 
     float s = 0.f;
 #pragma unroll
     for (int q = 0; q < 8; ++q) s += red[k][q][j];
-    if (col < p.n) partial[(by * 2 + k) * p.n + col] = s;
+    if (col >= p.n) continue;
+    if (partial) {
+      partial[(by * 2 + k) * part_row(p.n) + col] = s;
+    } else {
+      T* out = (T*)(k ? p.dbias : p.dweight);
+      if (out) out[col] = from_f32<T>(s);
+    }
   }
 }
 
@@ -324,13 +448,13 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(vb_layer_norm_bwd p, 
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* partial, int parts, int n, T* dweight, T* dbias) {
   __shared__ float red[16][64];
-  const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + c;  // of 2 n
+  const int c = threadIdx.x & 63, w = threadIdx.x >> 6, across = (n + 63) / 64;
+  const int of = blockIdx.x / across, col = blockIdx.x % across * 64 + c;
   constexpr int U = 8;
   float v = 0.f;
-  if (col < 2 * n) {
-    const float* q = partial + col;
-    const long long step = 2LL * n;
+  if (col < n) {
+    const long long step = 2LL * part_row(n);
+    const float* q = partial + (long long)of * part_row(n) + col;
     int i = w;
     for (; i + 16 * (U - 1) < parts; i += 16 * U) {
       float x[U];
@@ -343,12 +467,12 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* partial, in
   }
   red[w][c] = v;
   __syncthreads();
-  if (w || col >= 2 * n) return;
+  if (w || col >= n) return;
   float sum = red[0][c];
 #pragma unroll
   for (int k = 1; k < 16; ++k) sum += red[k][c];
-  T* out = col < n ? dweight : dbias;
-  if (out) out[col < n ? col : col - n] = from_f32<T>(sum);
+  T* out = of ? dbias : dweight;
+  if (out) out[col] = from_f32<T>(sum);
 }
 
 template <typename T>
@@ -356,76 +480,109 @@ int chunks_of(int n) {
   return (n + Vec<T>::EC - 1) / Vec<T>::EC;
 }
 
-template <typename T, int TH, int CH>
+template <typename T, int WG, int TH, int CH>
 hipError_t norm_rows(const vb_layer_norm_fwd& p, hipStream_t st) {
-  constexpr int PER = rows_at_once(TH);
-  norm_kernel<T, TH, CH><<<grid_of((p.rows + PER - 1) / PER), TH < 256 ? 256 : TH, 0, st>>>(p);
+  constexpr int PER = WG / TH;
+  norm_kernel<T, WG, TH, CH><<<grid_of((p.rows + PER - 1) / PER), WG, 0, st>>>(p);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t norm_typed(const vb_layer_norm_fwd& p, hipStream_t st) {
   const int chunks = chunks_of<T>(p.n);
-  if (chunks <= 64) return norm_rows<T, 64, 1>(p, st);
-  if (chunks <= 128) return norm_rows<T, 64, 2>(p, st);
-  if (chunks <= 256) return norm_rows<T, 64, 4>(p, st);
-  if (chunks <= 512) return norm_rows<T, 256, 2>(p, st);
-  if (chunks <= 1024) return norm_rows<T, 256, 4>(p, st);
-  if (chunks <= 2048) return norm_rows<T, 256, 8>(p, st);
-  if (chunks <= 4096) return norm_rows<T, 1024, 4>(p, st);
-  if (chunks <= 8192) return norm_rows<T, 1024, 8>(p, st);
-  return norm_rows<T, 1024, 0>(p, st);
+  if (p.n < Vec<T>::EC) return norm_rows<T, 256, 16, 0>(p, st);
+  if (chunks <= 16) return norm_rows<T, 256, 16, 1>(p, st);
+  if (chunks <= 64) return norm_rows<T, 256, 64, 1>(p, st);
+  if (chunks <= 128) return norm_rows<T, 256, 64, 2>(p, st);
+  if (chunks <= 256) return norm_rows<T, 256, 64, 4>(p, st);
+  if (chunks <= 512) return norm_rows<T, 256, 256, 2>(p, st);
+  if (chunks <= 1024) return norm_rows<T, 256, 256, 4>(p, st);
+  if (chunks <= 2048) return norm_rows<T, 512, 512, 4>(p, st);
+  if (chunks <= 4096) return norm_rows<T, 1024, 1024, 4>(p, st);
+  if (chunks <= 8192) return norm_rows<T, 1024, 1024, 8>(p, st);
+  return norm_rows<T, 1024, 1024, 0>(p, st);
 }
 
-// Workgroups that keep the sums of their rows, or rows of a part where a row is too long.
-constexpr int SUM_GROUPS = 512, SUM_CHUNKS = 2048;
-long long parts_of(long long rows, int n, int chunks) {
-  if (chunks > SUM_CHUNKS) return (rows + LONG_ROWS - 1) / LONG_ROWS;
-  const int per = chunks <= 256 ? 4 : 1;
+// Parts of the sums: workgroups that keep those of their rows, one a CU, as each part is
+// written and read again (8192 x 4096 in bf16 with 512 parts of 512 threads: 68 against 63 us); or
+// COLUMN_ROWS rows each.
+constexpr int SUM_GROUPS = 256, SUM_CHUNKS = 2048;
+long long groups_of(long long rows, int chunks) {
+  const int per = chunks <= 16 ? 64 : chunks <= 64 ? 16 : chunks <= 128 ? 8 : chunks <= 256 ? 4 : chunks <= 512 ? 2 : 1;
   return std::min<long long>((rows + per - 1) / per, SUM_GROUPS);
 }
+// By columns where sums do not stay in registers (or rows are less than a chunk), where one workgroup has all rows of a column
+// (64 x 16384 in bf16: 9.2 us, as parts 13.5), and where there is nearly a part for every row,
+// which costs more than reading the row twice (250 x 16384 in bf16: 15.0 against 21.3 us).
+bool by_columns(long long rows, int n, int es) {
+  const int chunks = (n * es + 15) / 16;
+  return n * es < 16 || chunks > SUM_CHUNKS || rows <= COLUMN_ROWS || groups_of(rows, chunks) * 4 > rows * es;
+}
+long long parts_of(long long rows, int n, int es) {
+  return by_columns(rows, n, es) ? (rows + COLUMN_ROWS - 1) / COLUMN_ROWS : groups_of(rows, (n * es + 15) / 16);
+}
 
-template <typename T, int TH, int CH, bool SUMS>
-hipError_t norm_grad_rows(const vb_layer_norm_bwd& p, float* partial, unsigned parts, hipStream_t st) {
-  constexpr int PER = rows_at_once(TH);
-  const dim3 grid = SUMS ? dim3(parts) : grid_of((p.rows + PER - 1) / PER);
-  norm_grad_kernel<T, TH, CH, SUMS><<<grid, TH < 256 ? 256 : TH, 0, st>>>(p, partial);
+template <typename T, int WG, int TH, int CH>
+hipError_t norm_sums_rows(const vb_layer_norm_bwd& p, float* partial, unsigned parts, hipStream_t st) {
+  if (!p.dx) norm_sums_kernel<T, WG, TH, CH, false, false><<<parts, WG, 0, st>>>(p, partial);
+  else if (!p.dresidual) norm_sums_kernel<T, WG, TH, CH, true, false><<<parts, WG, 0, st>>>(p, partial);
+  else norm_sums_kernel<T, WG, TH, CH, true, true><<<parts, WG, 0, st>>>(p, partial);
   return hipGetLastError();
 }
 
-template <typename T, bool SUMS>
-hipError_t norm_grad_sized(const vb_layer_norm_bwd& p, float* partial, unsigned parts, hipStream_t st) {
+template <typename T>
+hipError_t norm_sums(const vb_layer_norm_bwd& p, float* partial, unsigned parts, hipStream_t st) {
   const int chunks = chunks_of<T>(p.n);
-  if (chunks <= 64) return norm_grad_rows<T, 64, 1, SUMS>(p, partial, parts, st);
-  if (chunks <= 128) return norm_grad_rows<T, 64, 2, SUMS>(p, partial, parts, st);
-  if (chunks <= 256) return norm_grad_rows<T, 64, 4, SUMS>(p, partial, parts, st);
-  if (chunks <= 512) return norm_grad_rows<T, 256, 2, SUMS>(p, partial, parts, st);
-  if (chunks <= 1024) return norm_grad_rows<T, 256, 4, SUMS>(p, partial, parts, st);
-  if (chunks <= 2048) return norm_grad_rows<T, 1024, 2, SUMS>(p, partial, parts, st);
-  if constexpr (!SUMS) {
-    if (chunks <= 4096) return norm_grad_rows<T, 1024, 4, false>(p, partial, parts, st);
-    return norm_grad_rows<T, 1024, 0, false>(p, partial, parts, st);
-  }
-  return hipErrorInvalidValue;
+  if (chunks <= 16) return norm_sums_rows<T, 1024, 16, 1>(p, partial, parts, st);
+  if (chunks <= 64) return norm_sums_rows<T, 1024, 64, 1>(p, partial, parts, st);
+  if (chunks <= 128) return norm_sums_rows<T, 1024, 128, 1>(p, partial, parts, st);
+  if (chunks <= 256) return norm_sums_rows<T, 1024, 256, 1>(p, partial, parts, st);
+  if (chunks <= 512) return norm_sums_rows<T, 1024, 512, 1>(p, partial, parts, st);
+  if (chunks <= 1024) return norm_sums_rows<T, 512, 512, 2>(p, partial, parts, st);
+  return norm_sums_rows<T, 1024, 1024, 2>(p, partial, parts, st);
+}
+
+template <typename T, int WG, int TH, int CH>
+hipError_t norm_dx_rows(const vb_layer_norm_bwd& p, hipStream_t st) {
+  constexpr int PER = WG / TH;
+  const dim3 grid = grid_of((p.rows + PER - 1) / PER);
+  if (p.dresidual) norm_dx_kernel<T, WG, TH, CH, true><<<grid, WG, 0, st>>>(p);
+  else norm_dx_kernel<T, WG, TH, CH, false><<<grid, WG, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t norm_dx(const vb_layer_norm_bwd& p, hipStream_t st) {
+  const int chunks = chunks_of<T>(p.n);
+  if (p.n < Vec<T>::EC) return norm_dx_rows<T, 256, 16, 0>(p, st);
+  if (chunks <= 16) return norm_dx_rows<T, 256, 16, 1>(p, st);
+  if (chunks <= 64) return norm_dx_rows<T, 256, 64, 1>(p, st);
+  if (chunks <= 128) return norm_dx_rows<T, 128, 128, 1>(p, st);
+  if (chunks <= 256) return norm_dx_rows<T, 256, 256, 1>(p, st);
+  if (chunks <= 512) return norm_dx_rows<T, 256, 256, 2>(p, st);
+  if (chunks <= 1024) return norm_dx_rows<T, 512, 512, 2>(p, st);
+  if (chunks <= 2048) return norm_dx_rows<T, 1024, 1024, 2>(p, st);
+  if (chunks <= 4096) return norm_dx_rows<T, 1024, 1024, 4>(p, st);
+  return norm_dx_rows<T, 1024, 1024, 0>(p, st);
 }
 
 template <typename T>
 hipError_t norm_grad_typed(const vb_layer_norm_bwd& p, float* ws, hipStream_t st) {
-  if (!p.dweight && !p.dbias) return norm_grad_sized<T, false>(p, nullptr, 0, st);
-  const int chunks = chunks_of<T>(p.n);
-  const long long parts = parts_of(p.rows, p.n, chunks);
-  if (chunks <= SUM_CHUNKS) {
-    if (const hipError_t e = norm_grad_sized<T, true>(p, ws, (unsigned)parts, st)) return e;
+  if (!p.dweight && !p.dbias) return norm_dx<T>(p, st);
+  const long long parts = parts_of(p.rows, p.n, sizeof(T));
+  if (!by_columns(p.rows, p.n, sizeof(T))) {
+    if (const hipError_t e = norm_sums<T>(p, ws, (unsigned)parts, st)) return e;
   } else {
     // before dx, which may lie over dy
     const long long blocks = parts * ((p.n + 32 * Vec<T>::EC - 1) / (32 * Vec<T>::EC));
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    norm_columns_kernel<T><<<grid_of(blocks), 256, 0, st>>>(p, ws);
+    norm_columns_kernel<T><<<grid_of(blocks), 256, 0, st>>>(p, parts > 1 ? ws : nullptr);
     if (const hipError_t e = hipGetLastError()) return e;
     if (p.dx)
-      if (const hipError_t e = norm_grad_sized<T, false>(p, nullptr, 0, st)) return e;
+      if (const hipError_t e = norm_dx<T>(p, st)) return e;
+    if (parts == 1) return hipSuccess;
   }
-  norm_sum_kernel<T><<<(2 * p.n + 63) / 64, 1024, 0, st>>>(ws, (int)parts, p.n, (T*)p.dweight, (T*)p.dbias);
+  norm_sum_kernel<T><<<(p.n + 63) / 64 * 2, 1024, 0, st>>>(ws, (int)parts, p.n, (T*)p.dweight, (T*)p.dbias);
   return hipGetLastError();
 }
 
@@ -438,8 +595,7 @@ hipError_t launch_layer_norm(const vb_layer_norm_fwd& p, hipStream_t st) {
 }
 
 size_t norm_grad_bytes(long long rows, int n, int dtype) {
-  const int ec = 16 / (int)elem_size(dtype), chunks = (n + ec - 1) / ec;
-  return (size_t)parts_of(rows, n, chunks) * 2 * n * 4;
+  return (size_t)parts_of(rows, n, (int)elem_size(dtype)) * 2 * part_row(n) * 4;
 }
 
 hipError_t launch_layer_norm_grad(const vb_layer_norm_bwd& p, float* ws, hipStream_t st) {
