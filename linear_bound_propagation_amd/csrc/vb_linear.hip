@@ -760,12 +760,15 @@ __global__ __launch_bounds__(256) void rows_kernel(Product p) {
 // boundary, a workgroup takes rows of one distance, and its x chunks start as much
 // earlier.  (7 x 5001 -> 3999 in float16: 20.6 us with weight chunks from the rows' starts,
 // which cross a line every other time, 13.5 so.)
-// GATED: half of the weight rows are the gate's, half the same ones of up, whose chunks start
-// where the gate's do, on boundaries or not.
+// GATED: half of the weight rows are the gate's, half the same ones of up, which may lie at
+// another distance from a boundary.  Each half has blocks and x chunks of its own (the same
+// chunks where the distances are), or, in a workgroup of one block, half the block and up's
+// chunks off boundaries.  (7 x 5001 -> 3999 in float16: 33 us in blocks of both, 26 in blocks of
+// their own; 16 x 1024 -> 1024 in float32, where workgroups are few: 6.4 and 8.7.)
 template <typename T, int MB, int NB, int NW, bool GATED>
 __global__ __launch_bounds__(64 * NW) void narrow_kernel(Product p, int period) {
   typedef typename Chunk<T>::type C;
-  constexpr int EC = 16 / sizeof(T), U = 2, OUT = MB * NB * 256;
+  constexpr int EC = 16 / sizeof(T), H = GATED && NB > 1 ? 2 : 1, HB = NB / H, U = H == 2 ? 4 : 2, OUT = MB * NB * 256;
   __shared__ __align__(16) float red[NW][OUT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, quarter = lane >> 4;
   constexpr int RO = GATED ? 8 * NB : 16 * NB;  // outputs
@@ -778,7 +781,6 @@ __global__ __launch_bounds__(64 * NW) void narrow_kernel(Product p, int period) 
     const int row = 16 * b + r16;
     w[b] = (const T*)p.b + (long long)(min(n0 + row % RO * period, last) + row / RO * p.N) * p.ldb;
   }
-  const int lead = __builtin_amdgcn_readfirstlane((int)((uintptr_t)w[0] % 16 / sizeof(T)));
   const T* x[MB];
 #pragma unroll
   for (int m = 0; m < MB; ++m) x[m] = (const T*)p.a + min((long long)(16 * m + r16), p.M - 1) * p.lda;
@@ -787,54 +789,88 @@ __global__ __launch_bounds__(64 * NW) void narrow_kernel(Product p, int period) 
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int m = 0; m < MB; ++m) acc[b][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const C* wv, const C* xv) {
+  auto multiply = [&](const C* wv, const C (*xv)[MB]) {
 #pragma unroll
     for (int q = 0; q < Chunk<T>::MFMAS; ++q)
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int m = 0; m < MB; ++m) acc[b][m] = Chunk<T>::mma(wv[b], xv[m], acc[b][m], q);
+        for (int m = 0; m < MB; ++m) acc[b][m] = Chunk<T>::mma(wv[b], xv[b / HB][m], acc[b][m], q);
   };
   // whole chunks first .. end - 1 (chunk c holds elements c EC - lead on), of which runs
-  const int K = (int)p.K, first = lead > 0, end = (lead + K) / EC;
-  const int runs = max(end - first, 0) / (4 * U);
+  int lead[H], first[H], runs = 0x7fffffff;
+  const int K = (int)p.K;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    lead[h] = __builtin_amdgcn_readfirstlane((int)((uintptr_t)w[h * HB] % 16 / sizeof(T)));
+    first[h] = lead[h] > 0;
+    runs = min(runs, max((lead[h] + K) / EC - first[h], 0) / (4 * U));
+  }
+  const bool alike = lead[0] == lead[H - 1];
   const int turn = runs ? (int)(blockIdx.x % (unsigned)runs) : 0;
   for (int s = wave; s < runs; s += NW) {
     const int run = s + turn < runs ? s + turn : s + turn - runs;
-    C wv[U][NB], xv[U][MB];
-    const long long k0 = (long long)(first + run * (4 * U) + quarter) * EC - lead;
+    C wv[U][NB], xv[U][H][MB];
+    long long k0[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) k0[h] = (long long)(first[h] + run * (4 * U) + quarter) * EC - lead[h];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        wv[u][b] = GATED ? load_loose(w[b] + k0 + u * 4 * EC) : *(const C*)(w[b] + k0 + u * 4 * EC);
+        wv[u][b] = GATED && H == 1 ? load_loose(w[b] + k0[0] + u * 4 * EC) : *(const C*)(w[b] + k0[b / HB] + u * 4 * EC);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int m = 0; m < MB; ++m) xv[u][m] = load_loose(x[m] + k0 + u * 4 * EC);
+      for (int m = 0; m < MB; ++m) xv[u][0][m] = load_loose(x[m] + k0[0] + u * 4 * EC);
+    if constexpr (H == 2) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int m = 0; m < MB; ++m) xv[u][1][m] = xv[u][0][m];
+      if (!alike) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int m = 0; m < MB; ++m) xv[u][1][m] = load_loose(x[m] + k0[1] + u * 4 * EC);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) multiply(wv[u], xv[u]);
   }
   // the chunks left over and those that the row fills in part (the first one comes last),
   // zeros elsewhere, a step of four per wavefront
-  const int rest = first + runs * 4 * U, total = (lead + K + EC - 1) / EC - rest + first;
-  auto part = [&](const T* q, int i) {
-    const int c = i == total - 1 && first ? 0 : rest + i, k0 = c * EC - lead;
+  int rest[H], total[H], most = 0;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    rest[h] = first[h] + runs * 4 * U, total[h] = (lead[h] + K + EC - 1) / EC - rest[h] + first[h];
+    most = max(most, total[h]);
+  }
+  auto part = [&](const T* q, int i, int h) {
+    const int c = i == total[h] - 1 && first[h] ? 0 : rest[h] + i, k0 = c * EC - lead[h];
     C v;
-    if (i < total && k0 >= 0 && k0 + EC <= K) {
+    if (GATED && K >= EC) {  // a whole chunk within the row, of which these elements stay
+      const int from = max(min(k0, K - EC), 0), begin = i < total[h] ? max(k0, 0) : K, end = min(k0 + EC, K);
+      v = load_loose(q + from);
+#pragma unroll
+      for (int e = 0; e < EC; ++e)
+        if (from + e < begin || from + e >= end) v[e] = (T)0.f;
+    } else if (i < total[h] && k0 >= 0 && k0 + EC <= K) {
       v = load_loose(q + k0);
     } else {
 #pragma unroll
-      for (int e = 0; e < EC; ++e) v[e] = i < total && k0 + e >= 0 && k0 + e < K ? q[k0 + e] : (T)0.f;
+      for (int e = 0; e < EC; ++e) v[e] = i < total[h] && k0 + e >= 0 && k0 + e < K ? q[k0 + e] : (T)0.f;
     }
     return v;
   };
-  for (int i0 = wave * 4; i0 < total; i0 += 4 * NW) {
-    C wv[NB], xv[MB];
+  for (int i0 = wave * 4; i0 < most; i0 += 4 * NW) {
+    C wv[NB], xv[H][MB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) wv[b] = part(w[b], i0 + quarter);
+    for (int b = 0; b < NB; ++b) wv[b] = part(w[b], i0 + quarter, b / HB);
 #pragma unroll
-    for (int m = 0; m < MB; ++m) xv[m] = part(x[m], i0 + quarter);
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) xv[h][m] = part(x[m], i0 + quarter, h);
     multiply(wv, xv);
   }
 #pragma unroll
@@ -892,12 +928,17 @@ hipError_t launch_narrow(const Product& p, hipStream_t st) {
     if (GATED) rows /= 2;
     return (unsigned)((p.N + rows * period - 1LL) / (rows * period) * period);
   };
-  const bool many = blocks(64) >= 200;
+  // where the halves' distances from boundaries differ, blocks of their own are worth half the
+  // workgroups (9 x 3001 -> 2501 in bf16: 15.9 against 21.3 us; alike, 16 x 4096 -> 2048: 13.9 and 10.6)
+  const bool alike = p.N * p.ldb * (long long)sizeof(T) % 16 == 0;
+  const bool many = blocks(64) >= 200, two = GATED && blocks(32) >= (alike ? 200 : 100);
   if (p.M <= 16) {
     if (many) narrow_kernel<T, 1, 4, 4, GATED><<<blocks(64), 256, 0, st>>>(p, period);
+    else if (two) narrow_kernel<T, 1, GATED ? 2 : 1, 16, GATED><<<blocks(32), 1024, 0, st>>>(p, period);
     else narrow_kernel<T, 1, 1, 16, GATED><<<blocks(16), 1024, 0, st>>>(p, period);
   } else {
     if (many) narrow_kernel<T, 2, 4, 4, GATED><<<blocks(64), 256, 0, st>>>(p, period);
+    else if (two) narrow_kernel<T, 2, GATED ? 2 : 1, 16, GATED><<<blocks(32), 1024, 0, st>>>(p, period);
     else narrow_kernel<T, 2, 1, 16, GATED><<<blocks(16), 1024, 0, st>>>(p, period);
   }
   return hipGetLastError();
