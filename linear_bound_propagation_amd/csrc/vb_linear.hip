@@ -635,9 +635,11 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSums s) {
 }
 
 // Both products of a backward pass, and dbias, by one launch: the sums' workgroups, then
-// the tiles of the product with the longer reduction, then the other's.
+// the tiles of the product that takes longer for one, then the other's; of a product whose
+// reduction is split, the tiles of its first part, of its second, ...
 template <typename T, int BM, int BN, int WM, int WN, bool TWO>
-__global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void pair_kernel(Product dx, Product dw, ColumnSums s, int tn) {
+__global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void pair_kernel(Product dx, Product dw, ColumnSums s, int tn,
+                                                                              int splits_x, int splits_w, bool dx_first) {
   __shared__ __align__(16) char lds[Ring<BM, BN, false, true>::BYTES];
   static_assert(Ring<BM, BN, false, true>::BYTES == Ring<BM, BN, true, true>::BYTES, "one ring for both");
   unsigned block = workgroup_number();
@@ -648,12 +650,18 @@ __global__ __launch_bounds__(64 * WM * WN, BN == 64 ? 3 : 2) void pair_kernel(Pr
   }
   block -= sums;
   const int tx = (int)((dx.M + BM - 1) / BM), tw = (int)((dw.M + BM - 1) / BM);
-  if (block >= ((unsigned)tx + tw) * tn) return;  // the whole workgroup
-  const unsigned first = (dx.K >= dw.K ? tx : tw) * tn;
-  if ((block < first) == (dx.K >= dw.K))
-    gemm_tile<T, BM, BN, WM, WN, false, true, TWO>(dx, tx, tn, block < first ? block : block - first, 0, lds);
-  else
-    gemm_tile<T, BM, BN, WM, WN, true, true, TWO>(dw, tw, tn, block < first ? block : block - first, 0, lds);
+  const unsigned nx = (unsigned)tx * tn * splits_x, nw = (unsigned)tw * tn * splits_w;
+  if (block >= nx + nw) return;  // the whole workgroup
+  const unsigned first = dx_first ? nx : nw;
+  const bool second = block >= first;
+  if (second) block -= first;
+  if (second != dx_first) {
+    const unsigned tiles = (unsigned)tx * tn, split = splits_x > 1 ? block / tiles : 0;
+    gemm_tile<T, BM, BN, WM, WN, false, true, TWO>(dx, tx, tn, block - split * tiles, split, lds);
+  } else {
+    const unsigned tiles = (unsigned)tw * tn, split = splits_w > 1 ? block / tiles : 0;
+    gemm_tile<T, BM, BN, WM, WN, true, true, TWO>(dw, tw, tn, block - split * tiles, split, lds);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -947,9 +955,9 @@ hipError_t launch_narrow(const Product& p, hipStream_t st) {
 // Adds the parts of a split reduction, in order, and finishes the outputs: four of a row
 // per thread.
 template <typename T, bool GATED>
-__global__ __launch_bounds__(256) void join_kernel(Product p, int splits) {
+__device__ __forceinline__ void join_quads(const Product& p, int splits, unsigned block) {
   const int quads = p.ld_partial / (GATED ? 8 : 4);
-  const long long i = (long long)workgroup_number() * 256 + threadIdx.x;
+  const long long i = (long long)block * 256 + threadIdx.x;
   const long long m = i / quads;
   const int n = (int)(i % quads) * 4;
   if (m >= p.M) return;
@@ -985,6 +993,19 @@ __global__ __launch_bounds__(256) void join_kernel(Product p, int splits) {
   }
 }
 
+template <typename T, bool GATED>
+__global__ __launch_bounds__(256) void join_kernel(Product p, int splits) {
+  join_quads<T, GATED>(p, splits, workgroup_number());
+}
+
+// The same for those of two products that are split: the first's workgroups, then the other's.
+template <typename T>
+__global__ __launch_bounds__(256) void join_pair_kernel(Product a, int splits_a, Product b, int splits_b, unsigned first) {
+  const unsigned block = workgroup_number();
+  if (block < first) join_quads<T, false>(a, splits_a, block);
+  else join_quads<T, false>(b, splits_b, block - first);
+}
+
 template <typename T, int BM, int BN, int WM, int WN>
 hipError_t launch_gemm(const Product& p, int splits, hipStream_t st) {
   const int outputs = p.gated ? BN / 2 : BN;  // of a tile's row
@@ -1011,14 +1032,24 @@ hipError_t launch_gemm(const Product& p, int splits, hipStream_t st) {
 // float32 numbers of a row of parts
 int partial_row(const Product& p) { return (p.N + 3) / 4 * (p.gated ? 8 : 4); }
 
+// Splits p's reduction into about `splits` parts; returns how many.
 template <typename T>
-hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
+int set_splits(Product& p, int splits) {
   // in steps of 64 bytes, an even number of them to a part
   const int steps = (int)((p.K * (long long)sizeof(T) + 63) / 64);
-  p.split_steps = ((steps + t.splits - 1) / t.splits + 1) / 2 * 2;
-  const int splits = (steps + p.split_steps - 1) / p.split_steps;
+  p.split_steps = ((steps + splits - 1) / splits + 1) / 2 * 2;
+  splits = (steps + p.split_steps - 1) / p.split_steps;
   if (splits == 1) p.partial = nullptr;
   p.ld_partial = partial_row(p);
+  return splits;
+}
+long long join_blocks(const Product& p, int splits) {
+  return splits > 1 ? (p.M * (p.ld_partial / (p.gated ? 8 : 4)) + 255) / 256 : 0;
+}
+
+template <typename T>
+hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
+  const int splits = set_splits<T>(p, t.splits);
   hipError_t e;
   if constexpr (sizeof(T) == 2) {
     if (t.bm == 256 && t.bn == 256) e = launch_gemm<T, 256, 256, 2, 4>(p, splits, st);
@@ -1031,7 +1062,7 @@ hipError_t launch_tiled(Product p, const Tiling& t, hipStream_t st) {
     else e = launch_gemm<T, 64, 64, 2, 2>(p, splits, st);
   }
   if (e != hipSuccess || splits == 1) return e;
-  const long long quads = p.M * (p.ld_partial / (p.gated ? 8 : 4)), blocks = (quads + 255) / 256;
+  const long long blocks = join_blocks(p, splits);
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   if (p.gated) join_kernel<T, true><<<grid_of(blocks), 256, 0, st>>>(p, splits);
   else join_kernel<T, false><<<grid_of(blocks), 256, 0, st>>>(p, splits);
@@ -1312,21 +1343,27 @@ hipError_t launch_gate_grad_typed(GateGrad p, const PackJobs& jobs, unsigned cop
 }
 
 template <typename T>
-hipError_t launch_pair_typed(Product dx, Product dw, int tile, const ColumnSums& s, hipStream_t st) {
-  for (Product* p : {&dx, &dw})  // no split
-    p->split_steps = (int)((p->K * (long long)sizeof(T) + 127) / 128 * 2), p->partial = nullptr;
-  const int tn = (dx.N + tile - 1) / tile;
-  const long long tiles = ((dx.M + tile - 1) / tile + (dw.M + tile - 1) / tile) * tn;
+hipError_t launch_pair_typed(Product dx, Product dw, const Pair& pair, const ColumnSums& s, hipStream_t st) {
+  const int sx = set_splits<T>(dx, pair.splits_x), sw = set_splits<T>(dw, pair.splits_w);
+  const int tile = pair.tile, tn = (dx.N + tile - 1) / tile;
+  const long long tiles = ((dx.M + tile - 1) / tile * sx + (dw.M + tile - 1) / tile * sw) * tn;
   const long long blocks = tiles + (s.out ? (s.n + 63) / 64 : 0);
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+  const bool first = dx.split_steps >= dw.split_steps;
+  const dim3 grid = grid_of(blocks);
   constexpr bool TWO = sizeof(T) == 2;
   if (TWO && dx.a_low) {
-    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, TWO><<<grid_of(blocks), 256, 0, st>>>(dx, dw, s, tn);
-    else pair_kernel<T, 128, 128, 2, 4, TWO><<<grid_of(blocks), 512, 0, st>>>(dx, dw, s, tn);
+    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, TWO><<<grid, 256, 0, st>>>(dx, dw, s, tn, sx, sw, first);
+    else pair_kernel<T, 128, 128, 2, 4, TWO><<<grid, 512, 0, st>>>(dx, dw, s, tn, sx, sw, first);
   } else {
-    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, false><<<grid_of(blocks), 256, 0, st>>>(dx, dw, s, tn);
-    else pair_kernel<T, 128, 128, 2, 4, false><<<grid_of(blocks), 512, 0, st>>>(dx, dw, s, tn);
+    if (tile == 64) pair_kernel<T, 64, 64, 2, 2, false><<<grid, 256, 0, st>>>(dx, dw, s, tn, sx, sw, first);
+    else pair_kernel<T, 128, 128, 2, 4, false><<<grid, 512, 0, st>>>(dx, dw, s, tn, sx, sw, first);
   }
+  const hipError_t e = hipGetLastError();
+  const long long jx = join_blocks(dx, sx), jw = join_blocks(dw, sw);
+  if (e != hipSuccess || jx + jw == 0) return e;
+  if (jx + jw > 0x7fffffffLL) return hipErrorInvalidValue;
+  join_pair_kernel<T><<<grid_of(jx + jw), 256, 0, st>>>(dx, sx, dw, sw, (unsigned)jx);
   return hipGetLastError();
 }
 
@@ -1397,24 +1434,33 @@ double list_time(double a, double c, double a2, double c2) {
 
 }  // namespace
 
-// Side of the tiles with which both products of a backward pass take one launch, which
-// fills the card while the first one ends, or 0 where two launches are faster by the same
-// model (the second one: 2 us).  Together | apart, with g and dbias: 1024 x 1024 -> 1024 in
-// bf16 19.4 | 23.7 us (64-wide tiles), float32 44 | 52; 1024 x 2048 -> 2048 34 | 41 (128);
-// 4096 x 2048 -> 2048 96 | 92.  A split reduction stays one, so that each gradient has the
-// same bits alone as with the other.
-int pair_tile(const Product& dx, const Product& dw, int dtype) {
+size_t tiling_bytes(const Tiling& t, const Product& p) {
+  return t.splits > 1 ? (size_t)t.splits * p.M * partial_row(p) * 4 : 0;
+}
+
+// Tiles with which both products of a backward pass take one launch, which fills the card while
+// the first one ends, and their parts' sums another; or none where launches of their own are
+// faster by the same model (each of those past the first: 2 us).  Together | apart, with g and
+// dbias: 1024 x 1024 -> 1024 in bf16 19.4 | 23.7 us (64-wide tiles), float32 44 | 52; 1024 x 2048
+// -> 2048 34 | 41 (128); 4096 x 2048 -> 2048 96 | 92; split (728 x 49 -> 780 in float16, two-part g) 16 | 28.  Each reduction is split as the
+// product's own launch would split it, so that a gradient has the same bits alone as with the
+// other.
+Pair choose_pair(const Product& dx, const Product& dw, int dtype) {
   const Tiling x = choose_tiling(dtype, dx), w = choose_tiling(dtype, dw);
-  if (x.splits > 1 || w.splits > 1) return 0;
-  const Product &first = dx.K >= dw.K ? dx : dw, &second = dx.K >= dw.K ? dw : dx;
-  const double run = (double)steps_of(first.K, dtype) * first.passes, run2 = (double)steps_of(second.K, dtype) * second.passes;
-  int best = 0;
+  auto run_of = [&](const Product& p, int splits) { return (double)((steps_of(p.K, dtype) + splits - 1) / splits) * p.passes; };
+  const bool dx_first = run_of(dx, x.splits) >= run_of(dw, w.splits);
+  const Product &first = dx_first ? dx : dw, &second = dx_first ? dw : dx;
+  const int splits = dx_first ? x.splits : w.splits, splits2 = dx_first ? w.splits : x.splits;
+  const double run = run_of(first, splits), run2 = run_of(second, splits2);
+  double join = 0.0;
+  if (x.splits > 1 || w.splits > 1) join = 2.0 + 2.0 * (tiling_bytes(x, dx) + tiling_bytes(w, dw)) / 6e6;
+  Pair best{0, x.splits, w.splits};
   double best_us = x.us + w.us + 2.0;
   const Kind* kinds = dtype == VB_F32 ? k32 + 1 : k16 + 2;
   for (int k = 0; k < 2; ++k) {
     const Kind& c = kinds[k];
-    auto tiles = [&](const Product& p) { return (double)((p.M + c.bm - 1) / c.bm) * ((p.N + c.bn - 1) / c.bn); };
-    const double n = tiles(first), n2 = tiles(second);
+    auto tiles = [&](const Product& p, int s) { return (double)((p.M + c.bm - 1) / c.bm) * ((p.N + c.bn - 1) / c.bn) * s; };
+    const double n = tiles(first, splits), n2 = tiles(second, splits2);
     double us;
     if (c.per_cu == 1) {
       us = list_time(n, run * c.share + c.fixed, n2, run2 * c.share + c.fixed) + 3.0;
@@ -1423,13 +1469,14 @@ int pair_tile(const Product& dx, const Product& dw, int dtype) {
                                      (n * run + n2 * run2) / 256.0 + run / 2);
       us = std::fmax(c.latency * run, c.share * share) + c.fixed * std::ceil((n + n2) / 256.0) + 3.0;
     }
-    if (us < best_us) best_us = us, best = c.bm;
+    us += join;
+    if (us < best_us) best_us = us, best.tile = c.bm;
   }
   return best;
 }
 
-size_t tiling_bytes(const Tiling& t, const Product& p) {
-  return t.splits > 1 ? (size_t)t.splits * p.M * partial_row(p) * 4 : 0;
+size_t pair_bytes(const Pair& pair, const Product& p, int splits) {
+  return pair.tile && splits > 1 ? (size_t)splits * p.M * partial_row(p) * 4 : 0;
 }
 
 // Up to 16 rows, and up to 32 where the weights are few (24 x 1024 -> 1024 in bf16: 5.2
@@ -1505,10 +1552,10 @@ hipError_t launch_column_sums(const ColumnSums& s, int dtype, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_pair(const Product& dx, const Product& dw, int tile, const ColumnSums& s, int dtype, hipStream_t st) {
-  if (dtype == VB_F32) return launch_pair_typed<float>(dx, dw, tile, s, st);
-  if (dtype == VB_BF16) return launch_pair_typed<bf16>(dx, dw, tile, s, st);
-  return launch_pair_typed<f16>(dx, dw, tile, s, st);
+hipError_t launch_pair(const Product& dx, const Product& dw, const Pair& pair, const ColumnSums& s, int dtype, hipStream_t st) {
+  if (dtype == VB_F32) return launch_pair_typed<float>(dx, dw, pair, s, st);
+  if (dtype == VB_BF16) return launch_pair_typed<bf16>(dx, dw, pair, s, st);
+  return launch_pair_typed<f16>(dx, dw, pair, s, st);
 }
 
 hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long long ld_bytes, hipStream_t st) {

@@ -74,8 +74,12 @@ BackwardPlan vb::plan_backward(const BackwardCall& p) {
   if (p.dweight && !is_chunked(p.x, p.ld_x, p.n_in, dt)) f.x.take(f.total, p.rows * row);
   if (p.dx && !is_chunked(p.weight, p.ld_w, p.n_in, dt)) f.w.take(f.total, p.n_g * row);
   f.sums.take(f.total, p.sums_bytes);
-  if (p.dx && p.dweight) f.pair = pair_tile(a, b, dt);
-  if (f.pair) return f;
+  if (p.dx && p.dweight) f.pair = choose_pair(a, b, dt);
+  if (f.pair.tile) {
+    f.partial.take(f.total, pair_bytes(f.pair, a, f.pair.splits_x));
+    f.partial_w.take(f.total, pair_bytes(f.pair, b, f.pair.splits_w));
+    return f;
+  }
   size_t parts = 0;  // the products run one after the other
   if (p.dx) parts = product_bytes(a, dt);
   if (p.dweight) {
@@ -95,12 +99,13 @@ vb_status vb::run_backward(const BackwardCall& p, BackwardPlan& f, const ColumnS
   const long long ld = (long long)(chunked_row(p.n_in, p.dtype) / elem_size(p.dtype));
   if (f.w.used) f.dx.b = f.w.in(ws), f.dx.ldb = ld;
   if (f.x.used) f.dw.b = f.x.in(ws), f.dw.ldb = ld;
-  if (f.pair) {
+  f.dx.partial = f.dw.partial = (float*)f.partial.in(ws);
+  if (f.pair.tile) {
+    f.dw.partial = (float*)f.partial_w.in(ws);
     HIPCHK(launch_pair(f.dx, f.dw, f.pair, sums, p.dtype, st));
     return VB_OK;
   }
   if (sums.out) HIPCHK(launch_column_sums(sums, p.dtype, st));
-  f.dx.partial = f.dw.partial = (float*)f.partial.in(ws);
   if (p.dx) HIPCHK(launch_product(f.dx, p.dtype, st));
   if (p.dweight) HIPCHK(launch_product(f.dw, p.dtype, st));
   return VB_OK;

@@ -126,8 +126,8 @@ struct BackwardCall {
 };
 struct BackwardPlan {
   Product dx{}, dw{};
-  Part g, g_low, x, w, sums, partial;
-  int pair = 0;  // tiles of one launch for both products
+  Part g, g_low, x, w, sums, partial, partial_w;  // partial_w: dw's, where both run at once
+  Pair pair{};
   size_t total = 0;
 };
 BackwardPlan plan_backward(const BackwardCall& p);

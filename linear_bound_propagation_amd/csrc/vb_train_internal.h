@@ -170,9 +170,14 @@ hipError_t launch_act_grad(const ActGrad& p, PackJobs jobs, int dtype, ColumnSum
 size_t gate_grad_bytes(long long rows, int n, int dtype);
 hipError_t launch_gate_grad(const GateGrad& p, PackJobs jobs, int dtype, ColumnSums& sums, hipStream_t st);
 hipError_t launch_column_sums(const ColumnSums& s, int dtype, hipStream_t st);
-// Both products of a backward pass by one launch, with tiles of this side (0: use two)
-int pair_tile(const Product& dx, const Product& dw, int dtype);
-hipError_t launch_pair(const Product& dx, const Product& dw, int tile, const ColumnSums& s, int dtype, hipStream_t st);
+// Both products of a backward pass by one launch, with tiles of this side (0: use their own), and
+// the parts of each reduction.  pair_bytes: of a product's `partial`.
+struct Pair {
+  int tile, splits_x, splits_w;
+};
+Pair choose_pair(const Product& dx, const Product& dw, int dtype);
+size_t pair_bytes(const Pair& pair, const Product& p, int splits);
+hipError_t launch_pair(const Product& dx, const Product& dw, const Pair& pair, const ColumnSums& s, int dtype, hipStream_t st);
 hipError_t launch_fill_zero(void* p, long long rows, long long row_bytes, long long ld_bytes, hipStream_t st);
 
 hipError_t launch_layer_norm(const vb_layer_norm_fwd& p, hipStream_t st);
