@@ -1372,7 +1372,8 @@ hipError_t launch_pair_typed(Product dx, Product dw, const Pair& pair, const Col
 // Tile and split of a large product by the time they would take on the CU with the most
 // tiles: 64-byte steps, those of both passes, of `share` microseconds (64-wide tiles,
 // three to a CU at a time, take `latency` where one has its CU to itself), the `fixed`
-// part of each tile, mostly its outputs, and a launch.  Measured, in us at 1024 x 1024 x
+// part of each tile, mostly its outputs, what a second pass over the stages adds to it (29478 x
+// 4544 of 36 float16 rows: tiles of 256 158 us, 256 x 128 133), and a launch.  Measured, in us at 1024 x 1024 x
 // 1024 | 2048 x 4096 x 4096 | 4096 x 4096 x 4096 | 4096 x 4096 x 32: bf16 tiles of 64 6.9
 // | 111 | 197 | 15.6, 128 10.0 | 85 | 140 | 15.6, 256 x 128 14 | 61 | 122 | 12.6, 256 24
 // | 92 | 113 | 13.2; float32 tiles of 64 21 | 479 | 966 | 24, 128 62 | 475 | 948 | 25,
@@ -1383,11 +1384,12 @@ namespace {
 
 struct Kind {
   int bm, bn, per_cu;
-  double fixed, latency, share;
+  double fixed, latency, share, again;
+  double ends(const Product& p) const { return fixed + (p.passes > 1 ? again : 0.0); }
 };
-const Kind k16[] = {{256, 256, 1, 8.0, 0.82, 0.82}, {256, 128, 1, 4.5, 0.43, 0.43}, {128, 128, 1, 3.0, 0.255, 0.255},
-                    {64, 64, 3, 0.8, 0.13, 0.115}};
-const Kind k32[] = {{256, 128, 1, 7.0, 1.80, 1.80}, {128, 128, 1, 3.5, 0.915, 0.915}, {64, 64, 3, 0.8, 0.275, 0.235}};
+const Kind k16[] = {{256, 256, 1, 8.0, 0.82, 0.82, 6.0}, {256, 128, 1, 4.5, 0.43, 0.43, 2.5}, {128, 128, 1, 3.0, 0.255, 0.255, 1.8},
+                    {64, 64, 3, 0.8, 0.13, 0.115, 0.4}};
+const Kind k32[] = {{256, 128, 1, 7.0, 1.80, 1.80, 0}, {128, 128, 1, 3.5, 0.915, 0.915, 0}, {64, 64, 3, 0.8, 0.275, 0.235, 0}};
 
 long long steps_of(long long K, int dtype) { return (K * (long long)elem_size(dtype) + 63) / 64; }
 
@@ -1399,18 +1401,27 @@ Tiling choose_tiling(int dtype, const Product& p) {
   const Kind* kinds = dtype == VB_F32 ? k32 : k16;
   const int nk = dtype == VB_F32 ? 3 : 4;
   const long long stages = steps_of(K, dtype);
+  auto time = [&](const Kind& c, int n, double ends) {
+    const double tiles = (double)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    const double on_cu = std::ceil(tiles * n / 256.0), run = (double)((stages + n - 1) / n) * p.passes;
+    double us = std::fmax(c.latency, on_cu * c.share) * run + on_cu * ends + 3.0;
+    if (n > 1) us += 2.0 + (2.0 * n * M * N * 4.0) / 6e6;
+    return us;
+  };
   Tiling best{64, 64, 1, 1e30};
   double unsplit = 0;
   for (int n = 1; n <= 32 && (n == 1 || n * 4 <= stages); n *= 2) {
     for (int k = 0; k < nk; ++k) {
-      const Kind& c = kinds[k];
-      const double tiles = (double)((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
-      const double on_cu = std::ceil(tiles * n / 256.0), run = (double)((stages + n - 1) / n) * p.passes;
-      double us = std::fmax(c.latency, on_cu * c.share) * run + on_cu * c.fixed + 3.0;
-      if (n > 1) us += 2.0 + (2.0 * n * M * N * 4.0) / 6e6;
-      if (us < best.us && (n == 1 || us < 0.92 * unsplit)) best = Tiling{c.bm, c.bn, n, us};
+      const double us = time(kinds[k], n, kinds[k].fixed);
+      if (us < best.us && (n == 1 || us < 0.92 * unsplit)) best = Tiling{kinds[k].bm, kinds[k].bn, n, us};
     }
     if (n == 1) unsplit = best.us;
+  }
+  // the split stands, and with it the order of the sums
+  if (p.passes > 1) best.us = 1e30;
+  for (int k = 0; k < nk && p.passes > 1; ++k) {
+    const double us = time(kinds[k], best.splits, kinds[k].ends(p));
+    if (us < best.us) best = Tiling{kinds[k].bm, kinds[k].bn, best.splits, us};
   }
   return best;
 }
@@ -1463,11 +1474,11 @@ Pair choose_pair(const Product& dx, const Product& dw, int dtype) {
     const double n = tiles(first, splits), n2 = tiles(second, splits2);
     double us;
     if (c.per_cu == 1) {
-      us = list_time(n, run * c.share + c.fixed, n2, run2 * c.share + c.fixed) + 3.0;
+      us = list_time(n, run * c.share + c.ends(dx), n2, run2 * c.share + c.ends(dw)) + 3.0;
     } else {  // a CU has its share of the steps and half a tile more; its tiles' ends overlap
       const double share = std::fmin(std::ceil(n / 256.0) * run + std::ceil(n2 / 256.0) * run2,
                                      (n * run + n2 * run2) / 256.0 + run / 2);
-      us = std::fmax(c.latency * run, c.share * share) + c.fixed * std::ceil((n + n2) / 256.0) + 3.0;
+      us = std::fmax(c.latency * run, c.share * share) + c.ends(dx) * std::ceil((n + n2) / 256.0) + 3.0;
     }
     us += join;
     if (us < best_us) best_us = us, best.tile = c.bm;
@@ -1486,6 +1497,10 @@ bool product_is_narrow(const Product& p, int dtype) {
   if (p.across_a || p.across_b) return false;
   const long long row = p.K * (long long)elem_size(dtype);
   const int n = weight_rows_of(p);
+  // long rows of few weights: a split reduction has more wavefronts (gated, 16 x 8192 -> 300 in
+  // bf16 16.6 against 9.6 us, 31 x 2048 -> 300 in float32 13.3 and 10.3; 16 x 2048 -> 300 in bf16
+  // 6.1 and 8.0)
+  if (p.gated && p.M > 4 && p.N <= 2048 && row * (p.M > 16 ? 2 : 1) >= 16384) return false;
   return p.M <= 16 || (p.M <= 32 && (n * row <= 8 << 20 || (n >= 12800 && row >= 8192)));
 }
 

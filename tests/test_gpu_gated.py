@@ -14,7 +14,7 @@ TYPES = [torch.float32, torch.bfloat16, torch.float16]
 ACTS = ["none", "relu", "gelu", "silu"]
 # (rows, n_in, n_out): a single token to large products, odd sizes, few and many of each
 SIZES = [(1, 1, 1), (1, 100, 7), (2, 4096, 40), (1, 515, 2100), (4, 333, 1001), (3, 64, 5000), (7, 501, 399), (16, 128, 8192),
-         (16, 1000, 33), (24, 300, 200), (32, 4100, 6500), (33, 17, 9), (64, 128, 64), (100, 784, 100), (129, 257, 130),
+         (16, 1000, 33), (11, 9001, 33), (20, 9000, 130), (24, 300, 200), (32, 4100, 6500), (33, 17, 9), (64, 128, 64), (100, 784, 100), (129, 257, 130),
          (300, 64, 515), (1037, 201, 99), (512, 2048, 96), (130, 4096, 130)]
 
 
