@@ -1387,7 +1387,7 @@ struct Kind {
   double fixed, latency, share, again;
   double ends(const Product& p) const { return fixed + (p.passes > 1 ? again : 0.0); }
 };
-const Kind k16[] = {{256, 256, 1, 8.0, 0.82, 0.82, 6.0}, {256, 128, 1, 4.5, 0.43, 0.43, 2.5}, {128, 128, 1, 3.0, 0.255, 0.255, 1.8},
+const Kind k16[] = {{256, 256, 1, 8.0, 0.82, 0.82, 7.0}, {256, 128, 1, 4.5, 0.43, 0.43, 2.5}, {128, 128, 1, 3.0, 0.255, 0.255, 1.8},
                     {64, 64, 3, 0.8, 0.13, 0.115, 0.4}};
 const Kind k32[] = {{256, 128, 1, 7.0, 1.80, 1.80, 0}, {128, 128, 1, 3.5, 0.915, 0.915, 0}, {64, 64, 3, 0.8, 0.275, 0.235, 0}};
 
