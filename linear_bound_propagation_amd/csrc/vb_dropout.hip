@@ -3,8 +3,10 @@
 // The mask is computed where it is used: seven rounds of Philox4x32 give four words, one per
 // element, so that a pass moves x (and the residual) in and y out and nothing else.  A round is
 // two 32 x 32 -> 64 bit products; a chunk of eight 16-bit elements takes 28 of them, which
-// fits under its memory accesses (2^26 bf16 numbers: 44.7 us, 6.0 TB/s, as a plain copy of
-// the same shape, 45.8; with ten rounds 63.7 us).
+// fits under its memory accesses (2^26 bf16 numbers, flat: 44.7 us, 6.0 TB/s, a plain copy 45.8;
+// with ten rounds 63.7 us).  So HBM bounds it: 8192 x 4096 in bf16 27 us, 5.0 TB/s, as a large
+// copy; 8192 x 8192 with a residual 71 us, 5.6 TB/s.  One chunk per thread: two or four gave 4.9
+// and 5.3 TB/s of the flat case's 6.0.
 #include <cmath>
 
 #include "vb_train_device.h"

@@ -81,7 +81,10 @@ __device__ __forceinline__ float act_grad(float dy, float s, int act) {
 //
 // What bounds it: in 16 bits the card's power (8192 x 8192 -> 8192 in bf16 0.97 ms, 1.13
 // PFLOP/s at about 1.4 GHz; the library's product 0.84 ms), in float32 the matrix cores
-// (8192 x 8192 -> 4096 3.78 ms, 145 TFLOP/s; the library's 3.60 ms).
+// (8192 x 8192 -> 4096 3.78 ms, 145 TFLOP/s; the library's 3.60 ms).  Gated, 4096 x 4096 -> 2 x 8192
+// in bf16: 432 us, 1.27 PFLOP/s, 462 with both projections written out (the library's product
+// alone 388); gate and up as columns of one tile cost nothing that the same product as a
+// linear layer does not, and its outputs are half as many.
 //
 // The MFMA wants, per lane, chunk q = lane / 16 (16 bytes along the reduction) of row
 // lane % 16.
@@ -1203,7 +1206,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGrad p, PackJobs jobs)
 }
 
 // g of the gated layer, its copies and its column sums: as act_grad_kernel, each chunk of dy
-// giving one of dgate and one of dup.
+// giving one of dgate and one of dup.  HBM bounds it (4096 x 8192 in bf16, SiLU, both parts of g:
+// 86 us, 470 MB at 5.5 TB/s).
 template <typename T, int ACT>
 __global__ __launch_bounds__(256) void gate_grad_kernel(GateGrad p, PackJobs jobs) {
   typedef typename Chunk<T>::type C;
