@@ -142,9 +142,10 @@ __device__ __forceinline__ void sum_row(float& a, float& b, float (*red)[2]) {
   for (int i = 1; i < TH / 64; ++i) a += red[first + i][0], b += red[first + i][1];
 }
 
-// Differences are taken from the row's first element, whose distance from the others is as small
-// as the row's own spread (equal numbers: 0, exactly), then from their mean, and as that is
-// rounded, the mean of what is left comes beside the squares and is taken off as well.
+// The mean is the row's first element and the mean of the differences from it, so that it is
+// exact for equal numbers, whatever their size, and off by the rounding of the row's spread else.
+// What it is off by, the mean of the differences from it, comes beside their squares and is
+// taken off as well.
 // Workgroups of WG threads have WG / TH rows at a time.
 template <typename T, int WG, int TH, int CH>
 __global__ __launch_bounds__(WG) void norm_kernel(vb_layer_norm_fwd p) {
@@ -177,13 +178,11 @@ __global__ __launch_bounds__(WG) void norm_kernel(vb_layer_norm_fwd p) {
   });
   sum_row<TH>(first, unused, red[0]);
   if constexpr (CH > 0) forget(v);
-  first *= inv;
+  first = x0 + first * inv;
   float rest = 0.f, squares = 0.f;
   c.each([&](int k) {
     float d[EC];
-    differences(k, x0, d);
-#pragma unroll
-    for (int e = 0; e < EC; ++e) d[e] -= first;
+    differences(k, first, d);
     c.mask(k, d);
 #pragma unroll
     for (int e = 0; e < EC; ++e) rest += d[e], squares = fmaf(d[e], d[e], squares);
@@ -196,15 +195,15 @@ __global__ __launch_bounds__(WG) void norm_kernel(vb_layer_norm_fwd p) {
   const float rstd = 1.f / sqrtf(var + p.eps);
   c.each([&](int k) {
     float d[EC];
-    differences(k, x0, d);
+    differences(k, first, d);
     const V w = p.weight ? c.load((const T*)p.weight, k) : all_of<T>(1.f);
     const V b = p.bias ? c.load((const T*)p.bias, k) : all_of<T>(0.f);
 #pragma unroll
-    for (int e = 0; e < EC; ++e) d[e] = fmaf((d[e] - first - rest) * rstd, to_f32((T)w[e]), to_f32((T)b[e]));
+    for (int e = 0; e < EC; ++e) d[e] = fmaf((d[e] - rest) * rstd, to_f32((T)w[e]), to_f32((T)b[e]));
     c.store(y, k, d);
   });
   if (c.tid == 0) {
-    if (p.mean) p.mean[r] = x0 + (first + rest);
+    if (p.mean) p.mean[r] = first + rest;
     if (p.rstd) p.rstd[r] = rstd;
   }
 }
@@ -259,7 +258,7 @@ struct Grad {
     c.each([&](int k) {
       float xh[EC], d[EC], wf[EC];
       values(r, row, k, xh, d, wf);
-      c.mask(k, xh), c.mask(k, d);
+      c.mask(k, xh), c.mask(k, d), c.mask(k, wf);
 #pragma unroll
       for (int e = 0; e < EC; ++e) {
         const float g = d[e] * wf[e];

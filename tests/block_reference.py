@@ -25,20 +25,20 @@ def layer_norm(x, w, b, eps):
     rstd = (var + eps) ** -0.5
     wd = torch.ones_like(c[:1]) if w is None else w.double()
     y = c * rstd * wd
-    # differences s from the first element (u s), their mean (off by (n + 2) u mean s), differences
-    # d from that, and the mean of those
-    s = (x - x[:, :1]).abs()
-    first = (n + 2) * U32 * s.mean(1, keepdim=True)
+    # a first mean from differences s to the first element, off by (n + 4) u mean s and its own
+    # rounding; differences d from that (u d), and the mean of those
+    s = (x - x[:, :1]).abs().mean(1, keepdim=True)
+    first = (n + 4) * U32 * s + 2 * U32 * mean.abs()
     d = c.abs() + first
-    em = U32 * s.mean(1, keepdim=True) + (n + 4) * U32 * d.mean(1, keepdim=True)
-    ec = U32 * s + 2 * U32 * d + em
-    ev = ((n + 8) * U32 * d * d + 2 * U32 * s * d).mean(1, keepdim=True)
+    em = (n + 4) * U32 * d.mean(1, keepdim=True)
+    ec = 2 * U32 * d + em
+    ev = (n + 8) * U32 * (d * d).mean(1, keepdim=True)
     er = 0.5 * ev / (var + eps) + 4 * U32                       # relative, of rstd
     ey = (ec * rstd + c.abs() * rstd * (er + 3 * U32)) * wd.abs()
     if b is not None:
         y = y + b.double()
     ey = ey + 2 * U32 * (y.abs() + (c * rstd * wd).abs())
-    return {"y": (y, rounded(y, ey, dt)), "mean": (mean[:, 0], (em + 2 * U32 * (mean.abs() + s.mean(1, keepdim=True) + first))[:, 0] + TINY[torch.float32]),
+    return {"y": (y, rounded(y, ey, dt)), "mean": (mean[:, 0], (em + 2 * U32 * (mean.abs() + first))[:, 0] + TINY[torch.float32]),
             "rstd": (rstd[:, 0], (rstd * (er + U32))[:, 0])}
 
 

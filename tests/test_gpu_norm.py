@@ -90,6 +90,31 @@ def test_rows_far_off_zero(lbp, mean):
         check({"y": y, "mean": m, "rstd": r}, ref.layer_norm(x, w, b, float(torch.tensor(1e-5))), f"far off {mean} {n}")
 
 
+@pytest.mark.parametrize("n", [100, 4096, 9001, 140001])
+def test_one_large_element(lbp, n):
+    """An element a million times the others, the first one or another: the others keep the bits that
+    their own size gives them (bounds of differences from the mean, not from the large one)."""
+    for at in (0, n // 2, n - 1):
+        x, w, b, _, _ = make(3, n, torch.float32, 6)
+        x[:, at] = torch.tensor([1e6, -3e5, 1e3], device="cuda")
+        y, m, r = lbp.layer_norm(x, w, b, want_stats=True)
+        check({"y": y, "mean": m, "rstd": r}, ref.layer_norm(x, w, b, float(torch.tensor(1e-5))), f"large {n} {at}")
+
+
+def test_an_infinite_weight_at_the_end(lbp):
+    """Elements that a row's last chunk shares with the one before it count once."""
+    for n in (13, 1003, 5001):
+        x, w, b, dy, _ = make(5, n, torch.bfloat16, 7)
+        _, mean, rstd = lbp.layer_norm(x, w, b, want_stats=True)
+        w[n - 3] = math.inf
+        dy[:, n - 3] = 1.0
+        x[:, n - 3] = x.amax() + 1
+        dx, dw, db = lbp.layer_norm_backward(dy, x, mean, rstd, w)
+        want = ref.layer_norm_backward(dy, x, mean, rstd, w, None)
+        assert torch.equal(torch.isnan(dx), torch.isnan(want["dx"][0])), n
+        assert_within(dw, *want["dweight"], f"dweight {n}")
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("n", [7, 300, 3001, 9001, 140001])
 def test_strides_alignment_and_in_place(lbp, n, dtype):
