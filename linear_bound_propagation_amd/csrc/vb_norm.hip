@@ -256,15 +256,13 @@ struct Grad {
   __device__ void sums(long long r, const GradRow<T, CH>& row, float& along, float& level, F&& f) const {
     along = level = 0.f;
     c.each([&](int k) {
-      float xh[EC], d[EC], wf[EC];
-      values(r, row, k, xh, d, wf);
-      c.mask(k, xh), c.mask(k, d), c.mask(k, wf);
+      float xh[EC], d[EC], g[EC];
+      values(r, row, k, xh, d, g);
 #pragma unroll
-      for (int e = 0; e < EC; ++e) {
-        const float g = d[e] * wf[e];
-        level += g;
-        along = fmaf(g, xh[e], along);
-      }
+      for (int e = 0; e < EC; ++e) g[e] *= d[e];
+      c.mask(k, xh), c.mask(k, d), c.mask(k, g);
+#pragma unroll
+      for (int e = 0; e < EC; ++e) level += g[e], along = fmaf(g[e], xh[e], along);
       f(k, xh, d);
     });
   }
@@ -283,12 +281,76 @@ struct Grad {
   }
 };
 
+// Floats of a part's row: its columns' sums start on 16-byte boundaries.
+__host__ __device__ inline int part_row(int n) { return (n + 3) / 4 * 4; }
+
+// dweight and dbias of few rows, or of rows too long for their sums to stay in registers: a
+// thread has a chunk of columns and every (WG / 32)th of the workgroup's rows, 32 chunks a
+// workgroup.
+constexpr int COLUMN_ROWS = 64;
+template <typename T, int WG>
+constexpr int column_words = 2 * (WG / 32) * (32 * Vec<T>::EC + 1);
+template <typename T, int WG>
+__device__ __forceinline__ void sum_columns(const vb_layer_norm_bwd& p, unsigned block, float* partial, float* words) {
+  typedef typename Vec<T>::type V;
+  constexpr int EC = Vec<T>::EC, U = 4, SIDE = WG / 32;
+  float(*red)[SIDE][32 * EC + 1] = (float(*)[SIDE][32 * EC + 1])words;
+  const unsigned across = (p.n + 32 * EC - 1) / (32 * EC);
+  const unsigned bx = block % across;
+  const long long by = block / across, m0 = by * COLUMN_ROWS, end = min(m0 + COLUMN_ROWS, (long long)p.rows);
+  if (m0 >= p.rows) return;  // the whole workgroup
+  const int c = threadIdx.x & 31, w = threadIdx.x >> 5, i0 = (bx * 32 + c) * EC;
+  float sw[EC], sb[EC];
+#pragma unroll
+  for (int e = 0; e < EC; ++e) sw[e] = sb[e] = 0.f;
+  if (i0 < p.n)
+    for (long long m = m0 + w; m < end; m += SIDE * U) {
+      V d[U], x[U];
+      float mean[U], rstd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long long r = m + SIDE * u;
+        d[u] = x[u] = V{};
+        mean[u] = rstd[u] = 0.f;
+        if (r >= end) continue;
+        d[u] = load_part((const T*)p.dy + r * p.ld_dy, i0, p.n);
+        if (p.dweight) {
+          x[u] = load_part((const T*)p.x + r * p.ld_x, i0, p.n);
+          mean[u] = p.mean[r], rstd[u] = p.rstd[r];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < EC; ++e) {
+          const float g = to_f32((T)d[u][e]);
+          sw[e] = fmaf(g, (to_f32((T)x[u][e]) - mean[u]) * rstd[u], sw[e]);
+          sb[e] += g;
+        }
+    }
+#pragma unroll
+  for (int e = 0; e < EC; ++e) red[0][w][c * EC + e] = sw[e], red[1][w][c * EC + e] = sb[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * EC; i += WG) {
+    const int k = i / (32 * EC), j = i % (32 * EC), col = bx * 32 * EC + j;
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < SIDE; ++q) s += red[k][q][j];
+    if (col >= p.n) continue;
+    if (partial) {
+      partial[(by * 2 + k) * part_row(p.n) + col] = s;
+    } else {
+      T* out = (T*)(k ? p.dbias : p.dweight);
+      if (out) out[col] = from_f32<T>(s);
+    }
+  }
+}
+
 template <typename T, int WG, int TH, int CH, bool RES>
-__global__ __launch_bounds__(WG) void norm_dx_kernel(vb_layer_norm_bwd p) {
+__device__ __forceinline__ void dx_rows(const vb_layer_norm_bwd& p, unsigned block, float (*red)[2]) {
   constexpr int PER = WG / TH;
   static_assert(PER == 1 || TH <= 64, "rows that end before others pass no barrier");
-  __shared__ float red[WG / 64][2];
-  const long long r = (long long)workgroup_number() * PER + threadIdx.x / TH;
+  const long long r = (long long)block * PER + threadIdx.x / TH;
   if (r >= p.rows) return;
   Grad<T, TH, CH, RES> g{p, {(int)threadIdx.x % TH, p.n}};
   GradRow<T, CH> row;
@@ -302,8 +364,20 @@ __global__ __launch_bounds__(WG) void norm_dx_kernel(vb_layer_norm_bwd p) {
   g.store(r, row, along * inv, level * inv);
 }
 
-// Floats of a part's row: its columns' sums start on 16-byte boundaries.
-__host__ __device__ inline int part_row(int n) { return (n + 3) / 4 * 4; }
+template <typename T, int WG, int TH, int CH, bool RES>
+__global__ __launch_bounds__(WG) void norm_dx_kernel(vb_layer_norm_bwd p) {
+  __shared__ float red[WG / 64][2];
+  dx_rows<T, WG, TH, CH, RES>(p, workgroup_number(), red);
+}
+
+// Few rows: the workgroups of dx, then those of dweight and dbias, of one launch (16 x 100 in
+// float32: 3.0 us, in two 5.5; 64 x 16384 in bf16 5.2 and 9.2).
+template <typename T, int WG, int TH, int CH, bool RES>
+__global__ __launch_bounds__(WG) void norm_few_kernel(vb_layer_norm_bwd p, unsigned row_blocks) {
+  __shared__ float words[column_words<T, WG>];
+  if (blockIdx.x < row_blocks) dx_rows<T, WG, TH, CH, RES>(p, blockIdx.x, (float(*)[2])words);
+  else sum_columns<T, WG>(p, blockIdx.x - row_blocks, nullptr, words);
+}
 
 // dx (DX) and the sums of dweight and dbias in one pass: a workgroup goes through the rows, WG / TH
 // at a time, and keeps its rows' sums in registers, two float32 per column.  A row is on its way
@@ -383,63 +457,10 @@ __global__ __launch_bounds__(WG) void norm_sums_kernel(vb_layer_norm_bwd p, floa
   });
 }
 
-// dweight and dbias of few rows, or of rows too long for their sums to stay in registers: a
-// thread has a chunk of columns and every eighth of the workgroup's rows, 32 chunks a workgroup.
-constexpr int COLUMN_ROWS = 64;
 template <typename T>
 __global__ __launch_bounds__(256) void norm_columns_kernel(vb_layer_norm_bwd p, float* partial) {
-  typedef typename Vec<T>::type V;
-  constexpr int EC = Vec<T>::EC, U = 4;
-  __shared__ float red[2][8][32 * EC + 1];
-  const unsigned across = (p.n + 32 * EC - 1) / (32 * EC), block = workgroup_number();
-  const unsigned bx = block % across;
-  const long long by = block / across, m0 = by * COLUMN_ROWS, end = min(m0 + COLUMN_ROWS, (long long)p.rows);
-  if (m0 >= p.rows) return;  // the whole workgroup
-  const int c = threadIdx.x & 31, w = threadIdx.x >> 5, i0 = (bx * 32 + c) * EC;
-  float sw[EC], sb[EC];
-#pragma unroll
-  for (int e = 0; e < EC; ++e) sw[e] = sb[e] = 0.f;
-  if (i0 < p.n)
-    for (long long m = m0 + w; m < end; m += 8 * U) {
-      V d[U], x[U];
-      float mean[U], rstd[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const long long r = m + 8 * u;
-        d[u] = x[u] = V{};
-        mean[u] = rstd[u] = 0.f;
-        if (r >= end) continue;
-        d[u] = load_part((const T*)p.dy + r * p.ld_dy, i0, p.n);
-        if (p.dweight) {
-          x[u] = load_part((const T*)p.x + r * p.ld_x, i0, p.n);
-          mean[u] = p.mean[r], rstd[u] = p.rstd[r];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < EC; ++e) {
-          const float g = to_f32((T)d[u][e]);
-          sw[e] = fmaf(g, (to_f32((T)x[u][e]) - mean[u]) * rstd[u], sw[e]);
-          sb[e] += g;
-        }
-    }
-#pragma unroll
-  for (int e = 0; e < EC; ++e) red[0][w][c * EC + e] = sw[e], red[1][w][c * EC + e] = sb[e];
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * EC; i += 256) {
-    const int k = i / (32 * EC), j = i % (32 * EC), col = bx * 32 * EC + j;
-    float s = 0.f;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) s += red[k][q][j];
-    if (col >= p.n) continue;
-    if (partial) {
-      partial[(by * 2 + k) * part_row(p.n) + col] = s;
-    } else {
-      T* out = (T*)(k ? p.dbias : p.dweight);
-      if (out) out[col] = from_f32<T>(s);
-    }
-  }
+  __shared__ float red[column_words<T, 256>];
+  sum_columns<T, 256>(p, workgroup_number(), partial, red);
 }
 
 // dweight and dbias from the parts, in their order: 64 columns per workgroup, in 16 sums of
@@ -511,7 +532,7 @@ long long groups_of(long long rows, int chunks) {
   return std::min<long long>((rows + per - 1) / per, SUM_GROUPS);
 }
 // By columns where sums do not stay in registers (or rows are less than a chunk), where one workgroup has all rows of a column
-// (64 x 16384 in bf16: 9.2 us, as parts 13.5), and where there is nearly a part for every row,
+// (64 x 16384 in bf16: 5.2 us, as parts 13.5), and where there is nearly a part for every row,
 // which costs more than reading the row twice (250 x 16384 in bf16: 15.0 against 21.3 us).
 bool by_columns(long long rows, int n, int es) {
   const int chunks = (n * es + 15) / 16;
@@ -541,45 +562,58 @@ hipError_t norm_sums(const vb_layer_norm_bwd& p, float* partial, unsigned parts,
   return norm_sums_rows<T, 1024, 1024, 2>(p, partial, parts, st);
 }
 
+// What norm_dx launches: dx, of few rows dweight and dbias, or both.
+enum Wanted { DX, COLUMNS, BOTH };
+
 template <typename T, int WG, int TH, int CH>
-hipError_t norm_dx_rows(const vb_layer_norm_bwd& p, hipStream_t st) {
+hipError_t norm_dx_rows(const vb_layer_norm_bwd& p, Wanted what, hipStream_t st) {
   constexpr int PER = WG / TH;
-  const dim3 grid = grid_of((p.rows + PER - 1) / PER);
-  if (p.dresidual) norm_dx_kernel<T, WG, TH, CH, true><<<grid, WG, 0, st>>>(p);
-  else norm_dx_kernel<T, WG, TH, CH, false><<<grid, WG, 0, st>>>(p);
+  const long long blocks = what == COLUMNS ? 0 : (p.rows + PER - 1) / PER;
+  if (what == DX) {
+    if (p.dresidual) norm_dx_kernel<T, WG, TH, CH, true><<<grid_of(blocks), WG, 0, st>>>(p);
+    else norm_dx_kernel<T, WG, TH, CH, false><<<grid_of(blocks), WG, 0, st>>>(p);
+  } else {
+    const unsigned all = (unsigned)blocks + (p.n + 32 * Vec<T>::EC - 1) / (32 * Vec<T>::EC);
+    if (p.dresidual) norm_few_kernel<T, WG, TH, CH, true><<<all, WG, 0, st>>>(p, (unsigned)blocks);
+    else norm_few_kernel<T, WG, TH, CH, false><<<all, WG, 0, st>>>(p, (unsigned)blocks);
+  }
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t norm_dx(const vb_layer_norm_bwd& p, hipStream_t st) {
+hipError_t norm_dx(const vb_layer_norm_bwd& p, Wanted what, hipStream_t st) {
   const int chunks = chunks_of<T>(p.n);
-  if (p.n < Vec<T>::EC) return norm_dx_rows<T, 256, 16, 0>(p, st);
-  if (chunks <= 16) return norm_dx_rows<T, 256, 16, 1>(p, st);
-  if (chunks <= 64) return norm_dx_rows<T, 256, 64, 1>(p, st);
-  if (chunks <= 128) return norm_dx_rows<T, 128, 128, 1>(p, st);
-  if (chunks <= 256) return norm_dx_rows<T, 256, 256, 1>(p, st);
-  if (chunks <= 512) return norm_dx_rows<T, 256, 256, 2>(p, st);
-  if (chunks <= 1024) return norm_dx_rows<T, 512, 512, 2>(p, st);
-  if (chunks <= 2048) return norm_dx_rows<T, 1024, 1024, 2>(p, st);
-  if (chunks <= 4096) return norm_dx_rows<T, 1024, 1024, 4>(p, st);
-  return norm_dx_rows<T, 1024, 1024, 0>(p, st);
+  if (p.n < Vec<T>::EC) return norm_dx_rows<T, 256, 16, 0>(p, what, st);
+  if (chunks <= 16) return norm_dx_rows<T, 256, 16, 1>(p, what, st);
+  if (chunks <= 64) return norm_dx_rows<T, 256, 64, 1>(p, what, st);
+  if (chunks <= 128) return norm_dx_rows<T, 128, 128, 1>(p, what, st);
+  if (chunks <= 256) return norm_dx_rows<T, 256, 256, 1>(p, what, st);
+  if (chunks <= 512) return norm_dx_rows<T, 256, 256, 2>(p, what, st);
+  if (chunks <= 1024) return norm_dx_rows<T, 512, 512, 2>(p, what, st);
+  if (chunks <= 2048) return norm_dx_rows<T, 1024, 1024, 2>(p, what, st);
+  if (chunks <= 4096) return norm_dx_rows<T, 1024, 1024, 4>(p, what, st);
+  return norm_dx_rows<T, 1024, 1024, 0>(p, what, st);
 }
 
 template <typename T>
 hipError_t norm_grad_typed(const vb_layer_norm_bwd& p, float* ws, hipStream_t st) {
-  if (!p.dweight && !p.dbias) return norm_dx<T>(p, st);
+  if (!p.dweight && !p.dbias) return norm_dx<T>(p, DX, st);
   const long long parts = parts_of(p.rows, p.n, sizeof(T));
+  if (parts == 1 && by_columns(p.rows, p.n, sizeof(T))) {
+    if (p.dx && p.dx != p.dy) return norm_dx<T>(p, BOTH, st);
+    if (const hipError_t e = norm_dx<T>(p, COLUMNS, st)) return e;  // before dx, which may lie over dy
+    return p.dx ? norm_dx<T>(p, DX, st) : hipSuccess;
+  }
   if (!by_columns(p.rows, p.n, sizeof(T))) {
     if (const hipError_t e = norm_sums<T>(p, ws, (unsigned)parts, st)) return e;
   } else {
-    // before dx, which may lie over dy
+    // before dx here too
     const long long blocks = parts * ((p.n + 32 * Vec<T>::EC - 1) / (32 * Vec<T>::EC));
     if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    norm_columns_kernel<T><<<grid_of(blocks), 256, 0, st>>>(p, parts > 1 ? ws : nullptr);
+    norm_columns_kernel<T><<<grid_of(blocks), 256, 0, st>>>(p, ws);
     if (const hipError_t e = hipGetLastError()) return e;
     if (p.dx)
-      if (const hipError_t e = norm_dx<T>(p, st)) return e;
-    if (parts == 1) return hipSuccess;
+      if (const hipError_t e = norm_dx<T>(p, DX, st)) return e;
   }
   norm_sum_kernel<T><<<(p.n + 63) / 64 * 2, 1024, 0, st>>>(ws, (int)parts, p.n, (T*)p.dweight, (T*)p.dbias);
   return hipGetLastError();
