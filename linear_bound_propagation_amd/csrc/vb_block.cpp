@@ -36,6 +36,7 @@ GatedPlan plan_gated(const vb_gated_linear_fwd& p) {
   d.bias = p.bias, d.act = p.act;
   d.out = p.y, d.ld_out = p.ld_y, d.pre = p.pre, d.ld_pre = p.ld_pre;
   if (p.rows == 0 || product_is_narrow(d, p.dtype)) return f;
+  d.tiled = true;
   const size_t row = chunked_row(p.n_in, p.dtype);
   if (!is_chunked(p.x, p.ld_x, p.n_in, p.dtype)) f.x.take(f.total, p.rows * row);
   if (!is_chunked(p.weight, p.ld_w, p.n_in, p.dtype)) f.w.take(f.total, 2 * (size_t)p.n_out * row);

@@ -1494,17 +1494,35 @@ size_t pair_bytes(const Pair& pair, const Product& p, int splits) {
   return pair.tile && splits > 1 ? (size_t)splits * p.M * partial_row(p) * 4 : 0;
 }
 
+// Long rows of few weights, gated: a split reduction has more wavefronts than the narrow kernel,
+// whose time grows with the reduction and the rows, and with the weights only later.  Weights off
+// 16-byte boundaries have to be copied for the split, about their reading and writing again; the
+// narrow kernel reads those in place, 16-bit ones with more work for x.  In us, narrow | split: 16 x
+// 8192 -> 300 in bf16 16.6 | 9.4, 7 x 8192 -> 2048 15.1 | 17.6; float32 7 x 4096 -> 300 13.9 | 11.6, -> 2048
+// 15.6 | 23.5, 16 x 12000 -> 1000 50 | 33, 31 x 2048 -> 300 13.4 | 10.2; off boundaries float32 7 x 4097 -> 300
+// 12.3 | 18.6, 7 x 8191 -> 150 21.5 | 19.7, -> 2048 35 | 85, 31 x 2049 -> 300 11.7 | 14.5, 31 x 5001 -> 150
+// 23.4 | 17.9; bf16 16 x 8193 -> 600 28.8 | 19.5, -> 2048 30 | 40.  (Over 404 such products 0.6 % longer
+// than the better of both on average, 30 % at worst; always split 15 %, never 42 %.)
+namespace {
+
+bool split_is_faster(const Product& p, int dtype) {
+  const double k = p.K / 1000.0, rows = p.M > 16 ? p.M + 8.0 : p.M, mb = 2e-6 * p.N * p.K * elem_size(dtype);
+  if (!is_chunked(p.b, p.ldb, p.K, dtype))
+    return dtype == VB_F32 ? k * (2.2 + 0.05 * rows) > 14.5 + 0.5 * mb : k * (1.4 + 0.12 * rows) > 12.5 + 0.42 * mb;
+  if (p.M > 16) return true;
+  return dtype == VB_F32 ? k * (2.3 + 0.07 * rows) > 11.5 + 0.16 * mb : k * (1.0 + 0.04 * rows) > 9.5 + 0.1 * mb;
+}
+
+}  // namespace
+
 // Up to 16 rows, and up to 32 where the weights are few (24 x 1024 -> 1024 in bf16: 5.2
 // against 7.7 us; 24 x 4096 -> 4096: 14.7 against 13.2) or long and many (32 x 4096 ->
 // 16384: 34 against 37, float32 63 against 72; 32 x 1024 -> 65536: 36 against 31).
 bool product_is_narrow(const Product& p, int dtype) {
-  if (p.across_a || p.across_b) return false;
+  if (p.across_a || p.across_b || p.tiled) return false;
   const long long row = p.K * (long long)elem_size(dtype);
   const int n = weight_rows_of(p);
-  // long rows of few weights: a split reduction has more wavefronts (gated, 16 x 8192 -> 300 in
-  // bf16 16.6 against 9.6 us, 31 x 2048 -> 300 in float32 13.3 and 10.3; 16 x 2048 -> 300 in bf16
-  // 6.1 and 8.0)
-  if (p.gated && p.M > 4 && p.N <= 2048 && row * (p.M > 16 ? 2 : 1) >= 16384) return false;
+  if (p.gated && p.M > 4 && p.N <= 2048 && row * (p.M > 16 ? 2 : 1) >= 16384 && split_is_faster(p, dtype)) return false;
   return p.M <= 16 || (p.M <= 32 && (n * row <= 8 << 20 || (n >= 12800 && row >= 8192)));
 }
 

@@ -74,6 +74,7 @@ struct Product {
   // gated (neither operand across, one pass, no res): B has 2 N rows, bias 2 N numbers, pre 2 N
   // columns; out(m, n) = act(v(m, n)) v(m, N + n)
   bool gated;
+  bool tiled;  // operands that were chosen, or copied, for tiles: not narrow
   // epilogue: v = sum + bias[n] + res[m][n]; pre = v; out = act(v)
   const void* bias;
   const void* res;

@@ -1,0 +1,44 @@
+"""Which way the layers' products and layer norm's sums take, seen from the workspaces that the
+library asks for (no GPU: fake addresses, nothing is dereferenced)."""
+import ctypes
+
+import pytest
+
+from helpers import ensure_built
+
+ensure_built()
+import linear_bound_propagation_amd as lbp  # noqa: E402
+from linear_bound_propagation_amd import train  # noqa: E402
+
+L = lbp.lib()
+F32, BF16, F16 = 0, 1, 2
+
+
+def size(fn, *args):
+    out = ctypes.c_size_t(0)
+    assert fn(*args, ctypes.byref(out)) == 0
+    return out.value
+
+
+def gated(rows, n_in, n_out, dtype, ld_w=None, weight=1 << 20):
+    return size(L.vb_gated_linear_forward_workspace, ctypes.byref(train.vb_gated_linear_fwd(
+        rows=rows, n_in=n_in, n_out=n_out, dtype=dtype, act=3, x=4096, ld_x=n_in, weight=weight, ld_w=ld_w or n_in)))
+
+
+@pytest.mark.parametrize("rows, n_in, n_out, dtype", [
+    (7, 8191, 2048, F32), (16, 8191, 2048, F32), (5, 5001, 1000, F32), (7, 4097, 300, F32), (31, 2049, 300, F32),
+    (7, 8193, 2048, BF16), (16, 8193, 2048, F16), (5, 12001, 1500, BF16)])
+def test_gated_few_rows_do_not_copy_many_weights(rows, n_in, n_out, dtype):
+    """Weights off 16-byte boundaries, of a size whose copy costs more than a split reduction gains."""
+    weights = 2 * n_out * n_in * (4 if dtype == F32 else 2)
+    assert gated(rows, n_in, n_out, dtype) < weights // 8
+    # rows that end on boundaries but start off them
+    even = n_in // 8 * 8
+    assert gated(rows, even, n_out, dtype, ld_w=even + 1) < weights // 8
+    assert gated(rows, even, n_out, dtype, weight=(1 << 20) + 4) < weights // 8
+
+
+def test_gated_few_rows_split_long_reductions():
+    """Few weights: the reduction is split, and its parts are in the workspace."""
+    for rows, n_in, n_out, dtype in ((16, 8192, 300, BF16), (7, 8192, 300, F32), (31, 2048, 300, F32), (16, 8193, 300, BF16)):
+        assert gated(rows, n_in, n_out, dtype) >= 2 * rows * 2 * n_out * 4, (rows, n_in, n_out)
