@@ -1457,9 +1457,12 @@ size_t tiling_bytes(const Tiling& t, const Product& p) {
 // the first one ends, and their parts' sums another; or none where launches of their own are
 // faster by the same model (each of those past the first: 2 us).  Together | apart, with g and
 // dbias: 1024 x 1024 -> 1024 in bf16 19.4 | 23.7 us (64-wide tiles), float32 44 | 52; 1024 x 2048
-// -> 2048 34 | 41 (128); 4096 x 2048 -> 2048 96 | 92; split (728 x 49 -> 780 in float16, two-part g) 16 | 28.  Each reduction is split as the
-// product's own launch would split it, so that a gradient has the same bits alone as with the
-// other.
+// -> 2048 34 | 41 (128); 4096 x 2048 -> 2048 96 | 92; split (728 x 49 -> 780 in float16, two-part g)
+// 16 | 28.  Each reduction is split as the product's own launch would split it, so that a gradient has
+// the same bits alone as with the other.  In float32 a split pair takes 64-wide tiles or none: the
+// model, which counts 128-wide ones at their full rate, finds those faster, and they are not (1121 x
+// 2097 -> 14556: 128-wide 1193 us, 64-wide 1126, apart 1150; 622 x 1419 -> 2 x 4848 355, 315, 327; of 31
+// drawn 29 are slower by up to 14 %, two faster by 1 and 4 %; in 16 bits 128-wide ones gain up to 18 %).
 Pair choose_pair(const Product& dx, const Product& dw, int dtype) {
   const Tiling x = choose_tiling(dtype, dx), w = choose_tiling(dtype, dw);
   auto run_of = [&](const Product& p, int splits) { return (double)((steps_of(p.K, dtype) + splits - 1) / splits) * p.passes; };
@@ -1474,6 +1477,7 @@ Pair choose_pair(const Product& dx, const Product& dw, int dtype) {
   const Kind* kinds = dtype == VB_F32 ? k32 + 1 : k16 + 2;
   for (int k = 0; k < 2; ++k) {
     const Kind& c = kinds[k];
+    if (dtype == VB_F32 && join > 0.0 && c.bm > 64) continue;
     auto tiles = [&](const Product& p, int s) { return (double)((p.M + c.bm - 1) / c.bm) * ((p.N + c.bn - 1) / c.bn) * s; };
     const double n = tiles(first, splits), n2 = tiles(second, splits2);
     double us;

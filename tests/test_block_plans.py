@@ -1,10 +1,13 @@
 """Which way the layers' products and layer norm's sums take, seen from the workspaces that the
 library asks for (no GPU: fake addresses, nothing is dereferenced)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 
-from helpers import ensure_built
+from helpers import ROOT, ensure_built
 
 ensure_built()
 import linear_bound_propagation_amd as lbp  # noqa: E402
@@ -42,3 +45,19 @@ def test_gated_few_rows_split_long_reductions():
     """Few weights: the reduction is split, and its parts are in the workspace."""
     for rows, n_in, n_out, dtype in ((16, 8192, 300, BF16), (7, 8192, 300, F32), (31, 2048, 300, F32), (16, 8193, 300, BF16)):
         assert gated(rows, n_in, n_out, dtype) >= 2 * rows * 2 * n_out * 4, (rows, n_in, n_out)
+
+
+def test_tiles_of_both_backward_products(tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    package = os.path.join(ROOT, "linear_bound_propagation_amd")
+    exe = str(tmp_path / "plan_checks")
+    res = subprocess.run([gxx, "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include",
+                          "-I", os.path.join(ROOT, "include"), "-I", os.path.join(package, "csrc"),
+                          os.path.join(ROOT, "tests", "sanitize", "plan_checks.cpp"), lbp.LIB_PATH,
+                          "-Wl,-rpath," + package, "-L/opt/rocm/lib", "-Wl,-rpath,/opt/rocm/lib", "-lamdhip64", "-o", exe],
+                         capture_output=True, text=True)
+    assert res.returncode == 0, res.stdout + res.stderr
+    run = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert run.returncode == 0 and " 0 failure(s)" in run.stdout, run.stdout
