@@ -284,22 +284,22 @@ struct Grad {
 // Floats of a part's row: its columns' sums start on 16-byte boundaries.
 __host__ __device__ inline int part_row(int n) { return (n + 3) / 4 * 4; }
 
-// dweight and dbias of few rows, or of rows too long for their sums to stay in registers: a
-// thread has a chunk of columns and every (WG / 32)th of the workgroup's rows, 32 chunks a
-// workgroup.
+// dweight and dbias of few rows, or of rows too long for their sums to stay in registers or
+// shorter than a chunk: a thread has a chunk of columns and every (WG / ACROSS)th of the
+// workgroup's part_rows rows, ACROSS chunks a workgroup (one, of rows shorter than that).
 constexpr int COLUMN_ROWS = 64;
-template <typename T, int WG>
-constexpr int column_words = 2 * (WG / 32) * (32 * Vec<T>::EC + 1);
-template <typename T, int WG>
-__device__ __forceinline__ void sum_columns(const vb_layer_norm_bwd& p, unsigned block, float* partial, float* words) {
+template <typename T, int WG, int ACROSS>
+constexpr int column_words = 2 * (WG / ACROSS) * (ACROSS * Vec<T>::EC + 1);
+template <typename T, int WG, int ACROSS>
+__device__ __forceinline__ void sum_columns(const vb_layer_norm_bwd& p, unsigned block, int part_rows, float* partial, float* words) {
   typedef typename Vec<T>::type V;
-  constexpr int EC = Vec<T>::EC, U = 4, SIDE = WG / 32;
-  float(*red)[SIDE][32 * EC + 1] = (float(*)[SIDE][32 * EC + 1])words;
-  const unsigned across = (p.n + 32 * EC - 1) / (32 * EC);
+  constexpr int EC = Vec<T>::EC, U = 4, SIDE = WG / ACROSS, COLS = ACROSS * EC;
+  float(*red)[SIDE][COLS + 1] = (float(*)[SIDE][COLS + 1])words;
+  const unsigned across = (p.n + COLS - 1) / COLS;
   const unsigned bx = block % across;
-  const long long by = block / across, m0 = by * COLUMN_ROWS, end = min(m0 + COLUMN_ROWS, (long long)p.rows);
+  const long long by = block / across, m0 = by * part_rows, end = min(m0 + part_rows, (long long)p.rows);
   if (m0 >= p.rows) return;  // the whole workgroup
-  const int c = threadIdx.x & 31, w = threadIdx.x >> 5, i0 = (bx * 32 + c) * EC;
+  const int c = threadIdx.x % ACROSS, w = threadIdx.x / ACROSS, i0 = (bx * ACROSS + c) * EC;
   float sw[EC], sb[EC];
 #pragma unroll
   for (int e = 0; e < EC; ++e) sw[e] = sb[e] = 0.f;
@@ -331,10 +331,10 @@ __device__ __forceinline__ void sum_columns(const vb_layer_norm_bwd& p, unsigned
 #pragma unroll
   for (int e = 0; e < EC; ++e) red[0][w][c * EC + e] = sw[e], red[1][w][c * EC + e] = sb[e];
   __syncthreads();
-  for (int i = threadIdx.x; i < 64 * EC; i += WG) {
-    const int k = i / (32 * EC), j = i % (32 * EC), col = bx * 32 * EC + j;
+  for (int i = threadIdx.x; i < 2 * COLS; i += WG) {
+    const int k = i / COLS, j = i % COLS, col = bx * COLS + j;
     float s = 0.f;
-#pragma unroll
+#pragma unroll 32
     for (int q = 0; q < SIDE; ++q) s += red[k][q][j];
     if (col >= p.n) continue;
     if (partial) {
@@ -374,9 +374,9 @@ __global__ __launch_bounds__(WG) void norm_dx_kernel(vb_layer_norm_bwd p) {
 // float32: 3.0 us, in two 5.5; 64 x 16384 in bf16 5.2 and 9.2).
 template <typename T, int WG, int TH, int CH, bool RES>
 __global__ __launch_bounds__(WG) void norm_few_kernel(vb_layer_norm_bwd p, unsigned row_blocks) {
-  __shared__ float words[column_words<T, WG>];
+  __shared__ float words[column_words<T, WG, 32>];
   if (blockIdx.x < row_blocks) dx_rows<T, WG, TH, CH, RES>(p, blockIdx.x, (float(*)[2])words);
-  else sum_columns<T, WG>(p, blockIdx.x - row_blocks, nullptr, words);
+  else sum_columns<T, WG, 32>(p, blockIdx.x - row_blocks, COLUMN_ROWS, nullptr, words);
 }
 
 // dx (DX) and the sums of dweight and dbias in one pass: a workgroup goes through the rows, WG / TH
@@ -457,10 +457,10 @@ __global__ __launch_bounds__(WG) void norm_sums_kernel(vb_layer_norm_bwd p, floa
   });
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void norm_columns_kernel(vb_layer_norm_bwd p, float* partial) {
-  __shared__ float red[column_words<T, 256>];
-  sum_columns<T, 256>(p, workgroup_number(), partial, red);
+template <typename T, int ACROSS>
+__global__ __launch_bounds__(256) void norm_columns_kernel(vb_layer_norm_bwd p, int part_rows, float* partial) {
+  __shared__ float red[column_words<T, 256, ACROSS>];
+  sum_columns<T, 256, ACROSS>(p, workgroup_number(), part_rows, partial, red);
 }
 
 // dweight and dbias from the parts, in their order: 64 columns per workgroup, in 16 sums of
@@ -524,8 +524,7 @@ hipError_t norm_typed(const vb_layer_norm_fwd& p, hipStream_t st) {
 }
 
 // Parts of the sums: workgroups that keep those of their rows, one a CU, as each part is
-// written and read again (8192 x 4096 in bf16 with 512 parts of 512 threads: 68 against 63 us); or
-// COLUMN_ROWS rows each.
+// written and read again (8192 x 4096 in bf16 with 512 parts of 512 threads: 68 against 63 us).
 constexpr int SUM_GROUPS = 256, SUM_CHUNKS = 2048;
 long long groups_of(long long rows, int chunks) {
   const int per = chunks <= 16 ? 64 : chunks <= 64 ? 16 : chunks <= 128 ? 8 : chunks <= 256 ? 4 : chunks <= 512 ? 2 : 1;
@@ -538,8 +537,19 @@ bool by_columns(long long rows, int n, int es) {
   const int chunks = (n * es + 15) / 16;
   return n * es < 16 || chunks > SUM_CHUNKS || rows <= COLUMN_ROWS || groups_of(rows, chunks) * 4 > rows * es;
 }
+// Rows of a part by columns: COLUMN_ROWS, or four of each thread where a row is less than a chunk;
+// more where there would be over COLUMN_PARTS parts, each of whose numbers is added to a float32
+// sum (2^24 x 7 in float16, dx and all: with a part per 64 rows 6.6 ms, so 3.0).
+constexpr int COLUMN_PARTS = 1024;
+int column_rows(long long rows, int n, int es) {
+  const int unit = n * es < 16 ? 1024 : COLUMN_ROWS;
+  const long long parts = (rows + unit - 1) / unit;
+  return unit * (int)((parts + COLUMN_PARTS - 1) / COLUMN_PARTS);
+}
 long long parts_of(long long rows, int n, int es) {
-  return by_columns(rows, n, es) ? (rows + COLUMN_ROWS - 1) / COLUMN_ROWS : groups_of(rows, (n * es + 15) / 16);
+  if (!by_columns(rows, n, es)) return groups_of(rows, (n * es + 15) / 16);
+  const int per = column_rows(rows, n, es);
+  return (rows + per - 1) / per;
 }
 
 template <typename T, int WG, int TH, int CH>
@@ -599,7 +609,7 @@ template <typename T>
 hipError_t norm_grad_typed(const vb_layer_norm_bwd& p, float* ws, hipStream_t st) {
   if (!p.dweight && !p.dbias) return norm_dx<T>(p, DX, st);
   const long long parts = parts_of(p.rows, p.n, sizeof(T));
-  if (parts == 1 && by_columns(p.rows, p.n, sizeof(T))) {
+  if (p.rows <= COLUMN_ROWS) {
     if (p.dx && p.dx != p.dy) return norm_dx<T>(p, BOTH, st);
     if (const hipError_t e = norm_dx<T>(p, COLUMNS, st)) return e;  // before dx, which may lie over dy
     return p.dx ? norm_dx<T>(p, DX, st) : hipSuccess;
@@ -608,9 +618,9 @@ hipError_t norm_grad_typed(const vb_layer_norm_bwd& p, float* ws, hipStream_t st
     if (const hipError_t e = norm_sums<T>(p, ws, (unsigned)parts, st)) return e;
   } else {
     // before dx here too
-    const long long blocks = parts * ((p.n + 32 * Vec<T>::EC - 1) / (32 * Vec<T>::EC));
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    norm_columns_kernel<T><<<grid_of(blocks), 256, 0, st>>>(p, ws);
+    const int per = column_rows(p.rows, p.n, sizeof(T));
+    if (p.n < Vec<T>::EC) norm_columns_kernel<T, 1><<<(unsigned)parts, 256, 0, st>>>(p, per, ws);
+    else norm_columns_kernel<T, 32><<<grid_of(parts * ((p.n + 32 * Vec<T>::EC - 1) / (32 * Vec<T>::EC))), 256, 0, st>>>(p, per, ws);
     if (const hipError_t e = hipGetLastError()) return e;
     if (p.dx)
       if (const hipError_t e = norm_dx<T>(p, DX, st)) return e;

@@ -61,3 +61,15 @@ def test_tiles_of_both_backward_products(tmp_path):
     assert res.returncode == 0, res.stdout + res.stderr
     run = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert run.returncode == 0 and " 0 failure(s)" in run.stdout, run.stdout
+
+
+def norm_sums(rows, n, dtype):
+    """Parts of dweight and dbias: two float32 rows each, rounded up to 16 bytes."""
+    return size(L.vb_layer_norm_backward_workspace, rows, n, dtype) // (8 * ((n + 3) // 4 * 4))
+
+
+def test_parts_of_layer_norm_sums_are_bounded():
+    """Each part is a term of a float32 sum.  (The workspace is rounded up to 256 bytes, at most eight parts.)"""
+    for rows in (2 ** 20, 2 ** 27, 2 ** 31 - 1):
+        for n, dtype in ((1, F32), (3, F32), (7, F16), (7, BF16), (100, F32), (4096, BF16), (20000, F32), (2 ** 20, F16)):
+            assert norm_sums(rows, n, dtype) <= 1024 + 8, (rows, n, dtype)
