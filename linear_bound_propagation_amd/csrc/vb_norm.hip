@@ -530,12 +530,18 @@ long long groups_of(long long rows, int chunks) {
   const int per = chunks <= 16 ? 64 : chunks <= 64 ? 16 : chunks <= 128 ? 8 : chunks <= 256 ? 4 : chunks <= 512 ? 2 : 1;
   return std::min<long long>((rows + per - 1) / per, SUM_GROUPS);
 }
-// By columns where sums do not stay in registers (or rows are less than a chunk), where one workgroup has all rows of a column
-// (64 x 16384 in bf16: 5.2 us, as parts 13.5), and where there is nearly a part for every row,
-// which costs more than reading the row twice (250 x 16384 in bf16: 15.0 against 21.3 us).
+// By columns where sums do not stay in registers (or rows are less than a chunk), and where one
+// workgroup has all rows of a column (64 x 16384 in bf16: 5.2 us, as parts 13.2; 33 x 2001 in float16 5.5
+// and 7.3).  Between those, of long rows that end on a chunk's boundary (a row's odd end takes a
+// workgroup loads of single elements: 200 x 6001 in bf16 15.9 us, as parts 14.0), where reading the rows
+// twice costs less than a part for nearly every row: us as parts | by columns, 16 bits at 8192 70 rows
+// 9.6 | 10.5, 100 11.0 | 10.5, 256 16.8 | 11.8, 512 17.4 | 15.7, 640 16.8 | 18.2; at 16384 128 17.7 | 12.4,
+// 512 25.7 | 24.1, 768 30.0 | 31.9; float32 at 4096 128 7.6 | 9.4, 200 10.5 | 9.9, 300 11.3 | 10.9, 400 11.7 |
+// 12.0; at 8192 70 9.3 | 9.9, 256 16.6 | 14.0, 384 17.9 | 18.0; rows of 8 KB and less the same or slower.
 bool by_columns(long long rows, int n, int es) {
   const int chunks = (n * es + 15) / 16;
-  return n * es < 16 || chunks > SUM_CHUNKS || rows <= COLUMN_ROWS || groups_of(rows, chunks) * 4 > rows * es;
+  if (n * es < 16 || chunks > SUM_CHUNKS || rows <= COLUMN_ROWS) return true;
+  return chunks > 512 && n * es % 16 == 0 && rows * n > 700000 && rows * es <= 1100;
 }
 // Rows of a part by columns: COLUMN_ROWS, or four of each thread where a row is less than a chunk;
 // more where there would be over COLUMN_PARTS parts, each of whose numbers is added to a float32

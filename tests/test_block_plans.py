@@ -73,3 +73,12 @@ def test_parts_of_layer_norm_sums_are_bounded():
     for rows in (2 ** 20, 2 ** 27, 2 ** 31 - 1):
         for n, dtype in ((1, F32), (3, F32), (7, F16), (7, BF16), (100, F32), (4096, BF16), (20000, F32), (2 ** 20, F16)):
             assert norm_sums(rows, n, dtype) <= 1024 + 8, (rows, n, dtype)
+
+
+@pytest.mark.parametrize("rows, n, dtype, columns", [
+    (64, 8192, BF16, True), (70, 8192, BF16, False), (256, 8192, F16, True), (512, 16384, BF16, True), (640, 8192, BF16, False),
+    (100, 6001, BF16, False), (200, 6001, F32, False), (256, 4096, BF16, False), (128, 4096, F32, False), (256, 8192, F32, True),
+    (200, 5000, F32, True), (400, 8192, F32, False), (2048, 8192, BF16, False), (300, 8193, F32, True)])
+def test_way_of_layer_norm_sums(rows, n, dtype, columns):
+    """By columns in parts of 64 rows, or a part per workgroup of rows."""
+    assert (norm_sums(rows, n, dtype) <= (rows + 63) // 64) == columns
