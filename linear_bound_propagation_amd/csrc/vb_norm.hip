@@ -128,18 +128,32 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return (row(0) + row(16)) + (row(32) + row(48));
 }
 
-// Sums of a and b over the TH threads of a row, given to all of them; red: two words per
-// wavefront, of two sets in turn, so that one barrier does (all of the workgroup's threads).
+// Sums of a and b over the TH threads of a row, given to all of them in a[0] and b[0]; red: two
+// words per wavefront, of two sets in turn, so that one barrier does (all of the workgroup's
+// threads).  S numbers of a thread are added as those of S TH threads would be.
+template <int TH, int S>
+__device__ __forceinline__ void sum_row(float (&a)[S], float (&b)[S], float (*red)[2]) {
+  constexpr int W = TH / 64;
+  static_assert(S == 1 || W >= 1, "numbers of whole wavefronts");
+#pragma unroll
+  for (int s = 0; s < S; ++s) a[s] = sum_lanes<TH == 16 ? 16 : 64>(a[s]), b[s] = sum_lanes<TH == 16 ? 16 : 64>(b[s]);
+  if constexpr (S * W > 1) {
+    const int wave = threadIdx.x >> 6, row = wave / W;
+    red += row * S * W;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if ((threadIdx.x & 63) == 0) red[s * W + wave - row * W][0] = a[s], red[s * W + wave - row * W][1] = b[s];
+    __syncthreads();
+    a[0] = red[0][0], b[0] = red[0][1];
+#pragma unroll
+    for (int i = 1; i < S * W; ++i) a[0] += red[i][0], b[0] += red[i][1];
+  }
+}
 template <int TH>
 __device__ __forceinline__ void sum_row(float& a, float& b, float (*red)[2]) {
-  a = sum_lanes<TH == 16 ? 16 : 64>(a), b = sum_lanes<TH == 16 ? 16 : 64>(b);
-  if (TH <= 64) return;
-  const int wave = threadIdx.x >> 6, first = wave / (TH / 64) * (TH / 64);
-  if ((threadIdx.x & 63) == 0) red[wave][0] = a, red[wave][1] = b;
-  __syncthreads();
-  a = red[first][0], b = red[first][1];
-#pragma unroll
-  for (int i = 1; i < TH / 64; ++i) a += red[first + i][0], b += red[first + i][1];
+  float x[1] = {a}, y[1] = {b};
+  sum_row<TH, 1>(x, y, red);
+  a = x[0], b = y[0];
 }
 
 // The mean is the row's first element and the mean of the differences from it, so that it is
@@ -251,18 +265,20 @@ struct Grad {
       wf[e] = to_f32((T)wv[e]);
     }
   }
-  // f(k, xh, dy) of each chunk beside the row's two sums
-  template <typename F>
-  __device__ void sums(long long r, const GradRow<T, CH>& row, float& along, float& level, F&& f) const {
-    along = level = 0.f;
+  // f(k, xh, dy) of each chunk beside the row's two sums (S > 1: of chunk k in number k)
+  template <int S, typename F>
+  __device__ void sums(long long r, const GradRow<T, CH>& row, float (&along)[S], float (&level)[S], F&& f) const {
+#pragma unroll
+    for (int s = 0; s < S; ++s) along[s] = level[s] = 0.f;
     c.each([&](int k) {
+      const int s = S > 1 ? k : 0;
       float xh[EC], d[EC], g[EC];
       values(r, row, k, xh, d, g);
 #pragma unroll
       for (int e = 0; e < EC; ++e) g[e] *= d[e];
       c.mask(k, xh), c.mask(k, d), c.mask(k, g);
 #pragma unroll
-      for (int e = 0; e < EC; ++e) level += g[e], along = fmaf(g[e], xh[e], along);
+      for (int e = 0; e < EC; ++e) level[s] += g[e], along[s] = fmaf(g[e], xh[e], along[s]);
       f(k, xh, d);
     });
   }
@@ -346,9 +362,13 @@ __device__ __forceinline__ void sum_columns(const vb_layer_norm_bwd& p, unsigned
   }
 }
 
+// norm_sums_kernel has 512 threads for the rows that 256 with two chunks each have here: their sums
+// are added in its order, so that dx has the same bits without dweight and dbias.
+template <int TH, int CH>
+constexpr int sums_apart = TH == 256 && CH == 2 ? 2 : 1;
 template <typename T, int WG, int TH, int CH, bool RES>
 __device__ __forceinline__ void dx_rows(const vb_layer_norm_bwd& p, unsigned block, float (*red)[2]) {
-  constexpr int PER = WG / TH;
+  constexpr int PER = WG / TH, S = sums_apart<TH, CH>;
   static_assert(PER == 1 || TH <= 64, "rows that end before others pass no barrier");
   const long long r = (long long)block * PER + threadIdx.x / TH;
   if (r >= p.rows) return;
@@ -356,17 +376,17 @@ __device__ __forceinline__ void dx_rows(const vb_layer_norm_bwd& p, unsigned blo
   GradRow<T, CH> row;
   g.load(r, row);
   g.load_weight();
-  float along, level;
+  float along[S], level[S];
   g.sums(r, row, along, level, [](int, const float*, const float*) {});
-  sum_row<TH>(along, level, red);
+  sum_row<TH, S>(along, level, red);
   if constexpr (CH > 0) forget(row.x), forget(row.dy), forget(g.w);
   const float inv = 1.f / (float)p.n;
-  g.store(r, row, along * inv, level * inv);
+  g.store(r, row, along[0] * inv, level[0] * inv);
 }
 
 template <typename T, int WG, int TH, int CH, bool RES>
 __global__ __launch_bounds__(WG) void norm_dx_kernel(vb_layer_norm_bwd p) {
-  __shared__ float red[WG / 64][2];
+  __shared__ float red[WG / 64 * sums_apart<TH, CH>][2];
   dx_rows<T, WG, TH, CH, RES>(p, workgroup_number(), red);
 }
 
@@ -407,7 +427,7 @@ __global__ __launch_bounds__(WG) void norm_sums_kernel(vb_layer_norm_bwd p, floa
   for (long long r0 = first; r0 < p.rows; r0 += step) {
     const long long r = r0 + side;
     g.load(min(r + AHEAD * step, p.rows - 1), row[AHEAD]);
-    float along, level;
+    float along[1], level[1];
     g.sums(r, row[0], along, level, [&](int k, const float* xh, const float* d) {
 #pragma unroll
       for (int e = 0; e < EC; ++e) {
@@ -418,10 +438,10 @@ __global__ __launch_bounds__(WG) void norm_sums_kernel(vb_layer_norm_bwd p, floa
       }
     });
     if (DX) {
-      sum_row<TH>(along, level, red[set]);
+      sum_row<TH, 1>(along, level, red[set]);
       set ^= 1;
       forget(row[0].x), forget(row[0].dy), forget(g.w);
-      if (r < p.rows) g.store(r, row[0], along * inv, level * inv);
+      if (r < p.rows) g.store(r, row[0], along[0] * inv, level[0] * inv);
     }
     forget(g.w);
 #pragma unroll

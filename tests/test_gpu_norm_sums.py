@@ -1,8 +1,10 @@
-"""dweight and dbias of layer norm over very many rows."""
+"""dweight and dbias of layer norm: each way that they are summed, and very many rows."""
 import pytest
 import torch
 
+import block_reference as ref
 from helpers import ensure_built
+from test_gpu_norm import TYPES, check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +31,28 @@ def test_short_rows_keep_their_bits(lbp):
     one = float(dy[0, 0])
     for got, want in ((dw, 3 * one * ROWS), (db, one * ROWS)):
         assert float((got.double() - want).abs().max()) <= 852 * 2.0 ** -24 * want
+
+
+# either way of the sums beyond 64 rows, and the row ends of each: parts of workgroups of 512 and 1024
+# threads with one and two chunks a thread, columns of rows that do and do not end on a chunk
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("size", [(1300, 2051), (1300, 4093), (1100, 9003), (300, 9001), (200, 40003), (256, 8192), (300, 8193),
+                                  (200, 5000), (100, 6001), (600, 12000), (1500, 16381), (700, 500), (300, 1300), (65, 3), (1025, 7), (3001, 5)], ids=str)
+def test_both_ways(lbp, size, dtype):
+    x, w, b, dy, res = make(*size, dtype, 31)
+    what = f"norm backward {size} {dtype}"
+    print(what, flush=True)
+    _, mean, rstd = lbp.layer_norm(x, w, b, want_stats=True)
+    want = ref.layer_norm_backward(dy, x, mean, rstd, w, res)
+    got = lbp.layer_norm_backward(dy, x, mean, rstd, w, dresidual=res)
+    check(dict(zip(("dx", "dweight", "dbias"), got)), want, what)
+    only = [lbp.layer_norm_backward(dy, x, mean, rstd, w, dresidual=res, want_x=i == 0, want_weight=i == 1, want_bias=i == 2)[i]
+            for i in range(3)]
+    assert all(torch.equal(a, c) for a, c in zip(only, got))
+    plain = lbp.layer_norm_backward(dy, x, mean, rstd, w)
+    check(dict(zip(("dx", "dweight", "dbias"), plain)), ref.layer_norm_backward(dy, x, mean, rstd, w, None), f"{what} alone")
+    for over in (dy.clone(), res.clone()):                # dx over dy, over dresidual
+        first = over if torch.equal(over, dy) else dy
+        second = over if first is dy else res
+        again = lbp.layer_norm_backward(first, x, mean, rstd, w, dresidual=second, dx=over)
+        assert again[0] is over and all(torch.equal(a, c) for a, c in zip(again, got))
