@@ -1,4 +1,5 @@
-"""The gated linear layer's few rows on either side of a split reduction, at any alignment."""
+"""The gated linear layer's few-row kernels where gate and up lie at other distances from 16-byte
+boundaries, with two and four blocks of weight rows, and on either side of a split reduction."""
 import pytest
 import torch
 
@@ -9,8 +10,10 @@ from train_reference import assert_within
 
 pytestmark = pytest.mark.gpu
 
-# long rows of few weights, copied for a split reduction or read in place
-SIZES = [(7, 8191, 2048), (16, 8193, 301), (16, 8193, 1025), (31, 2049, 300), (31, 5001, 151), (6, 4097, 31)]
+# blocks of both halves: four with 17 .. 32 rows, two, four with other distances of both halves;
+# then long rows of few weights, copied for a split reduction or read in place
+SIZES = [(24, 64, 5000), (20, 131, 2501), (9, 1001, 7001), (27, 65, 7001), (32, 40, 1700), (17, 33, 6400), (16, 77, 7001),
+         (5, 303, 3501), (7, 8191, 2048), (16, 8193, 301), (16, 8193, 1025), (31, 2049, 300), (31, 5001, 151), (6, 4097, 31)]
 
 
 @pytest.fixture(scope="module")
@@ -35,7 +38,7 @@ def test_forward(lbp, size, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
-@pytest.mark.parametrize("size", [(7, 8191, 300), (16, 4100, 1000), (31, 2049, 300)], ids=str)
+@pytest.mark.parametrize("size", [(20, 131, 2501), (9, 1001, 7001), (7, 8191, 300), (16, 4100, 1000), (31, 2049, 300)], ids=str)
 def test_strides(lbp, size, dtype):
     """Rows of weights and x from any element on, their surroundings NaN; outputs inside a buffer."""
     rows, n_in, n_out = size
