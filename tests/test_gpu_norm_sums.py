@@ -5,6 +5,7 @@ import torch
 import block_reference as ref
 from helpers import ensure_built
 from test_gpu_norm import TYPES, check, make
+from train_reference import assert_within
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,35 @@ def test_both_ways(lbp, size, dtype):
         second = over if first is dy else res
         again = lbp.layer_norm_backward(first, x, mean, rstd, w, dresidual=second, dx=over)
         assert again[0] is over and all(torch.equal(a, c) for a, c in zip(again, got))
+
+
+def small_integers(seed, *shape, most):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g, device="cuda", dtype=torch.int8)
+
+
+@pytest.mark.parametrize("n, dtype", [(8, torch.float32), (3, torch.float32), (8, torch.float16), (7, torch.bfloat16)], ids=str)
+def test_exact_sums_of_many_rows(lbp, n, dtype):
+    """Small integers with a mean of 0 and rstd of 1 as the statistics: the sums, and any part of them, are
+    integers far below 2^24 (their standard deviation is 1.3e4), so that every row counts exactly once."""
+    print(f"{ROWS} x {n} {dtype}", flush=True)
+    x, dy = small_integers(1, ROWS, n, most=1), small_integers(2, ROWS, n, most=2)
+    want_w, want_b = (x * dy).sum(0, dtype=torch.int64), dy.sum(0, dtype=torch.int64)
+    mean, rstd = torch.zeros(ROWS, device="cuda"), torch.ones(ROWS, device="cuda")
+    assert int(want_w.abs().max()) < 65504 and int(want_b.abs().max()) < 65504
+    _, dw, db = lbp.layer_norm_backward(dy.to(dtype), x.to(dtype), mean, rstd, want_x=False)
+    assert torch.equal(dw, want_w.double().to(dtype)) and torch.equal(db, want_b.double().to(dtype))
+    _, dw, db = lbp.layer_norm_backward(dy.to(dtype), x.to(dtype), mean, rstd)
+    assert torch.equal(dw, want_w.double().to(dtype)) and torch.equal(db, want_b.double().to(dtype))
+
+
+@pytest.mark.parametrize("n", [8, 3])
+def test_statistics_of_many_rows(lbp, n):
+    x = small_integers(3, ROWS, n, most=9).half()
+    _, mean, rstd = lbp.layer_norm(x, want_stats=True)
+    for a in range(0, ROWS, 2 ** 23):
+        part = slice(a, a + 2 ** 23)
+        want = ref.layer_norm(x[part], None, None, float(torch.tensor(1e-5)))
+        assert_within(mean[part], *want["mean"], f"mean {a}")
+        assert_within(rstd[part], *want["rstd"], f"rstd {a}")
