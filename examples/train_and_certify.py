@@ -1,9 +1,10 @@
 """Trains the 784-100-100-10 ReLU network on synthetic classes with the package's training
 operators (fused linear layers and their gradients, cross entropy, gradient clipping), then
 certifies the trained network with CROWN: how many inputs keep their class under every
-perturbation of at most eps.
+perturbation of at most eps.  Dropout of the hidden layers, where asked for, is a matter of training
+alone: what is certified is the same ReLU network.
 
-    python examples/train_and_certify.py [--steps 200] [--eps 0.01]
+    python examples/train_and_certify.py [--steps 200] [--eps 0.01] [--dropout 0]
 """
 from __future__ import annotations
 
@@ -32,26 +33,36 @@ def make_data(n: int, seed: int = 0):
 
 
 class Net:
-    """The network's parameters on the device: [(weight, bias)] per layer."""
+    """The network's parameters on the device: [(weight, bias)] per layer.  dropout: the share of hidden
+    values that a training step drops, by the masks of (seed, the step's number and the layer)."""
 
-    def __init__(self, nodes, device="cuda"):
+    def __init__(self, nodes, device="cuda", dropout: float = 0.0, seed: int = 0):
         self.layers = [(torch.tensor(n.weight, device=device), torch.tensor(n.bias, device=device))
                        for n in nodes if n.op == "linear"]
+        self.dropout, self.seed, self.steps = dropout, seed, 0
 
-    def forward(self, x):
-        """Logits, and the input of every layer (a ReLU's output is what its gradient needs)."""
+    def drop(self, h, layer):
+        """h, or its gradient, with this step's mask."""
+        return lbp.dropout(h, self.dropout, self.seed, self.steps * len(self.layers) + layer, out=h)
+
+    def forward(self, x, train: bool = False):
+        """Logits, and the input of every layer (a ReLU's output is what its gradient needs; where a value
+        is dropped the gradient is too)."""
         inputs = [x]
         for i, (w, b) in enumerate(self.layers):
             last = i + 1 == len(self.layers)
-            inputs.append(lbp.linear(inputs[-1], w, b, act="none" if last else "relu"))
+            h = lbp.linear(inputs[-1], w, b, act="none" if last else "relu")
+            inputs.append(self.drop(h, i) if train and self.dropout and not last else h)
         return inputs[-1], inputs[:-1]
 
     def backward(self, dlogits, inputs):
-        """Gradients in the order of `parameters`."""
+        """Gradients in the order of `parameters`, of forward(train=True)."""
         grads, d = [], dlogits
         for i in reversed(range(len(self.layers))):
             last = i + 1 == len(self.layers)
             saved = None if last else inputs[i + 1]
+            if self.dropout and not last:
+                d = self.drop(d, i)
             d, dw, db, _ = lbp.linear_backward(d, inputs[i], self.layers[i][0], act="none" if last else "relu",
                                                saved=saved, want_x=i > 0)
             grads = [dw, db] + grads
@@ -62,12 +73,13 @@ class Net:
 
     def step(self, x, labels, lr: float, max_norm: float):
         """One step of gradient descent; returns (loss, gradient norm), both on the device."""
-        logits, inputs = self.forward(x)
+        logits, inputs = self.forward(x, train=True)
         loss, _, dlogits = lbp.cross_entropy(logits, labels, dlogits=logits)    # the gradient over the logits
         grads = self.backward(dlogits, inputs)
         norm, grads = lbp.clip_grad_norm(grads, max_norm)
         for p, g in zip(self.parameters(), grads):
             p.add_(g, alpha=-lr)
+        self.steps += 1
         return loss, norm
 
 
@@ -91,9 +103,9 @@ def certify(net: Net, nodes, x: np.ndarray, labels: np.ndarray, eps: float):
 
 
 def run(steps: int = 200, batch: int = 128, eps: float = 0.01, lr: float = 0.1, max_norm: float = 1.0, n_test: int = 64,
-        log=print):
+        log=print, dropout: float = 0.0):
     nodes = wk.mlp(WIDTHS, 1, eps, 1).nodes
-    net = Net(nodes)
+    net = Net(nodes, dropout=dropout)
     x, labels = make_data(batch * 16 + n_test)
     test = slice(batch * 16, None)
     xd, yd = torch.tensor(x, device="cuda"), torch.tensor(labels, device="cuda")
@@ -115,5 +127,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--eps", type=float, default=0.01)
+    ap.add_argument("--dropout", type=float, default=0.0)
     a = ap.parse_args()
-    run(steps=a.steps, eps=a.eps)
+    run(steps=a.steps, eps=a.eps, dropout=a.dropout)
