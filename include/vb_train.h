@@ -1,9 +1,10 @@
 /* vb_train.h -- C ABI of the training and evaluation operators in libvbprop.so.
  *
- * The networks whose bounds vb.h computes are evaluated and trained with these
- * calls: the fused linear layer and its backward pass, the gated linear layer,
- * layer norm and dropout with theirs, the softmax cross entropy with its gradient,
- * and the clipping of gradients to a global norm.
+ * The networks whose bounds vb.h computes are evaluated and trained with the fused
+ * linear layer and its backward pass, dropout (while training), the softmax cross
+ * entropy with its gradient and the clipping of gradients to a global norm.  The gated
+ * linear layer and layer norm, with their backward passes, are for the feed-forward
+ * blocks of networks that vb.h does not bound: it knows no node for either.
  *
  * Conventions (those of vb.h, where they apply):
  *  - Tensor pointers are DEVICE pointers owned by the caller; nothing is kept
@@ -144,8 +145,9 @@ vb_status vb_gated_linear_backward(const vb_gated_linear_bwd* p, void* ws, size_
 /* Layer norm of each row: mean = sum x / n, rstd = 1 / sqrt(sum (x - mean)^2 / n + eps),
  *   y = (x - mean) * rstd * weight + bias.
  * The variance comes from differences, so that rows far off zero keep it.  (Rows that spread over
- * more than 1e19 overflow the float32 squares.)  A row with an infinity or NaN is NaN, as is a
- * row of equal numbers with eps = 0. */
+ * more than 1e19 overflow the float32 squares, and with eps below 1e-38 those that spread over less
+ * than 1e-19 lose them: below 1e-23 the variance is 0.)  A row with an infinity or NaN is NaN, as is
+ * a row of equal numbers with eps = 0. */
 typedef struct {
   int64_t rows;                          /* >= 0 (0: nothing is enqueued)          */
   int32_t n;                             /* in [1, 2^20]                           */

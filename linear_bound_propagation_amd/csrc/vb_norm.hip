@@ -1,12 +1,18 @@
 // Layer norm and its backward pass.
 //
 // A row is read once and stays in registers: TH threads have a row, CH chunks of 16 bytes
-// each (16 lanes per row up to 256 bytes, a wavefront up to 4 KB, a workgroup up to 128 KB).
-// Longer rows are read again for each step (CH = 0).  Rows may start anywhere: 16-byte accesses
-// at element alignment are ordinary ones here, which cost extra only where a line is crossed.
+// each.  Forward: 16 lanes per row up to 256 bytes, a wavefront up to 4 KB, a workgroup up to 128
+// KB.  Backward, where a row is two or three: 16 lanes up to 256 bytes, a wavefront up to 1 KB, a
+// workgroup up to 64 KB for dx.  Longer rows are read again for each step (CH = 0).  With dweight or
+// dbias a row's columns have two float32 sums each in registers as well, up to rows of 32 KB; of
+// longer ones, and of some short matrices (by_columns), dy and x are read twice.  Rows may start
+// anywhere: 16-byte accesses at element alignment are ordinary ones here, which cost extra only where
+// a line is crossed.
 //
 // What bounds it: HBM.  8192 x 8192 in bf16, 268 MB: 50 us, 5.4 TB/s (a large copy: 5.0);
-// backward at 8192 x 4096 with dresidual, dweight and dbias, 268 MB and 17 of parts: 56 us.
+// backward at 8192 x 4096 with dresidual, dweight and dbias, 268 MB and 17 of parts: 56 us.  Of float32
+// rows beyond 8192 numbers the second reading: 2048 x 16384 138 us, 671 MB at 4.9 TB/s of 403 that one
+// pass would move; 2048 x 8192 in one pass 44 us.
 #include <algorithm>
 #include <type_traits>
 

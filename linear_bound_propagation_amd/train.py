@@ -1,7 +1,8 @@
-"""Training and evaluation of the networks whose bounds the package computes:
-the fused linear layer, the gated linear layer, layer norm and dropout, each with its
-backward pass, the softmax cross entropy with its gradient, and the clipping of gradients
-to a global norm (include/vb_train.h).
+"""Training and evaluation of the networks whose bounds the package computes: the fused
+linear layer and its backward pass, dropout, the softmax cross entropy with its gradient
+and the clipping of gradients to a global norm; and, for feed-forward blocks of networks
+that it does not bound, the gated linear layer and layer norm with their backward passes
+(include/vb_train.h).
 
 Thin ctypes binding, like the rest of the package: every step runs in the
 library's HIP kernels on the current stream; results are new tensors on it.

@@ -89,3 +89,14 @@ def test_statistics_of_many_rows(lbp, n):
         want = ref.layer_norm(x[part], None, None, float(torch.tensor(1e-5)))
         assert_within(mean[part], *want["mean"], f"mean {a}")
         assert_within(rstd[part], *want["rstd"], f"rstd {a}")
+
+
+def test_small_spreads(lbp):
+    """The float32 squares of differences of 1e-18 are normal numbers, those of 1e-24 are 0."""
+    x, w, b, _, _ = make(4, 300, torch.float32, 41, mean=0.0)
+    y, mean, rstd = lbp.layer_norm(x * 1e-18, w, b, eps=0.0, want_stats=True)
+    check({"y": y, "mean": mean, "rstd": rstd}, ref.layer_norm(x * 1e-18, w, b, 0.0), "spread 1e-18")
+    _, _, rstd = lbp.layer_norm(x * 1e-24, w, b, eps=0.0, want_stats=True)
+    assert torch.isposinf(rstd).all()
+    y, mean, rstd = lbp.layer_norm(x * 1e-24, w, b, want_stats=True)
+    check({"y": y, "mean": mean, "rstd": rstd}, ref.layer_norm(x * 1e-24, w, b, float(torch.tensor(1e-5))), "spread 1e-24")
